@@ -11,6 +11,12 @@ or, in one call without recomputing the logits,
     loss, lse, _, dH, dW = forward_backward(H, W, idx, tlogit, mask, grad_loss, chunk)
 
 or, through autograd, ``chunked_kl_loss(H, W, idx, tlogit, mask, chunk, fused=False)``.
+
+Around the loss: ``teacher_topk`` makes the sparse teacher from full logits;
+``embedding`` is the lookup in a table of the head's shape, whose gradient
+``embedding_backward`` can add to the head's; ``act_encode`` / ``act_decode``
+hold activations in 8 bits, and ``rms_norm_8bit`` is a norm that saves its
+input so.
 """
 from ._binding import (  # noqa: F401
     CKL_BF16,
@@ -31,4 +37,22 @@ from ._binding import (  # noqa: F401
     timing_read,
     workspace_size,
 )
-from .autograd import ChunkedKLLoss, FusedChunkedKLLoss, chunked_kl_loss  # noqa: F401
+from .autograd import (  # noqa: F401
+    ChunkedKLLoss,
+    ChunkedKLLoss8Bit,
+    Embedding,
+    FusedChunkedKLLoss,
+    RMSNorm8Bit,
+    chunked_kl_loss,
+    embedding,
+    rms_norm_8bit,
+)
+from .ops import (  # noqa: F401
+    act_decode,
+    act_encode,
+    embedding_backward,
+    embedding_forward,
+    norm_backward,
+    norm_forward,
+    teacher_topk,
+)

@@ -34,6 +34,16 @@ EXPORTED = (
     "ckl_scale_cast",
     "ckl_shard_forward",
     "ckl_shard_combine",
+    "ckl_topk_workspace_size",
+    "ckl_teacher_topk",
+    "ckl_embedding_forward",
+    "ckl_embedding_workspace_size",
+    "ckl_embedding_backward",
+    "ckl_act_encode",
+    "ckl_act_decode",
+    "ckl_norm_forward",
+    "ckl_norm_workspace_size",
+    "ckl_norm_backward",
     "ckl_timing_enable",
     "ckl_timing_read",
     "ckl_status_string",
@@ -103,6 +113,27 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.ckl_shard_forward.restype = i32
     lib.ckl_shard_combine.argtypes = [P, ctypes.c_int32, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.ckl_shard_combine.restype = i32
+    i64, f32, szp = ctypes.c_int64, ctypes.c_float, ctypes.POINTER(ctypes.c_size_t)
+    lib.ckl_topk_workspace_size.argtypes = [i64, i64, i64, szp]
+    lib.ckl_topk_workspace_size.restype = i32
+    lib.ckl_teacher_topk.argtypes = [vp, i32, i64, i64, i64, i32, vp, vp, vp, vp, vp, sz, vp]
+    lib.ckl_teacher_topk.restype = i32
+    lib.ckl_embedding_forward.argtypes = [vp, i32, i64, i64, i64, vp, i32, i64, f32, vp, vp]
+    lib.ckl_embedding_forward.restype = i32
+    lib.ckl_embedding_workspace_size.argtypes = [i64, i64, i64, szp]
+    lib.ckl_embedding_workspace_size.restype = i32
+    lib.ckl_embedding_backward.argtypes = [vp, i32, i64, i64, vp, i32, i64, i64, f32, vp, i32, i32, vp, sz, vp]
+    lib.ckl_embedding_backward.restype = i32
+    lib.ckl_act_encode.argtypes = [vp, i32, i64, i64, vp, vp, vp]
+    lib.ckl_act_encode.restype = i32
+    lib.ckl_act_decode.argtypes = [vp, vp, i64, i64, vp, vp, i32, vp, i32, vp]
+    lib.ckl_act_decode.restype = i32
+    lib.ckl_norm_forward.argtypes = [vp, i32, i64, i64, vp, i32, f32, vp, vp, vp, vp, vp]
+    lib.ckl_norm_forward.restype = i32
+    lib.ckl_norm_workspace_size.argtypes = [i64, i64, szp]
+    lib.ckl_norm_workspace_size.restype = i32
+    lib.ckl_norm_backward.argtypes = [vp, i32, i64, i64, vp, vp, vp, vp, i32, vp, vp, vp, sz, vp]
+    lib.ckl_norm_backward.restype = i32
     lib.ckl_timing_enable.argtypes = [ctypes.c_int]
     lib.ckl_timing_enable.restype = i32
     lib.ckl_timing_read.argtypes = [ctypes.c_int, ctypes.POINTER(ctypes.c_double), i64p]
@@ -155,7 +186,7 @@ def fused_plan(prob: Problem):
 
 
 KERNEL_CLASSES = ("teacher_prep", "fwd_lse", "fwd_finalize", "bwd_grad", "gemm_dhdw", "g_pass", "transpose",
-                  "other")
+                  "other", "topk", "embedding", "activation")
 
 
 def timing_enable(on: bool = True) -> None:

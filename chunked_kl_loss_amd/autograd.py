@@ -7,12 +7,20 @@ FusedChunkedKLLoss: one library call in the forward computes the loss and the
 fp32 gradients of the loss itself (no recompute); the backward multiplies them
 by the incoming gradient and rounds them once to the dtypes of H and W, in the
 library (ckl_scale_cast).  When neither H nor W needs a gradient the forward
-computes the loss alone."""
+computes the loss alone.
+
+ChunkedKLLoss8Bit: as ChunkedKLLoss, but the backward's hidden states are
+rebuilt from 8 bits per value; with a norm before the head, the norm's input is
+what is saved, once for the norm's gradient and the head's.
+
+Embedding and RMSNorm8Bit: the embedding by a table of the head's shape, and the
+norm that saves its input in 8 bits."""
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
-from . import _binding
+from . import _binding, ops
 
 
 class ChunkedKLLoss(torch.autograd.Function):
@@ -70,8 +78,84 @@ class FusedChunkedKLLoss(torch.autograd.Function):
         return dH, dW, None, None, None, None, None, None
 
 
+class ChunkedKLLoss8Bit(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, H, W, idx, tlogit, mask, chunk, teacher_form, norm_weight, norm_eps):
+        need = any(ctx.needs_input_grad)
+        rstd = codes = exps = None
+        dtype = H.dtype
+        if norm_weight is not None:
+            H, codes, exps, rstd = ops.norm_forward(H, norm_weight, norm_eps, save=need)
+        elif need:
+            codes, exps = ops.act_encode(H)
+        loss, lse, _ = _binding.forward(H, W, idx, tlogit, mask, chunk=chunk, teacher_form=teacher_form)
+        if need:
+            ctx.save_for_backward(codes, exps, rstd, norm_weight, W, idx, tlogit, mask, lse)
+        ctx.chunk, ctx.teacher_form, ctx.dtype = chunk, teacher_form, dtype
+        return loss[0]
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad):
+        codes, exps, rstd, norm_weight, W, idx, tlogit, mask, lse = ctx.saved_tensors
+        H = ops.act_decode(codes, exps, rstd, norm_weight, dtype=ctx.dtype)
+        g = grad.reshape(1).to(torch.float32)
+        dH, dW = _binding.backward(H, W, idx, tlogit, mask, lse, g, chunk=ctx.chunk, dh_dtype=ctx.dtype,
+                                   dw_dtype=W.dtype, teacher_form=ctx.teacher_form)
+        dnorm = None
+        if norm_weight is not None and (ctx.needs_input_grad[0] or ctx.needs_input_grad[7]):
+            dH, dnorm = ops.norm_backward(dH, codes, exps, rstd, norm_weight)
+        need = ctx.needs_input_grad
+        return (dH if need[0] else None, dW if need[1] else None, None, None, None, None, None,
+                dnorm if need[7] else None, None)
+
+
+class Embedding(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, W, tokens, scale: float = 1.0):
+        ctx.save_for_backward(tokens)
+        ctx.V, ctx.dtype, ctx.scale = W.shape[0], W.dtype, scale
+        return ops.embedding_forward(W, tokens, scale)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad):
+        (tokens,) = ctx.saved_tensors
+        dW = ops.embedding_backward(grad.contiguous(), tokens, ctx.V, ctx.scale, dw_dtype=ctx.dtype)
+        return dW, None, None
+
+
+class RMSNorm8Bit(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, eps: float = 1e-6):
+        y, codes, exps, rstd = ops.norm_forward(x, weight, eps, save=any(ctx.needs_input_grad))
+        if codes is not None:
+            ctx.save_for_backward(codes, exps, rstd, weight)
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad):
+        codes, exps, rstd, weight = ctx.saved_tensors
+        dx, dweight = ops.norm_backward(grad.contiguous(), codes, exps, rstd, weight)
+        return (dx if ctx.needs_input_grad[0] else None), (dweight if ctx.needs_input_grad[1] else None), None
+
+
+def embedding(W, tokens, scale: float = 1.0):
+    """scale * W[tokens], differentiable with respect to the table W [V, d] (the output head's, when tied).
+    tokens: int32 / int64 of any shape; a token outside [0, V) gives a zero row and no gradient."""
+    return Embedding.apply(W.contiguous(), tokens.contiguous(), scale)
+
+
+def rms_norm_8bit(x, weight, eps: float = 1e-6):
+    """RMS norm of the last dimension, differentiable with respect to x [..., d] and weight [d].  The output is
+    that of the exact x; the backward pass reads x from 8 bits (ops.act_encode), so that the norm keeps d bytes a
+    row instead of x."""
+    return RMSNorm8Bit.apply(x.contiguous(), weight.contiguous(), eps)
+
+
 def chunked_kl_loss(H, W, idx, tlogit, mask=None, chunk: int = 2048, fused: bool = False, teacher_form: int = 0,
-                    dw_group_rows: int = 0):
+                    dw_group_rows: int = 0, save_8bit: bool = False, norm_weight=None, norm_eps: float = 1e-6):
     """Mean forward KL(teacher || student) over unmasked rows, differentiable
     with respect to H and W.  fused=True computes the gradients together with
     the loss (one pass over the logits; it keeps the logit gradients of up to
@@ -79,6 +163,14 @@ def chunked_kl_loss(H, W, idx, tlogit, mask=None, chunk: int = 2048, fused: bool
     a smaller value holds less memory and updates dW more often).
     teacher_form 1: tlogit holds truncated teacher log-probabilities, used as
     given (teacher mass below one).
+
+    save_8bit=True: the loss is that of the exact H, but the backward pass
+    rebuilds H from 8 bits per value (ops.act_encode), so that d bytes a row are
+    kept from forward to backward instead of H.  norm_weight [d] (with
+    save_8bit): H is the input of an RMS norm before the head, whose input is
+    saved instead, once for both; differentiable with respect to norm_weight
+    too.  fused=True keeps gradients instead of H, so there save_8bit goes with
+    norm_weight only.
 
     Leading batch dimensions are flattened into rows: H [..., d], idx and
     tlogit [..., K], mask [...].  The library takes contiguous tensors, int32
@@ -93,6 +185,15 @@ def chunked_kl_loss(H, W, idx, tlogit, mask=None, chunk: int = 2048, fused: bool
     tlogit = tlogit.reshape(-1, K).to(torch.float32).contiguous()
     if mask is not None:
         mask = mask.reshape(-1).contiguous()
+    if norm_weight is not None and not save_8bit:
+        raise ValueError("norm_weight needs save_8bit=True: the norm saves its input in 8 bits")
+    if fused and save_8bit:
+        if norm_weight is None:
+            raise ValueError("fused=True keeps no hidden states: save_8bit there needs norm_weight")
+        H = rms_norm_8bit(H, norm_weight, norm_eps)
+    if save_8bit and not fused:
+        nw = None if norm_weight is None else norm_weight.contiguous()
+        return ChunkedKLLoss8Bit.apply(H, W, idx, tlogit, mask, chunk, teacher_form, nw, norm_eps)
     if fused:
         return FusedChunkedKLLoss.apply(H, W, idx, tlogit, mask, chunk, teacher_form, dw_group_rows)
     return ChunkedKLLoss.apply(H, W, idx, tlogit, mask, chunk, teacher_form)

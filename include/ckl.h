@@ -283,6 +283,99 @@ ckl_status ckl_shard_combine(const ckl_problem* p, int32_t n_shards,
                              float* loss, float* lse, float* row_loss,
                              void* ws, size_t ws_bytes, void* stream);
 
+/* ---- Operators around the loss -------------------------------------------
+ * The teacher's cache that the loss reads, the embedding table that shares the
+ * head's weights, and hidden states held in 8 bits.  As above: row-major packed
+ * device arrays, 16-byte aligned where not said otherwise; asynchronous on
+ * `stream`; bitwise reproducible (sums run in an order fixed by the sizes);
+ * outputs disjoint from every other buffer.  T may be 0 (T-sized arrays may
+ * then be NULL).  d is a multiple of 8 up to 65536; T and V at most 4,000,000. */
+
+/* Top-K teacher cache from full logits: for every row the K largest logits in
+ * descending order and log sum exp of the whole row, in one pass over the row.
+ *   logits: [T, V] dtype.  mask: [T] uint8 (nonzero = keep) or NULL.
+ *   idx:    [T, K] int32.  Equal logits (-0 equals +0) are ordered by index,
+ *           lower first, so the choice at the K-th place is defined; NaN orders
+ *           above every number.
+ *   values: [T, K] float32.  teacher_form CKL_TEACHER_LOGITS: the logits;
+ *           CKL_TEACHER_LOGPROBS: logit - lse (a logit of -inf gives -inf).
+ *   lse:    [T] float32 (4-byte aligned); NaN for a row that holds a NaN, -inf
+ *           for a row of nothing but -inf.
+ * Rows with mask 0 are not read; they get idx = 0 .. K-1, values 0 and lse 0,
+ * which the loss never uses when given the same mask.  1 <= K <= min(V, 4096),
+ * T*K < 2^31.  ws: ckl_topk_workspace_size(T, V, K) bytes (0 for many rows;
+ * ws may then be NULL).  idx, values are what ckl_forward takes as idx, tlogit
+ * with the same teacher_form. */
+ckl_status ckl_topk_workspace_size(int64_t T, int64_t V, int64_t K, size_t* bytes);
+ckl_status ckl_teacher_topk(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t K,
+                            int32_t teacher_form, const uint8_t* mask, int32_t* idx, float* values,
+                            float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* Embedding by a table of the head's shape: out[t] = scale * W[tokens[t] - v_offset]
+ * rounded once to dtype.  A token outside [v_offset, v_offset + V) selects no
+ * row: its output row is zero.  So negative ids can pad a batch, and with W one
+ * vocabulary shard the outputs of all shards add up to the whole table's.
+ *   W: [V, d] dtype.  tokens: [T] int32 or int64 (token_bytes 4 or 8), aligned
+ *   to their size.  out: [T, d] dtype. */
+ckl_status ckl_embedding_forward(const void* W, int32_t dtype, int64_t V, int64_t d, int64_t v_offset,
+                                 const void* tokens, int32_t token_bytes, int64_t T, float scale, void* out,
+                                 void* stream);
+
+/* Its gradient: dW[v] = scale * sum of dY[t] over the positions t of token
+ * v + v_offset, the positions sorted by token and summed in fp32 in a fixed
+ * order.  accumulate = 0: dW is overwritten (rows without a token become zero);
+ * 1: the sums are added to dW and rows without a token are neither read nor
+ * written, which adds the embedding's share to the gradient ckl_backward or
+ * ckl_forward_backward left in dW when the table is the output head.  Tokens
+ * outside the table contribute nothing.
+ *   dY: [T, d] dtype.  dW: [V, d] dw_dtype; each element is rounded once.
+ *   ws: ckl_embedding_workspace_size(T, d, V) bytes. */
+ckl_status ckl_embedding_workspace_size(int64_t T, int64_t d, int64_t V, size_t* bytes);
+ckl_status ckl_embedding_backward(const void* dY, int32_t dtype, int64_t T, int64_t d, const void* tokens,
+                                  int32_t token_bytes, int64_t V, int64_t v_offset, float scale, void* dW,
+                                  int32_t dw_dtype, int32_t accumulate, void* ws, size_t ws_bytes, void* stream);
+
+/* Activations in 8 bits.  Every block of CKL_ACT_BLOCK columns of a row (the
+ * last one may be short) shares the power of two 2^(E - 127): the smallest that
+ * brings the block's largest magnitude below 127.5, from 2^-126 to 2^121.  A
+ * code is the value divided by it, rounded to the nearest integer, ties to
+ * even, limited to [-127, 127]; it stands for code * 2^(E - 127), which is exact
+ * in bf16 and fp32 and within half a step, max|x| / 127.5, of x (within a whole
+ * step where |x| > 127.5 * 2^121, within 2^-127 in blocks below 2^-119).
+ * E = 255 marks a block that holds an infinity or a NaN: all of it stands for
+ * NaN.
+ *   x: [T, d] dtype.  codes: [T, d] int8.  exps: [T, ceil(d / CKL_ACT_BLOCK)]
+ *   uint8, any alignment. */
+#define CKL_ACT_BLOCK 32
+ckl_status ckl_act_encode(const void* x, int32_t dtype, int64_t T, int64_t d, int8_t* codes, uint8_t* exps,
+                          void* stream);
+
+/* The values the codes stand for, in out_dtype; or, with rstd [T] float32 and
+ * weight [d] weight_dtype (both or neither), value * rstd[t] * weight[i]
+ * rounded once: the output of ckl_norm_forward rebuilt from its codes. */
+ckl_status ckl_act_decode(const int8_t* codes, const uint8_t* exps, int64_t T, int64_t d, const float* rstd,
+                          const void* weight, int32_t weight_dtype, void* out, int32_t out_dtype, void* stream);
+
+/* RMS norm that saves its input in 8 bits: rstd[t] = 1 / sqrt(mean_i x[t,i]^2 + eps),
+ * y = x * rstd * weight (in fp32, rounded once), codes and exps of x as
+ * ckl_act_encode writes them.
+ *   x, y: [T, d] dtype.  weight: [d] weight_dtype.  rstd: [T] float32.
+ *   codes, exps and rstd may all be NULL where no backward pass follows. */
+ckl_status ckl_norm_forward(const void* x, int32_t dtype, int64_t T, int64_t d, const void* weight,
+                            int32_t weight_dtype, float eps, void* y, int8_t* codes, uint8_t* exps, float* rstd,
+                            void* stream);
+
+/* Its backward pass from the 8-bit form.  With n = (what the codes stand for) * rstd:
+ *   dx = rstd * (dy * weight - n * mean_i(dy * weight * n)),   dweight = sum_t dy * n,
+ * in fp32, each result rounded once.  (rstd is that of the exact x, so the only
+ * approximation is that of x by its codes.)
+ *   dy, dx: [T, d] dtype.  dweight: [d] weight_dtype (zero for T = 0).
+ *   ws: ckl_norm_workspace_size(T, d) bytes. */
+ckl_status ckl_norm_workspace_size(int64_t T, int64_t d, size_t* bytes);
+ckl_status ckl_norm_backward(const void* dy, int32_t dtype, int64_t T, int64_t d, const int8_t* codes,
+                             const uint8_t* exps, const float* rstd, const void* weight, int32_t weight_dtype,
+                             void* dx, void* dweight, void* ws, size_t ws_bytes, void* stream);
+
 /* Kernel classes for the timing records below. */
 typedef enum {
   CKL_KERNEL_TEACHER_PREP = 0, /* teacher softmax + sort                      */
@@ -293,7 +386,10 @@ typedef enum {
   CKL_KERNEL_G_PASS = 5,       /* fused call: u -> G (fp32 also G^T)        */
   CKL_KERNEL_TRANSPOSE = 6,    /* H^T and W^T staging                         */
   CKL_KERNEL_OTHER = 7,        /* counts, scales, fills, casts               */
-  CKL_KERNEL_CLASSES = 8
+  CKL_KERNEL_TOPK = 8,         /* ckl_teacher_topk                            */
+  CKL_KERNEL_EMBEDDING = 9,    /* ckl_embedding_forward / _backward           */
+  CKL_KERNEL_ACTIVATION = 10,  /* ckl_act_encode / _decode, ckl_norm_*        */
+  CKL_KERNEL_CLASSES = 11
 } ckl_kernel_class;
 
 /* Optional per-kernel timing, a measurement aid.  While enabled (on = 1),
