@@ -40,6 +40,10 @@ __device__ __forceinline__ void store8(float* p, const float* f) {
   reinterpret_cast<f32x4*>(p)[0] = f32x4{f[0], f[1], f[2], f[3]};
   reinterpret_cast<f32x4*>(p)[1] = f32x4{f[4], f[5], f[6], f[7]};
 }
+__device__ __forceinline__ void store4(bf16_t* p, f32x4 v) {
+  *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+}
+__device__ __forceinline__ void store4(float* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
 // A weight of either type, eight columns.
 __device__ __forceinline__ void load8_any(const void* p, int is_bf16, int64_t at, float* f) {
   if (is_bf16)
@@ -51,6 +55,17 @@ __device__ __forceinline__ void load8_any(const void* p, int is_bf16, int64_t at
 __device__ __forceinline__ float wave_sum_f(float x) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o);
+  return x;
+}
+
+// Inclusive sums over the wave, lane by lane.
+__device__ __forceinline__ int wave_scan(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);  // from 1, 2, 4, 8 lanes below in the row of 16
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);  // row ends into rows 1 and 3
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);  // lane 31 into rows 2 and 3
   return x;
 }
 
@@ -89,38 +104,121 @@ Units units(int64_t n) {
 // One pass over the row.  An element is a 64-bit word: a key that orders the
 // values as unsigned integers (NaN largest, -0 = +0) above the inverted index,
 // so that larger words come first and no two are equal.  A workgroup walks its
-// segment in tiles; elements above the threshold go into a buffer in shared
-// memory, and when a further tile might not fit, the buffer is cut to its K
-// best and the threshold becomes the K-th key.  Later elements with that very
-// key have higher indices than all kept, so they lose and a strict comparison
-// is enough.  The log-sum-exp runs along (maximum and sum per thread).
+// segment of the row in tiles of 8192 columns held in registers.  From the
+// first it takes a key with at least K elements at or above it, found by
+// counting the keys of a range in 256 bins; from then on only elements above
+// that key go into a buffer in shared memory: those with the very key come later
+// than K others and lose.  A filling buffer is cut in the same way, which raises
+// the key.  Where too many elements share one key for a cut by keys, a radix
+// selection over the words decides by index.  What remains is sorted.  Per
+// vector of eight the common path is eight exponentials, one running maximum
+// and one comparison.
 constexpr int kTopkThreads = 256;
-constexpr int kTopkTile = kTopkThreads * 8;
+constexpr int kTopkVecs = 4;                                 // vectors of eight a thread holds
+constexpr int kTopkStep = kTopkThreads * 8;                  // columns of one vector each
+constexpr int kTopkTile = kTopkVecs * kTopkStep;
+constexpr uint32_t kNanKey = 0xfffffffeu;                    // every key lies below 2^32 - 1
 
 __device__ __forceinline__ uint32_t order_key(float x) {
-  if (x != x) return 0xffffffffu;
+  if (x != x) return kNanKey;
   const uint32_t b = __float_as_uint(x + 0.f);  // -0 + 0 = +0
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
+// (keys that no number has, above that of infinity and below that of -infinity,
+// give NaNs)
 __device__ __forceinline__ float key_value(uint32_t k) {
-  if (k == 0xffffffffu) return __uint_as_float(0x7fc00000u);
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
 
 struct TopkShared {
   uint32_t hist[256];
   uint32_t wave_n[4];
+  uint32_t range[2][4];
   float wave_m[4], wave_s[4];
-  uint32_t count, sel, need, bin, min_key;
+  uint32_t count, sel, need, bin;
 };
 
-// Cuts the n > K words of buf to the K largest, in any order, and returns the
-// smallest of their keys.  All threads of the workgroup call it; it begins and
-// ends with a barrier.
-__device__ uint32_t topk_cut(uint64_t* buf, int n, int K, TopkShared& sh) {
+// Places for a lane's `mine` words behind those in the buffer: one addition to
+// the counter a wave.
+__device__ __forceinline__ int topk_place(int mine, TopkShared& sh) {
+  const int inc = wave_scan(mine);
+  int at = 0;
+  if ((threadIdx.x & 63) == 63) at = (int)atomicAdd(&sh.count, (uint32_t)inc);
+  return __builtin_amdgcn_readlane(at, 63) + inc - mine;
+}
+
+// The extremes of a value over the workgroup.
+__device__ __forceinline__ void topk_range(uint32_t& lo, uint32_t& hi, TopkShared& sh) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    const uint32_t a = __shfl_xor(lo, o), b = __shfl_xor(hi, o);
+    lo = a < lo ? a : lo;
+    hi = b > hi ? b : hi;
+  }
+  if ((threadIdx.x & 63) == 0) {
+    sh.range[0][threadIdx.x >> 6] = lo;
+    sh.range[1][threadIdx.x >> 6] = hi;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const uint32_t a = sh.range[0][w], b = sh.range[1][w];
+    lo = a < lo ? a : lo;
+    hi = b > hi ? b : hi;
+  }
+}
+
+// A key t in [lo, hi) that at least K elements reach: count(t) >= K.  The range
+// is counted in 256 bins and narrowed to one of them until count(t) <= limit or
+// it holds one key only; *n = count(t).  No element reaches hi; at_lo =
+// count(lo), or more.  each(f) calls f for a thread's keys.  All threads call
+// it, after a barrier behind the last use of sh.
+template <typename E>
+__device__ __forceinline__ uint32_t topk_select(E each, uint32_t lo, uint32_t hi, int at_lo, int K, int limit,
+                                                TopkShared& sh, int* n) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  uint32_t above = 0;  // elements that reach hi
+  while (at_lo > limit && hi - lo > 1) {
+    const int bits = 32 - __clz((int)(hi - lo - 1)), shift = bits > 8 ? bits - 8 : 0;
+    sh.hist[tid] = 0;
+    __syncthreads();
+    each([&](uint32_t k) {
+      if (k >= lo && k < hi) atomicAdd(&sh.hist[(k - lo) >> shift], 1u);
+    });
+    __syncthreads();
+    // suffix sums: thread b holds the elements that reach bin b
+    const uint32_t own = sh.hist[tid];
+    uint32_t suf = (uint32_t)wave_scan((int)own);
+    const uint32_t in_wave = (uint32_t)__builtin_amdgcn_readlane((int)suf, 63);
+    suf = in_wave - suf + own;
+    if (lane == 0) sh.wave_n[wave] = in_wave;
+    __syncthreads();
+    suf += above;
+    for (int w = wave + 1; w < 4; ++w) suf += sh.wave_n[w];
+    if (suf >= (uint32_t)K && suf - own < (uint32_t)K) {
+      sh.sel = (uint32_t)tid;
+      sh.need = suf;
+      sh.bin = own;
+    }
+    __syncthreads();
+    lo += sh.sel << shift;
+    const uint32_t end = lo + (1u << shift);
+    hi = end < hi ? end : hi;
+    at_lo = (int)sh.need;
+    above = sh.need - sh.bin;
+  }
+  *n = at_lo;
+  return lo;
+}
+
+// Cuts the n > K words of buf to exactly the K largest, by radix selection:
+// where keys are equal the index decides.  In any order; begins and ends with a
+// barrier.
+__device__ __forceinline__ void topk_cut_exact(uint64_t* buf, int n, int K, TopkShared& sh) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   uint64_t prefix = 0, pmask = 0;
   uint32_t need = (uint32_t)K;
+  __syncthreads();
   for (int shift = 56; shift >= 0; shift -= 8) {
     sh.hist[tid] = 0;
     __syncthreads();
@@ -151,48 +249,174 @@ __device__ uint32_t topk_cut(uint64_t* buf, int n, int K, TopkShared& sh) {
     need = sh.need;
     if (sh.bin == need) break;  // the whole bin is kept
   }
-  if (tid == 0) {
-    sh.count = 0;
-    sh.min_key = 0xffffffffu;
-  }
+  if (tid == 0) sh.count = 0;
   // in place: the words kept so far never reach past the words read so far
   for (int i0 = 0; i0 < n; i0 += kTopkThreads) {
     const int i = i0 + tid;
     const uint64_t c = i < n ? buf[i] : 0;
     __syncthreads();
-    if (i < n && (c & pmask) >= prefix) {
-      buf[atomicAdd(&sh.count, 1u)] = c;
-      atomicMin(&sh.min_key, (uint32_t)(c >> 32));
-    }
+    if (i < n && (c & pmask) >= prefix) buf[atomicAdd(&sh.count, 1u)] = c;
   }
   __syncthreads();
-  return sh.min_key;
 }
 
-// Descending bitonic sort of the first n <= cap words (padded with zeros up to
-// a power of two, which must fit the buffer).
-__device__ void topk_sort(uint64_t* buf, int n) {
-  int p = 1;
-  while (p < n) p <<= 1;
-  for (int i = n + (int)threadIdx.x; i < p; i += kTopkThreads) buf[i] = 0;
+// Cuts the n > limit >= K words of buf (n < 64 kTopkThreads), none with a key
+// below `floor_key`, to at most `limit` of the largest, at least K, in any
+// order.  Returns their number and sets *key to a key that at least K of them,
+// and none less, reach.  Begins and ends with a barrier.
+__device__ __forceinline__ int topk_cut(uint64_t* buf, int n, int K, int limit, uint32_t floor_key, TopkShared& sh,
+                                        uint32_t* key) {
+  const int tid = threadIdx.x;
+  const uint32_t* keys = reinterpret_cast<const uint32_t*>(buf) + 1;
   __syncthreads();
-  for (int size = 2; size <= p; size <<= 1) {
-    for (int stride = size >> 1; stride > 0; stride >>= 1) {
-      for (int i = threadIdx.x; i < p / 2; i += kTopkThreads) {
-        const int a = 2 * i - (i & (stride - 1)), b = a + stride;
-        const uint64_t x = buf[a], y = buf[b];
-        const bool down = (a & size) == 0;
-        if ((x < y) == down) {
-          buf[a] = y;
-          buf[b] = x;
+  uint32_t least = 0, most = 0;
+#pragma unroll 4
+  for (int i = tid; i < n; i += kTopkThreads) most = keys[2 * i] > most ? keys[2 * i] : most;
+  topk_range(least, most, sh);
+  int kept;
+  const uint32_t t = topk_select(
+      [&](auto f) {
+#pragma unroll 4
+        for (int i = tid; i < n; i += kTopkThreads) f(keys[2 * i]);
+      },
+      floor_key, most + 1, n, K, limit, sh, &kept);
+  *key = t;
+  if (kept > limit) {
+    topk_cut_exact(buf, n, K, sh);
+    return K;
+  }
+  __syncthreads();
+  if (tid == 0) sh.count = 0;
+  // in place: the words kept so far never reach past the words read so far
+  for (int i0 = 0; i0 < n; i0 += kTopkThreads) {
+    const int i = i0 + tid;
+    const uint64_t c = i < n ? buf[i] : 0;
+    __syncthreads();
+    const bool keep = i < n && (uint32_t)(c >> 32) >= t;
+    const int at = topk_place(keep ? 1 : 0, sh);
+    if (keep) buf[at] = c;
+  }
+  __syncthreads();
+  return kept;
+}
+
+// Descending order of the n words in buf, by the place a word has among them:
+// the words that are larger, counted.  For n up to kTopkThreads.
+__device__ __forceinline__ void topk_sort_by_rank(uint64_t* buf, int n) {
+  const int tid = threadIdx.x;
+  const uint64_t mine = tid < n ? buf[tid] : 0;
+  if (tid >= n && tid < ((n + 7) & ~7)) buf[tid] = 0;  // (no word is zero)
+  __syncthreads();
+  int rank = 0;
+  for (int i = 0; i < n; i += 8) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) rank += buf[i + k] > mine ? 1 : 0;
+  }
+  __syncthreads();
+  if (tid < n) buf[rank] = mine;
+  __syncthreads();
+}
+
+// The value of lane ^ LANES.
+template <int LANES>
+__device__ __forceinline__ uint32_t lane_xor(uint32_t x) {
+  if constexpr (LANES == 1) return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0xb1, 0xf, 0xf, true);  // quad 1 0 3 2
+  if constexpr (LANES == 2) return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x4e, 0xf, 0xf, true);  // quad 2 3 0 1
+  if constexpr (LANES == 4) {  // from 4 above in banks 0 and 2 of a row, from 4 below in the others
+    const int up = __builtin_amdgcn_update_dpp((int)x, (int)x, 0x104, 0xf, 0x5, false);
+    return (uint32_t)__builtin_amdgcn_update_dpp(up, (int)x, 0x114, 0xf, 0xa, false);
+  }
+  if constexpr (LANES == 8) return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x128, 0xf, 0xf, true);  // row turned by 8
+  return (uint32_t)__shfl_xor((int)x, LANES);
+}
+
+// Descending bitonic sort of n words, W to a thread: partners are in the same
+// thread, in the same wave, or (the largest distances) in another wave, where
+// they meet in buf.  n <= W kTopkThreads, which fit buf.
+template <int W>
+__device__ __forceinline__ void topk_sort_bitonic(uint64_t* buf, int n) {
+  const int tid = threadIdx.x;
+  uint64_t x[W];
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < W; ++w) x[w] = tid * W + w < n ? buf[tid * W + w] : 0;
+  __syncthreads();
+#pragma unroll 1
+  for (int size = 2; size <= W * kTopkThreads; size <<= 1) {
+#pragma unroll 1
+    for (int stride = size >> 1; stride >= W; stride >>= 1) {
+      const int lanes = stride / W;
+      // the larger word goes first where the block of `size` words is an even
+      // one, and to the lower partner there
+      const bool keep_max = ((tid & lanes) == 0) == (((tid * W) & size) == 0);
+      auto exchange = [&](auto partner) {
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          const uint64_t y = partner(w);
+          if ((x[w] < y) == keep_max) x[w] = y;
+        }
+      };
+      auto by_lane = [&](auto l) {
+        exchange([&](int w) {
+          return (uint64_t)lane_xor<decltype(l)::value>((uint32_t)(x[w] >> 32)) << 32 |
+                 lane_xor<decltype(l)::value>((uint32_t)x[w]);
+        });
+      };
+      switch (lanes) {
+        case 1: by_lane(std::integral_constant<int, 1>{}); break;
+        case 2: by_lane(std::integral_constant<int, 2>{}); break;
+        case 4: by_lane(std::integral_constant<int, 4>{}); break;
+        case 8: by_lane(std::integral_constant<int, 8>{}); break;
+        case 16: by_lane(std::integral_constant<int, 16>{}); break;
+        case 32: by_lane(std::integral_constant<int, 32>{}); break;
+        default:
+#pragma unroll
+          for (int w = 0; w < W; ++w) buf[w * kTopkThreads + tid] = x[w];
+          __syncthreads();
+          exchange([&](int w) { return buf[w * kTopkThreads + (tid ^ lanes)]; });
+          __syncthreads();
+      }
+    }
+    // within the thread
+#pragma unroll
+    for (int b = W / 2; b > 0; b >>= 1) {
+      if (b < size) {
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          if ((w & b) == 0) {
+            const uint64_t u = x[w], v = x[w | b];
+            const bool swap = (u < v) == (((tid * W + w) & size) == 0);
+            x[w] = swap ? v : u;
+            x[w | b] = swap ? u : v;
+          }
         }
       }
-      __syncthreads();
     }
   }
+#pragma unroll
+  for (int w = 0; w < W; ++w) buf[tid * W + w] = x[w];
+  __syncthreads();
 }
 
-// Merge of two (maximum, sum of exp(x - maximum)) states.
+// (a buffer of 4096 words serves K up to 1024, whose sort takes at most 2048)
+template <int CAP>
+__device__ __forceinline__ void topk_sort(uint64_t* buf, int n) {
+  if (CAP <= 4096 && n <= kTopkThreads)
+    topk_sort_by_rank(buf, n);
+  else if (CAP <= 4096 || n <= 2048)
+    topk_sort_bitonic<8>(buf, n);
+  else
+    topk_sort_bitonic<CAP / kTopkThreads>(buf, n);
+}
+
+// Words that the final sort takes without a cut before it: what the sort that K
+// and an eighth of it need holds.
+__device__ __forceinline__ int topk_sort_limit(int K) {
+  const int k = K + K / 8;
+  return k <= 256 ? 256 : k <= 2048 ? 2048 : 8192;
+}
+
+// Merge of two (reference m, sum of exp(x - m)) states.
 __device__ __forceinline__ void exp_merge(float& m, float& s, float m2, float s2) {
   const float mn = fmaxf(m, m2);
   if (mn == -INFINITY) {
@@ -218,18 +442,15 @@ __device__ __forceinline__ void topk_reduce_state(float& m, float& s, TopkShared
   m = sh.wave_m[0];
   s = sh.wave_s[0];
   for (int w = 1; w < 4; ++w) exp_merge(m, s, sh.wave_m[w], sh.wave_s[w]);
-  __syncthreads();
 }
 
 // The sorted words of a row and its state, as the row's results.
-__device__ void topk_write(const uint64_t* buf, int K, float m, float s, int logprob, int* idx, float* val,
+__device__ __forceinline__ void topk_write(const uint64_t* buf, int K, float m, float s, int logprob, int* idx, float* val,
                            float* lse) {
   const float top = key_value((uint32_t)(buf[0] >> 32));
   float l;
-  if (top != top)
-    l = top;  // a NaN anywhere in the row comes first
-  else if (top == INFINITY || top == -INFINITY)
-    l = top;
+  if (top != top || top == INFINITY || top == -INFINITY)
+    l = top;  // a NaN anywhere in the row comes first, then an infinity
   else
     l = m + logf(s);
   for (int k = threadIdx.x; k < K; k += kTopkThreads) {
@@ -250,9 +471,59 @@ __device__ __forceinline__ void topk_masked_row(int K, int* idx, float* val, flo
   if (threadIdx.x == 0) *lse = 0.f;
 }
 
+// Eight columns as they are in memory.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<bf16_t> {
+  u32x4 a;
+  __device__ __forceinline__ void load(const bf16_t* p) { a = *reinterpret_cast<const u32x4*>(p); }
+  __device__ __forceinline__ void take(bool c, const Raw8& o) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = c ? (uint32_t)o.a[i] : (uint32_t)a[i];
+  }
+  __device__ __forceinline__ void from(const float* f) {
+    a = u32x4{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])};
+  }
+  __device__ __forceinline__ float get(int i) const {
+    return (i & 1) ? __uint_as_float(a[i >> 1] & 0xffff0000u) : __uint_as_float(a[i >> 1] << 16);
+  }
+  // (i not known at compile time)
+  __device__ __forceinline__ float pick(int i) const {
+    const uint32_t lo = (i & 2) ? a[1] : a[0], hi = (i & 2) ? a[3] : a[2];
+    const uint32_t w = (i & 4) ? hi : lo;
+    return __uint_as_float((i & 1) ? w & 0xffff0000u : w << 16);
+  }
+};
+template <>
+struct Raw8<float> {
+  f32x4 a[2];
+  __device__ __forceinline__ void load(const float* p) {
+    a[0] = reinterpret_cast<const f32x4*>(p)[0];
+    a[1] = reinterpret_cast<const f32x4*>(p)[1];
+  }
+  __device__ __forceinline__ void take(bool c, const Raw8& o) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i >> 2][i & 3] = c ? (float)o.a[i >> 2][i & 3] : (float)a[i >> 2][i & 3];
+  }
+  __device__ __forceinline__ void from(const float* f) {
+    a[0] = f32x4{f[0], f[1], f[2], f[3]};
+    a[1] = f32x4{f[4], f[5], f[6], f[7]};
+  }
+  __device__ __forceinline__ float get(int i) const { return a[i >> 2][i & 3]; }
+  __device__ __forceinline__ float pick(int i) const {
+    const f32x4 w = (i & 4) ? a[1] : a[0];
+    const float lo = (i & 1) ? w[1] : w[0], hi = (i & 1) ? w[3] : w[2];
+    return (i & 2) ? hi : lo;
+  }
+};
+
+// What a segment of a row leaves for the merge: up to `slots` words.
+__host__ __device__ inline int topk_slots(int K) { return K + K / 8 + 32; }
+
 template <typename T, int CAP>
-__global__ __launch_bounds__(kTopkThreads) void topk_rows_kernel(const T* __restrict__ logits, int64_t V, int K,
-                                                                 int segments, int64_t seg_cols, int logprob,
+__global__ __launch_bounds__(kTopkThreads) void topk_rows_kernel(const T* __restrict__ logits, int64_t rows, int V, int K,
+                                                                 int segments, int seg_cols, int logprob,
                                                                  const uint8_t* __restrict__ mask,
                                                                  int* __restrict__ idx, float* __restrict__ val,
                                                                  float* __restrict__ lse, uint64_t* __restrict__ cand,
@@ -268,72 +539,207 @@ __global__ __launch_bounds__(kTopkThreads) void topk_rows_kernel(const T* __rest
   }
   // Columns shifted so that shifted column 0 lies on a 16-byte boundary (rows
   // of an odd V begin anywhere).
-  const T* p = logits + row * V;
+  const T* p = logits + row * (int64_t)V;
   const int shift = (int)(((uintptr_t)p & 15u) / sizeof(T));
   const T* base = p - shift;
-  const int64_t lo = (int64_t)seg * seg_cols;
-  const int64_t hi = (lo + seg_cols < V + shift) ? lo + seg_cols : V + shift;
+  const int lo = seg * seg_cols, first = lo > shift ? lo : shift;
+  const int hi = (lo + seg_cols < V + shift) ? lo + seg_cols : V + shift;
+  const int mid_limit = K + K / 4 + 64;  // what a cut on the way may leave: at most CAP - kTopkStep
+  const int cut_at = 2 * mid_limit < CAP - 1024 ? 2 * mid_limit : CAP - 1024;
+  uint32_t after = 0;
 
-  if (tid == 0) sh.count = 0;
-  __syncthreads();
-  uint32_t thr = 0;
-  float m = -INFINITY, s = 0.f;
-  for (int64_t t0 = lo; t0 < hi; t0 += kTopkTile) {
-    const int64_t j = t0 + tid * 8;
-    float x[8];
-    int in = 0;
-    if (j >= shift && j + 8 <= hi) {
-      load8(base + j, x);
-      in = 255;
+  const int end = row + 1 < rows ? V + shift + 8 : V + shift;  // columns that can be read
+  // Vector u of a tile, with -infinity outside [first, hi).
+  auto fetch = [&](int t0, int u) {
+    const int j = t0 + u * kTopkStep + tid * 8;
+    Raw8<T> r;
+    if (j + 8 <= hi && j >= first) {
+      r.load(base + j);
+    } else {
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = -INFINITY;
+      if (j < hi) {
+        if (j + 8 <= end) {
+          load8(base + j, f);  // (a row's neighbours in memory; the first row begins on a boundary)
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] = j + i < end ? (float)base[j + i] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = j + i >= first && j + i < hi ? f[i] : -INFINITY;
+      }
+      r.from(f);
+    }
+    return r;
+  };
+  uint32_t need = 0;  // keys from here on are wanted
+  float need_value = key_value(0);
+  // which of a vector's elements are wanted; need_value is a NaN where need is
+  // no number's key, and all vectors are looked at
+  auto wanted = [&](const Raw8<T>& r, int j) {
+    int hits = 0;
+    if (need_value != need_value) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) hits |= order_key(r.get(i)) >= need ? 1 << i : 0;
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const bool ok = j + i >= shift && j + i < hi;
-        x[i] = ok ? (float)base[j + i] : -INFINITY;
-        in |= ok ? 1 << i : 0;
+      for (int i = 0; i < 8; ++i) hits |= !(r.get(i) < need_value) ? 1 << i : 0;
+    }
+    if (j < first || j + 8 > hi) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) hits &= j + i >= first && j + i < hi ? -1 : ~(1 << i);
+    }
+    return hits;
+  };
+  auto append = [&](const Raw8<T>& r, int j) {
+    int hits = wanted(r, j);
+    if (!__ballot(hits)) return;
+    int at = topk_place(__popc(hits), sh);
+    while (hits) {
+      const int i = __ffs(hits) - 1;
+      hits &= hits - 1;
+      if (at < CAP) buf[at] = ((uint64_t)order_key(r.pick(i)) << 32) | ~(uint32_t)(j - shift + i);
+      ++at;
+    }
+  };
+
+  if (tid == 0) sh.count = 0;
+  Raw8<T> raw[kTopkVecs], next[kTopkVecs];
+  // sum of 2^(x log2 e + neg), neg = -m log2 e rounded, for a reference m
+  float m = -INFINITY, neg = 0.f, s = 0.f;
+  int n = 0;
+  for (int t0 = lo - kTopkTile; t0 < hi; t0 += kTopkTile) {
+    if (t0 + kTopkTile < hi) {
+#pragma unroll
+      for (int u = 0; u < kTopkVecs; ++u) next[u] = fetch(t0 + kTopkTile, u);
+    }
+    if (t0 >= lo) {
+      uint32_t hot = 0;  // vectors in which some lane of the wave has something wanted
+#pragma unroll
+      for (int u = 0; u < kTopkVecs; ++u) {
+        float vm = raw[u].get(0), sum = 0.f;
+#pragma unroll
+        for (int i = 1; i < 8; ++i) vm = fmaxf(vm, raw[u].get(i));
+        // The reference moves only when it falls behind by 40: terms up to e^40
+        // are as precise and cannot overflow.
+        if (vm > m + 40.f) {
+          const float to = -vm * kLog2e;
+          s *= fast_exp2((m - vm) * kLog2e);
+          if (fabsf(neg) < 1e30f && m > -INFINITY) s *= fast_exp2(-fmaf(m, kLog2e, neg));  // the old neg's rounding
+          m = vm;
+          neg = to;
+        }
+        if (fabsf(neg) < 1e30f) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum += fast_exp2(fmaf(raw[u].get(i), kLog2e, neg));
+        } else {  // rows of a type's lowest value, infinities: the products above would overflow
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum += fast_exp2((raw[u].get(i) - m) * kLog2e);
+        }
+        s += sum;
+        // (NaN: fmaxf passes it over, the sum does not)
+        if (__ballot(!(vm < need_value) || sum != sum)) hot |= 1u << u;
       }
-    }
-    float vm = x[0];
+      auto vec = [&](int u) {
+        Raw8<T> r = raw[0];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) vm = fmaxf(vm, x[i]);
-    if (vm > m) {
-      s *= fast_exp2((m - vm) * kLog2e);
-      m = vm;
+        for (int k = 1; k < kTopkVecs; ++k) r.take(u == k, raw[k]);
+        return r;
+      };
+#pragma unroll 1
+      for (int u = 0; u < kTopkVecs; ++u)
+        if (hot & (1u << u)) append(vec(u), t0 + u * kTopkStep + tid * 8);
+      __syncthreads();
+      const int now = (int)sh.count;
+      __syncthreads();
+      // Words above the key come at a rate that the key's age sets: the buffer
+      // is cut when it holds twice what a cut leaves.  Where not all fitted,
+      // the tile is taken once more, a vector (2048 consecutive columns) at a
+      // time, with room made for each.
+      const bool again = now > CAP;
+      if (again) {
+        if (tid == 0) sh.count = (uint32_t)n;
+        __syncthreads();
+      } else {
+        n = now;
+        need = after > need ? after : need;
+      }
+#pragma unroll 1
+      for (int u = 0; u < (again ? kTopkVecs : 1); ++u) {
+        if (n > (again ? CAP - kTopkStep : cut_at) && (again || t0 + kTopkTile < hi)) {
+          uint32_t key;
+          n = topk_cut(buf, n, K, mid_limit, need > 0 ? need - 1 : 0, sh, &key);
+          need = key + 1 > need ? key + 1 : need;
+          need_value = key_value(need);
+        }
+        if (again) {
+          append(vec(u), t0 + u * kTopkStep + tid * 8);
+          __syncthreads();
+          n = (int)sh.count;
+          __syncthreads();
+        }
+      }
+      need = after > need ? after : need;
+      need_value = key_value(need);
     }
-    if (m > -INFINITY) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s += fast_exp2((x[i] - m) * kLog2e);
+    for (int u = 0; u < kTopkVecs; ++u) raw[u] = next[u];
+    if (t0 < lo) {
+      // the first tile's key: what is wanted of that tile, and `after` of the rest
+      const int total = (int)((hi < lo + kTopkTile ? hi : lo + kTopkTile) - first);
+      if (total > mid_limit) {
+        uint32_t key[kTopkVecs * 8];
+        uint32_t most = 0, least_vec = ~0u, least = ~0u;
+#pragma unroll
+        for (int u = 0; u < kTopkVecs; ++u) {
+          uint32_t top = 0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int j = lo + u * kTopkStep + tid * 8 + i;
+            const uint32_t k = j >= first && j < hi ? order_key(raw[u].get(i)) : 0;
+            key[u * 8 + i] = k;
+            top = k > top ? k : top;
+            least = k < least ? k : least;
+          }
+          most = top > most ? top : most;
+          least_vec = top < least_vec ? top : least_vec;
+        }
+        // the least of K or more maxima (of the threads, of the vectors) is
+        // reached by K elements; so is the least element
+        uint32_t from = K <= kTopkThreads ? most : K <= kTopkThreads * kTopkVecs ? least_vec : least;
+        topk_range(from, most, sh);
+        int got;
+        need = topk_select(
+            [&](auto f) {
+#pragma unroll
+              for (int e = 0; e < kTopkVecs * 8; ++e) f(key[e]);
+            },
+            from, most + 1, total, K, mid_limit, sh, &got);
+        after = need + 1;
+        need_value = key_value(need);
+      }
+      __syncthreads();
     }
-    int hits = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) hits |= order_key(x[i]) > thr ? 1 << i : 0;
-    hits &= in;
-    if (hits) {
-      uint32_t at = atomicAdd(&sh.count, (uint32_t)__popc(hits));
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (hits & (1 << i)) buf[at++] = ((uint64_t)order_key(x[i]) << 32) | ~(uint32_t)(j + i - shift);
-    }
-    __syncthreads();
-    const int n = (int)sh.count;
-    __syncthreads();
-    if (n > CAP - kTopkTile) thr = topk_cut(buf, n, K, sh);
   }
-  const int n = (int)sh.count;
-  __syncthreads();
-  if (n > K) topk_cut(buf, n, K, sh);
+  if (fabsf(neg) < 1e30f && m > -INFINITY) s *= fast_exp2(-fmaf(m, kLog2e, neg));  // the rounding of neg
+  const int limit = segments == 1 ? topk_sort_limit(K) : topk_slots(K);
+  if (n > limit) {
+    uint32_t key;
+    n = topk_cut(buf, n, K, limit, need > 0 ? need - 1 : 0, sh, &key);
+  }
   topk_reduce_state(m, s, sh);
   if (segments == 1) {
-    topk_sort(buf, K);
+    topk_sort<CAP>(buf, n);
     topk_write(buf, K, m, s, logprob, idx + row * K, val + row * K, lse + row);
   } else {
-    uint64_t* c = cand + (int64_t)blockIdx.x * K;
-    for (int k = tid; k < K; k += kTopkThreads) c[k] = k < n ? buf[k] : 0;
+    uint64_t* c = cand + (int64_t)blockIdx.x * limit;
+    for (int k = tid; k < limit; k += kTopkThreads) c[k] = k < n ? buf[k] : 0;
     if (tid == 0) state[blockIdx.x] = make_float2(m, s);
   }
 }
 
-// The segments' words of a row, cut to the K best in the same way.
+// The segments' words of a row, cut and sorted in the same way.
 template <int CAP>
 __global__ __launch_bounds__(kTopkThreads) void topk_merge_kernel(const uint64_t* __restrict__ cand,
                                                                   const float2* __restrict__ state, int K,
@@ -349,30 +755,43 @@ __global__ __launch_bounds__(kTopkThreads) void topk_merge_kernel(const uint64_t
     topk_masked_row(K, idx + row * K, val + row * K, lse + row);
     return;
   }
-  const uint64_t* c = cand + row * segments * K;
-  const int total = segments * K;
+  const int total = segments * topk_slots(K);
+  const uint64_t* c = cand + row * total;
   if (tid == 0) sh.count = 0;
   __syncthreads();
-  uint64_t floor_word = 0;
-  for (int t0 = 0; t0 < total; t0 += kTopkTile) {
-    for (int i = t0 + tid; i < total && i < t0 + kTopkTile; i += kTopkThreads) {
-      const uint64_t w = c[i];
-      if (w > floor_word) buf[atomicAdd(&sh.count, 1u)] = w;
+  uint32_t need = 1;  // (empty slots are zero)
+  uint32_t key;
+  int n = 0;
+  for (int t0 = 0; t0 < total; t0 += kTopkStep) {
+    if (n > CAP - kTopkStep) {
+      // (the words of a segment are in no order, so one with this very key may
+      // still come with a lower index)
+      n = topk_cut(buf, n, K, K + K / 4 + 64, need, sh, &need);
     }
+    uint64_t w[8];
+    int hits = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int at = t0 + i * kTopkThreads + tid;
+      w[i] = at < total ? c[at] : 0;
+      hits += (uint32_t)(w[i] >> 32) >= need ? 1 : 0;
+    }
+    int at = topk_place(hits, sh);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if ((uint32_t)(w[i] >> 32) >= need) buf[at++] = w[i];
     __syncthreads();
-    const int n = (int)sh.count;
+    n = (int)sh.count;
     __syncthreads();
-    // words of the K-th key itself may still be needed: segments come in index
-    // order, but the words of one segment do not
-    if (n > CAP - kTopkTile) floor_word = (uint64_t)topk_cut(buf, n, K, sh) << 32;
   }
-  const int n = (int)sh.count;
-  __syncthreads();
-  if (n > K) topk_cut(buf, n, K, sh);
+  if (n > topk_sort_limit(K)) n = topk_cut(buf, n, K, topk_sort_limit(K), need, sh, &key);
   float m = -INFINITY, s = 0.f;
-  for (int i = tid; i < segments; i += kTopkThreads) exp_merge(m, s, state[row * segments + i].x, state[row * segments + i].y);
+  for (int i = tid; i < segments; i += kTopkThreads) {
+    const float2 st = state[row * segments + i];
+    exp_merge(m, s, st.x, st.y);
+  }
   topk_reduce_state(m, s, sh);
-  topk_sort(buf, K);
+  topk_sort<CAP>(buf, n);
   topk_write(buf, K, m, s, logprob, idx + row * K, val + row * K, lse + row);
 }
 
@@ -411,89 +830,115 @@ __device__ __forceinline__ uint32_t token_key(const I* tokens, int64_t t, int64_
 }
 
 // Few positions: each one's rank is counted directly.  A workgroup ranks 64
-// positions; its waves share the comparisons.
+// positions; its waves share the comparisons, 16 keys at a time.
 constexpr int kRankMax = 8192;
 constexpr int kRankWaves = 16;
 template <typename I>
 __global__ __launch_bounds__(64 * kRankWaves) void rank_sort_kernel(const I* __restrict__ tokens, int n, int64_t V,
                                                                      int64_t v_offset, uint32_t* __restrict__ key_out,
-                                                                     uint32_t* __restrict__ pos_out) {
-  __shared__ uint32_t keys[kRankMax];
+                                                                     uint32_t* __restrict__ pos_out,
+                                                                     uint32_t* __restrict__ joins) {
+  __shared__ __attribute__((aligned(16))) uint32_t keys[kRankMax];
   __shared__ int part[kRankWaves][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int i = threadIdx.x; i < n; i += 64 * kRankWaves) keys[i] = token_key(tokens, i, V, v_offset);
+  const int n16 = (n + 15) & ~15;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *joins = 0;
+  for (int i = threadIdx.x; i < n16; i += 64 * kRankWaves)
+    keys[i] = i < n ? token_key(tokens, i, V, v_offset) : 0xffffffffu;
   __syncthreads();
   const int t = blockIdx.x * 64 + lane;
   const uint32_t mine = t < n ? keys[t] : 0;
   int less = 0;
-  for (int i = wave; i < n; i += kRankWaves) {
-    const uint32_t k = keys[i];
-    less += (k < mine || (k == mine && i < t)) ? 1 : 0;
+  for (int i = wave * 16; i < n16; i += kRankWaves * 16) {
+    u32x4 k[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) k[j] = *reinterpret_cast<const u32x4*>(keys + i + 4 * j);
+    // equal keys count where they come earlier: all of a group before this
+    // workgroup's positions, none of a group after them
+    if (i + 16 <= (int)blockIdx.x * 64) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) less += k[j >> 2][j & 3] <= mine ? 1 : 0;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const uint32_t x = k[j >> 2][j & 3];
+        less += (x < mine || (x == mine && i + j < t)) ? 1 : 0;
+      }
+    }
   }
   part[wave][lane] = less;
   __syncthreads();
   if (wave == 0 && t < n) {
     int r = 0;
+#pragma unroll
     for (int w = 0; w < kRankWaves; ++w) r += part[w][lane];
     key_out[r] = mine;
     pos_out[r] = (uint32_t)t;
   }
 }
 
-// Many positions: a stable radix sort, digits of up to 9 bits, blocks of 4096
-// keys.  hist[pass][block][digit] counts the keys of a block: the first pass's
-// table from the tokens, each later one while the pass before scatters.
-constexpr int kSortKeys = 4096;
+// Many positions: a stable radix sort, digits of up to 9 bits, a workgroup per
+// block of 1024 ROUNDS keys.  hist[block][digit] counts the keys of a block.
+// (Counting the next pass's digits while a pass scatters, by atomics, took
+// 40 us more than a launch of its own: frequent tokens meet on one counter.)
 constexpr int kSortWaves = 16;
 constexpr int kSortBins = 512;
 
-template <typename I>
+template <typename I, int ROUNDS>
 __global__ __launch_bounds__(64 * kSortWaves) void sort_hist_kernel(const I* __restrict__ tokens, int64_t n, int64_t V,
-                                                                     int64_t v_offset, int bins, int passes,
+                                                                     int64_t v_offset, int bins, int shift,
                                                                      uint32_t* __restrict__ key,
-                                                                     uint32_t* __restrict__ hist) {
+                                                                     uint32_t* __restrict__ hist,
+                                                                     uint32_t* __restrict__ joins) {
+  // tokens NULL: the keys are there already
   __shared__ uint32_t h[kSortBins];
-  const int64_t row = (int64_t)gridDim.x * kSortBins;
-  for (int i = threadIdx.x; i < kSortBins; i += 64 * kSortWaves) h[i] = 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *joins = 0;
+  if (threadIdx.x < kSortBins) h[threadIdx.x] = 0;
   __syncthreads();
-  for (int i = threadIdx.x; i < kSortKeys; i += 64 * kSortWaves) {
-    const int64_t t = (int64_t)blockIdx.x * kSortKeys + i;
+#pragma unroll
+  for (int r = 0; r < ROUNDS; ++r) {
+    const int64_t t = ((int64_t)blockIdx.x * ROUNDS + r) * 1024 + threadIdx.x;
     if (t < n) {
-      const uint32_t k = token_key(tokens, t, V, v_offset);
-      key[t] = k;
-      atomicAdd(&h[k & (bins - 1)], 1u);
+      uint32_t k;
+      if (tokens != nullptr)
+        key[t] = k = token_key(tokens, t, V, v_offset);
+      else
+        k = key[t];
+      atomicAdd(&h[(k >> shift) & (bins - 1)], 1u);
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < kSortBins; i += 64 * kSortWaves) {
-    uint32_t* at = hist + (int64_t)blockIdx.x * kSortBins + i;
-    at[0] = h[i];
-    for (int p = 1; p < passes; ++p) at[p * row] = 0;
-  }
+  if (threadIdx.x < kSortBins) hist[(int64_t)blockIdx.x * kSortBins + threadIdx.x] = h[threadIdx.x];
 }
 
+template <int ROUNDS>
 __global__ __launch_bounds__(64 * kSortWaves) void sort_scatter_kernel(
-    const uint32_t* __restrict__ key_in, const uint32_t* __restrict__ pos_in, int64_t n, int pass, int passes,
-    int digit_bits, uint32_t* hist, uint32_t* __restrict__ key_out, uint32_t* __restrict__ pos_out) {
-  __shared__ uint32_t off[kSortBins];                 // where the block's first key of a digit goes
-  __shared__ uint32_t cnt[kSortWaves][kSortBins];     // per wave: keys of a digit, then the wave's next place
-  __shared__ uint32_t wtot[8];
+    const uint32_t* __restrict__ key_in, const uint32_t* __restrict__ pos_in, int64_t n, int shift, int digit_bits,
+    const uint32_t* __restrict__ hist, uint32_t* __restrict__ key_out, uint32_t* __restrict__ pos_out) {
+  __shared__ uint32_t cnt[kSortWaves][kSortBins];  // per wave: keys of a digit, then the wave's next place
+  __shared__ uint32_t wtot[kSortBins / 64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int bins = 1 << digit_bits, shift = pass * digit_bits;
-  const int64_t row = (int64_t)gridDim.x * kSortBins;
-  const uint32_t* mine = hist + (int64_t)pass * row;
-  const int64_t begin = (int64_t)blockIdx.x * kSortKeys;
+  const int bins = 1 << digit_bits;
 
+  // a wave's keys are consecutive, so waves, rounds and lanes are in order
+  uint32_t k[ROUNDS], pos[ROUNDS];
+#pragma unroll
+  for (int r = 0; r < ROUNDS; ++r) {
+    const int64_t t = ((int64_t)blockIdx.x * 1024 + wave * 64) * ROUNDS + r * 64 + lane;
+    k[r] = t < n ? key_in[t] : 0;
+    pos[r] = (t < n && pos_in != nullptr) ? pos_in[t] : (uint32_t)t;
+  }
   for (int i = tid; i < kSortWaves * kSortBins; i += 64 * kSortWaves) (&cnt[0][0])[i] = 0;
   uint32_t before = 0, total = 0;
-  if (tid < kSortBins && tid < bins) {
-    for (int64_t b = 0; b < gridDim.x; ++b) {
-      const uint32_t c = mine[b * kSortBins + tid];
+  if (tid < bins) {
+    const int blocks = gridDim.x, me = blockIdx.x;
+#pragma unroll 16
+    for (int b = 0; b < blocks; ++b) {
+      const uint32_t c = hist[(int64_t)b * kSortBins + tid];
       total += c;
-      before += b < blockIdx.x ? c : 0;
+      before += b < me ? c : 0;
     }
   }
-  __syncthreads();
   // exclusive sums of the totals over the digits
   uint32_t inc = total;
 #pragma unroll
@@ -501,25 +946,18 @@ __global__ __launch_bounds__(64 * kSortWaves) void sort_scatter_kernel(
     const uint32_t v = __shfl_up(inc, o);
     if (lane >= o) inc += v;
   }
-  if (wave < 8 && lane == 63) wtot[wave] = inc;
+  if (wave < kSortBins / 64 && lane == 63) wtot[wave] = inc;
   __syncthreads();
-  if (tid < kSortBins) {
-    uint32_t o = inc - total + before;
-    for (int w = 0; w < wave; ++w) o += wtot[w];
-    off[tid] = o;
-  }
-  // a wave's keys are consecutive, so waves, rounds and lanes are in order
-  constexpr int kRounds = kSortKeys / (64 * kSortWaves);
-  uint32_t k[kRounds];
 #pragma unroll
-  for (int r = 0; r < kRounds; ++r) {
-    const int64_t t = begin + (wave * kRounds + r) * 64 + lane;
-    k[r] = t < n ? key_in[t] : 0;
+  for (int r = 0; r < ROUNDS; ++r) {
+    const int64_t t = ((int64_t)blockIdx.x * 1024 + wave * 64) * ROUNDS + r * 64 + lane;
     if (t < n) atomicAdd(&cnt[wave][(k[r] >> shift) & (bins - 1)], 1u);
   }
   __syncthreads();
   if (tid < kSortBins) {
-    uint32_t at = off[tid];
+    uint32_t at = inc - total + before;
+    for (int w = 0; w < wave; ++w) at += wtot[w];
+#pragma unroll
     for (int w = 0; w < kSortWaves; ++w) {
       const uint32_t c = cnt[w][tid];
       cnt[w][tid] = at;
@@ -528,12 +966,13 @@ __global__ __launch_bounds__(64 * kSortWaves) void sort_scatter_kernel(
   }
   __syncthreads();
 #pragma unroll
-  for (int r = 0; r < kRounds; ++r) {
-    const int64_t t = begin + (wave * kRounds + r) * 64 + lane;
+  for (int r = 0; r < ROUNDS; ++r) {
+    const int64_t t = ((int64_t)blockIdx.x * 1024 + wave * 64) * ROUNDS + r * 64 + lane;
     const bool ok = t < n;
     const uint32_t dgt = (k[r] >> shift) & (bins - 1);
     uint64_t same = __ballot(ok);
-    for (int b = 0; b < digit_bits; ++b) {
+#pragma unroll
+    for (int b = 0; b < 9; ++b) {  // (bits past digit_bits are zero everywhere)
       const uint64_t one = __ballot((dgt >> b) & 1);
       same &= ((dgt >> b) & 1) ? one : ~one;
     }
@@ -545,87 +984,125 @@ __global__ __launch_bounds__(64 * kSortWaves) void sort_scatter_kernel(
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     if (ok) {
       key_out[at] = k[r];
-      pos_out[at] = pos_in ? pos_in[t] : (uint32_t)t;
-      if (pass + 1 < passes)
-        atomicAdd(hist + (int64_t)(pass + 1) * row + (int64_t)(at / kSortKeys) * kSortBins +
-                      ((k[r] >> (shift + digit_bits)) & (bins - 1)),
-                  1u);
+      pos_out[at] = pos[r];
     }
   }
 }
 
-template <typename G>
-__device__ __forceinline__ void write_grad(G* dst, const float* sum, float scale, int accumulate) {
-  float f[8];
-  if (accumulate) {
-    load8(dst, f);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] += scale * sum[i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = scale * sum[i];
-  }
-  store8(dst, f);
-}
-
-// A thread sums eight columns over one chunk of the sorted positions.  Runs of
-// one token inside the chunk are final; a run that crosses a border leaves its
-// sum in part[chunk][0] (it began before the chunk) or part[chunk][1] (it
-// begins here and goes on).
-template <typename T, typename G>
+// A thread sums eight columns over one chunk of the sorted positions, four at a
+// time: their rows, and the old gradients of the tokens that end among them,
+// are loaded together, so that eight loads are under way instead of one (the
+// rows of a token are anywhere in dY).  Runs of one token inside the chunk are
+// final; a run that crosses a border leaves its sum in part[chunk][0] (it began
+// before the chunk) or part[chunk][1] (it begins here and goes on; the chunk is
+// then listed for the join).
+constexpr int kSumBatch = 4;
+template <typename T, typename G, bool ADD>
 __global__ __launch_bounds__(256) void embedding_sum_kernel(const T* __restrict__ dY, const uint32_t* __restrict__ key,
                                                             const uint32_t* __restrict__ pos, int64_t n, int chunk,
                                                             int64_t chunks, Units q, uint32_t V, float scale,
-                                                            int accumulate, G* __restrict__ dW,
-                                                            float* __restrict__ part) {
+                                                            G* __restrict__ dW, float* __restrict__ part,
+                                                            uint32_t* __restrict__ joins) {
   int64_t c;
   uint32_t col;
   unit_at(q, (int64_t)blockIdx.x * 256, threadIdx.x, &c, &col);
   if (c >= chunks) return;
   const int64_t b = c * chunk, e = b + chunk < n ? b + chunk : n;
-  int64_t i = b;
-  while (i < e) {
-    const uint32_t k = key[i];
-    if (k >= V) return;
-    float sum[8] = {};
-    const bool from_before = i == b && b > 0 && key[b - 1] == k;
-    for (; i < e && key[i] == k; ++i) {
-      float f[8];
-      load8(dY + ((int64_t)pos[i] * q.n + col) * 8, f);
+  bool from_before = b > 0 && key[b - 1] == key[b];
+  float sum[8] = {};
+  for (int64_t i = b; i < e; i += kSumBatch) {
+    uint32_t k[kSumBatch + 1], p[kSumBatch];
+    const int m = e - i < kSumBatch ? (int)(e - i) : kSumBatch;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum[j] += f[j];
+    for (int j = 0; j < kSumBatch; ++j) {
+      k[j] = j < m ? key[i + j] : 0xffffffffu;
+      p[j] = j < m ? pos[i + j] : 0;
     }
-    const bool goes_on = i == e && e < n && key[e] == k;
-    if (!from_before && !goes_on)
-      write_grad(dW + ((int64_t)k * q.n + col) * 8, sum, scale, accumulate);
-    else
-      store8(part + ((2 * c + (from_before ? 0 : 1)) * (int64_t)q.n + col) * 8, sum);
+    k[kSumBatch] = i + kSumBatch < e ? key[i + kSumBatch] : 0xffffffffu;
+    if (k[0] >= V) return;
+    float f[kSumBatch][8], old[kSumBatch][8];
+#pragma unroll
+    for (int j = 0; j < kSumBatch; ++j) {
+      if (k[j] < V) load8(dY + ((int64_t)p[j] * q.n + col) * 8, f[j]);
+      if (ADD && k[j] < V && k[j] != k[j + 1]) load8(dW + ((int64_t)k[j] * q.n + col) * 8, old[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < kSumBatch; ++j) {
+      if (k[j] >= V) return;
+#pragma unroll
+      for (int x = 0; x < 8; ++x) sum[x] += f[j][x];
+      if (k[j] != k[j + 1]) {  // the run ends here, or the chunk does
+        const bool goes_on = i + j + 1 == e && e < n && key[e] == k[j];
+        if (!from_before && !goes_on) {
+#pragma unroll
+          for (int x = 0; x < 8; ++x) sum[x] = ADD ? old[j][x] + scale * sum[x] : scale * sum[x];
+          store8(dW + ((int64_t)k[j] * q.n + col) * 8, sum);
+        } else {
+          store8(part + ((2 * c + (from_before ? 0 : 1)) * (int64_t)q.n + col) * 8, sum);
+          if (!from_before && col == 0) joins[1 + atomicAdd(joins, 1u)] = (uint32_t)c;
+        }
+        from_before = false;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) sum[x] = 0.f;
+      }
+    }
   }
 }
 
-// The runs that cross borders: the chunk where one begins adds its parts.
-template <typename G>
+// The runs that cross borders: the listed chunk, where one begins, and the
+// chunks that it goes on through.  A workgroup takes 32 vectors of columns of
+// one run; eight slices share its chunks and are added in order, so the order
+// of the list does not matter.
+template <typename G, bool ADD>
 __global__ __launch_bounds__(256) void embedding_join_kernel(const uint32_t* __restrict__ key, int64_t n, int chunk,
-                                                             int64_t chunks, Units q, uint32_t V, float scale,
-                                                             int accumulate, G* __restrict__ dW,
-                                                             const float* __restrict__ part) {
-  int64_t c;
-  uint32_t col;
-  unit_at(q, (int64_t)blockIdx.x * 256, threadIdx.x, &c, &col);
-  if (c + 1 >= chunks) return;
-  const int64_t b = c * chunk, e = b + chunk;
-  const uint32_t k = key[e - 1];
-  if (k >= V || key[e] != k) return;                       // no run goes on from here
-  if (key[b] == k && b > 0 && key[b - 1] == k) return;     // it began earlier
-  float sum[8];
-  load8(part + ((2 * c + 1) * (int64_t)q.n + col) * 8, sum);
-  for (int64_t j = c + 1; j < chunks && key[j * chunk] == k; ++j) {
-    float f[8];
-    load8(part + (2 * j * (int64_t)q.n + col) * 8, f);
+                                                             int64_t chunks, int nv, float scale, G* __restrict__ dW,
+                                                             const float* __restrict__ part,
+                                                             const uint32_t* __restrict__ joins) {
+  __shared__ float sums[8][32][9];
+  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+  const int slabs = (nv + 31) / 32;
+  const int64_t items = (int64_t)joins[0] * slabs;
+  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+    const int64_t c = joins[1 + it / slabs];
+    const int col = (int)(it % slabs) * 32 + lane;
+    const uint32_t k = key[(c + 1) * chunk];
+    // the chunks after c that begin with this token: [c + 1, end)
+    int64_t lo = c + 2, hi = chunks;
+    while (lo < hi) {
+      const int64_t mid = (lo + hi) >> 1;
+      if (key[mid * chunk] == k)
+        lo = mid + 1;
+      else
+        hi = mid;
+    }
+    float sum[8] = {};
+    if (col < nv) {
+      if (slice == 0) load8(part + ((2 * c + 1) * (int64_t)nv + col) * 8, sum);
+#pragma unroll 4
+      for (int64_t j = c + 1 + slice; j < lo; j += 8) {
+        float f[8];
+        load8(part + (2 * j * (int64_t)nv + col) * 8, f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum[i] += f[i];
+        for (int x = 0; x < 8; ++x) sum[x] += f[x];
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < 8; ++x) sums[slice][lane][x] = sum[x];
+    __syncthreads();
+    if (slice == 0 && col < nv) {
+#pragma unroll
+      for (int s = 1; s < 8; ++s)
+#pragma unroll
+        for (int x = 0; x < 8; ++x) sum[x] += sums[s][lane][x];
+      G* dst = dW + ((int64_t)k * nv + col) * 8;
+      float old[8] = {};
+      if (ADD) load8(dst, old);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) sum[x] = ADD ? old[x] + scale * sum[x] : scale * sum[x];
+      store8(dst, sum);
+    }
+    __syncthreads();
   }
-  write_grad(dW + ((int64_t)k * q.n + col) * 8, sum, scale, accumulate);
 }
 
 __global__ __launch_bounds__(256) void zero_kernel(u32x4* __restrict__ p, int64_t n) {
@@ -842,19 +1319,28 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(const T* __restrict
   }
 }
 
+// The workgroups' shares added: 16 lanes of four columns each and 64 slices of
+// the shares, the slices added in a fixed order.  (One thread per eight columns
+// walking all 1024 shares took 282 us at d = 2880, on two workgroups; this
+// takes 6 us.)
 template <typename T>
-__global__ __launch_bounds__(256) void norm_dweight_kernel(const float* __restrict__ part, int groups, int nv,
-                                                           T* __restrict__ dweight) {
-  const int v = blockIdx.x * 256 + threadIdx.x;
-  if (v >= nv) return;
-  float sum[8] = {};
-  for (int g = 0; g < groups; ++g) {
-    float f[8];
-    load8(part + ((int64_t)g * nv + v) * 8, f);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sum[i] += f[i];
+__global__ __launch_bounds__(1024) void norm_dweight_kernel(const float* __restrict__ part, int groups, int d,
+                                                            T* __restrict__ dweight) {
+  __shared__ f32x4 sums[64][16];
+  const int lane = threadIdx.x & 15, slice = threadIdx.x >> 4;
+  const int col = (blockIdx.x * 16 + lane) * 4;
+  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+  if (col < d) {
+#pragma unroll 8
+    for (int g = slice; g < groups; g += 64) sum += *reinterpret_cast<const f32x4*>(part + (int64_t)g * d + col);
   }
-  store8(dweight + (int64_t)v * 8, sum);
+  sums[slice][lane] = sum;
+  __syncthreads();
+  if (slice == 0 && col < d) {
+#pragma unroll 8
+    for (int i = 1; i < 64; ++i) sum += sums[i][lane];
+    store4(dweight + col, sum);
+  }
 }
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -862,25 +1348,28 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 }  // namespace
 
 // -------------------------------------------------------------- launchers --
-void topk_plan(int64_t rows, int64_t V, int64_t K, int* segments, int64_t* seg_cols) {
+// Rows are cut into segments (whole tiles) where there are too few of them for
+// three workgroups on each of the 256 compute units.
+void topk_plan(int64_t rows, int64_t V, int* segments, int64_t* seg_cols) {
   const int64_t tiles = cdiv(V + 7, kTopkTile);
-  const int64_t want = std::max<int64_t>(1, std::min<int64_t>({cdiv(1024, std::max<int64_t>(rows, 1)), tiles, 64}));
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>({cdiv(768, std::max<int64_t>(rows, 1)), tiles, 64}));
   const int64_t per = cdiv(tiles, want);
   *seg_cols = per * kTopkTile;
   *segments = (int)cdiv(tiles, per);
 }
+int64_t topk_segment_words(int64_t K) { return topk_slots((int)K); }
 
 hipError_t launch_teacher_topk(const void* logits, int bf16, int64_t rows, int64_t V, int K, int logprob,
                                const uint8_t* mask, int* idx, float* val, float* lse, uint64_t* cand, float2* state,
                                hipStream_t st) {
   int segments;
   int64_t seg_cols;
-  topk_plan(rows, V, K, &segments, &seg_cols);
+  topk_plan(rows, V, &segments, &seg_cols);
   const unsigned blocks = (unsigned)(rows * segments);
   auto go = [&](auto* p, auto cap) {
     using E = std::remove_const_t<std::remove_pointer_t<decltype(p)>>;
     constexpr int CAP = decltype(cap)::value;
-    topk_rows_kernel<E, CAP><<<blocks, kTopkThreads, 0, st>>>(p, V, K, segments, seg_cols, logprob, mask, idx, val, lse,
+    topk_rows_kernel<E, CAP><<<blocks, kTopkThreads, 0, st>>>(p, rows, (int)V, K, segments, (int)seg_cols, logprob, mask, idx, val, lse,
                                                              cand, state);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || segments == 1) return e;
@@ -888,7 +1377,7 @@ hipError_t launch_teacher_topk(const void* logits, int bf16, int64_t rows, int64
                                                                    lse);
     return hipGetLastError();
   };
-  // the buffer holds K words and a tile, and a power of two for the sort
+  // room for what a cut may leave and 2048 more words, and for the final sort
   using Small = std::integral_constant<int, 4096>;
   using Large = std::integral_constant<int, 8192>;
   if (bf16) return K <= 1024 ? go((const bf16_t*)logits, Small{}) : go((const bf16_t*)logits, Large{});
@@ -918,66 +1407,81 @@ EmbedWs embed_ws(int64_t T, int64_t V, int64_t d) {
     o += (bytes + 255) & ~(size_t)255;
     return at;
   };
-  w.chunk = T <= 4096 ? 8 : 32;
+  w.chunk = T <= 4096 ? 8 : 16;
   w.chunks = cdiv(T, w.chunk);
   if (T > kRankMax) {
     int bits = 1;
     while (((int64_t)1 << bits) <= V) ++bits;  // keys 0 .. V
     w.passes = (int)cdiv(bits, 9);
     w.digit_bits = (int)cdiv(bits, w.passes);
-    w.sort_blocks = cdiv(T, kSortKeys);
+    // a scattering workgroup adds up the counts of all blocks: few of them
+    w.sort_rounds = T <= 65536 ? 1 : 4;
+    w.sort_blocks = cdiv(T, 1024 * w.sort_rounds);
   }
   w.key0 = take(T * 4);
   w.pos0 = take(T * 4);
   if (w.passes) {
     w.key1 = take(T * 4);
     w.pos1 = take(T * 4);
-    w.hist = take((size_t)w.passes * w.sort_blocks * kSortBins * 4);
+    w.hist = take((size_t)w.sort_blocks * kSortBins * 4);
   }
+  w.joins = take((size_t)(1 + w.chunks) * 4);
   w.part = take((size_t)2 * w.chunks * d * 4);
   w.total = o;
   return w;
 }
 
-template <typename T, typename G>
-static hipError_t embedding_reduce(const T* dY, int64_t n, int d, int64_t V, float scale, G* dW, int accumulate,
-                                   const EmbedWs& w, const uint32_t* key, const uint32_t* pos, float* part,
-                                   hipStream_t st) {
+template <bool ADD, typename T, typename G>
+static hipError_t embedding_reduce(const T* dY, int64_t n, int d, int64_t V, float scale, G* dW, const EmbedWs& w,
+                                   char* ws, const uint32_t* key, const uint32_t* pos, hipStream_t st) {
   const Units q = units(d / 8);
-  const unsigned blocks = (unsigned)cdiv(w.chunks * q.n, 256);
-  embedding_sum_kernel<<<blocks, 256, 0, st>>>(dY, key, pos, n, (int)w.chunk, w.chunks, q, (uint32_t)V, scale,
-                                               accumulate, dW, part);
+  float* part = (float*)(ws + w.part);
+  uint32_t* joins = (uint32_t*)(ws + w.joins);
+  embedding_sum_kernel<T, G, ADD><<<(unsigned)cdiv(w.chunks * q.n, 256), 256, 0, st>>>(
+      dY, key, pos, n, (int)w.chunk, w.chunks, q, (uint32_t)V, scale, dW, part, joins);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || w.chunks < 2) return e;
-  embedding_join_kernel<<<blocks, 256, 0, st>>>(key, n, (int)w.chunk, w.chunks, q, (uint32_t)V, scale, accumulate, dW,
-                                                (const float*)part);
+  const int64_t most = (w.chunks - 1) * cdiv(q.n, 32);
+  embedding_join_kernel<G, ADD><<<(unsigned)std::min<int64_t>(most, 1024), 256, 0, st>>>(
+      key, n, (int)w.chunk, w.chunks, (int)q.n, scale, dW, part, joins);
   return hipGetLastError();
 }
 
-template <typename I>
-static hipError_t embedding_sort(const I* tokens, int64_t T, int64_t V, int64_t v_offset, const EmbedWs& w, char* ws,
-                                 const uint32_t** key, const uint32_t** pos, hipStream_t st) {
+template <int ROUNDS, typename I>
+static hipError_t embedding_radix(const I* tokens, int64_t T, int64_t V, int64_t v_offset, const EmbedWs& w, char* ws,
+                                  const uint32_t** key, const uint32_t** pos, hipStream_t st) {
   uint32_t* k[2] = {(uint32_t*)(ws + w.key0), (uint32_t*)(ws + w.key1)};
   uint32_t* p[2] = {(uint32_t*)(ws + w.pos0), (uint32_t*)(ws + w.pos1)};
-  hipError_t e;
-  if (!w.passes) {
-    rank_sort_kernel<<<(unsigned)cdiv(T, 64), 64 * kRankWaves, 0, st>>>(tokens, (int)T, V, v_offset, k[0], p[0]);
-    *key = k[0];
-    *pos = p[0];
-    return hipGetLastError();
-  }
   uint32_t* hist = (uint32_t*)(ws + w.hist);
-  const unsigned blocks = (unsigned)w.sort_blocks;
-  sort_hist_kernel<<<blocks, 64 * kSortWaves, 0, st>>>(tokens, T, V, v_offset, 1 << w.digit_bits, w.passes, k[0], hist);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
+  const unsigned blocks = (unsigned)w.sort_blocks, threads = 64 * kSortWaves;
   for (int i = 0; i < w.passes; ++i) {
-    sort_scatter_kernel<<<blocks, 64 * kSortWaves, 0, st>>>(k[i & 1], i ? p[i & 1] : nullptr, T, i, w.passes,
-                                                            w.digit_bits, hist, k[~i & 1], p[~i & 1]);
+    const int from = i & 1, shift = i * w.digit_bits;
+    sort_hist_kernel<I, ROUNDS><<<blocks, threads, 0, st>>>(i ? nullptr : tokens, T, V, v_offset, 1 << w.digit_bits,
+                                                            shift, k[from], hist, (uint32_t*)(ws + w.joins));
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    sort_scatter_kernel<ROUNDS><<<blocks, threads, 0, st>>>(k[from], i ? p[from] : nullptr, T, shift, w.digit_bits,
+                                                            hist, k[from ^ 1], p[from ^ 1]);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   *key = k[w.passes & 1];
   *pos = p[w.passes & 1];
   return hipSuccess;
+}
+
+template <typename I>
+static hipError_t embedding_sort(const I* tokens, int64_t T, int64_t V, int64_t v_offset, const EmbedWs& w, char* ws,
+                                 const uint32_t** key, const uint32_t** pos, hipStream_t st) {
+  if (w.passes)
+    return w.sort_rounds == 1 ? embedding_radix<1>(tokens, T, V, v_offset, w, ws, key, pos, st)
+                              : embedding_radix<4>(tokens, T, V, v_offset, w, ws, key, pos, st);
+  *key = (uint32_t*)(ws + w.key0);
+  *pos = (uint32_t*)(ws + w.pos0);
+  rank_sort_kernel<<<(unsigned)cdiv(T, 64), 64 * kRankWaves, 0, st>>>(tokens, (int)T, V, v_offset,
+                                                                      (uint32_t*)(ws + w.key0),
+                                                                      (uint32_t*)(ws + w.pos0),
+                                                                      (uint32_t*)(ws + w.joins));
+  return hipGetLastError();
 }
 
 hipError_t launch_embedding_backward(const void* dY, int bf16, int64_t T, int d, const void* tokens, int tokens64,
@@ -997,11 +1501,12 @@ hipError_t launch_embedding_backward(const void* dY, int bf16, int64_t T, int d,
   else
     e = embedding_sort((const int32_t*)tokens, T, V, v_offset, w, ws, &key, &pos, st);
   if (e != hipSuccess) return e;
-  float* part = (float*)(ws + w.part);
-  if (bf16 && dw_bf16) return embedding_reduce((const bf16_t*)dY, T, d, V, scale, (bf16_t*)dW, accumulate, w, key, pos, part, st);
-  if (bf16) return embedding_reduce((const bf16_t*)dY, T, d, V, scale, (float*)dW, accumulate, w, key, pos, part, st);
-  if (dw_bf16) return embedding_reduce((const float*)dY, T, d, V, scale, (bf16_t*)dW, accumulate, w, key, pos, part, st);
-  return embedding_reduce((const float*)dY, T, d, V, scale, (float*)dW, accumulate, w, key, pos, part, st);
+  auto go = [&](auto* dy, auto* dw) {
+    return accumulate ? embedding_reduce<true>(dy, T, d, V, scale, dw, w, ws, key, pos, st)
+                      : embedding_reduce<false>(dy, T, d, V, scale, dw, w, ws, key, pos, st);
+  };
+  if (bf16) return dw_bf16 ? go((const bf16_t*)dY, (bf16_t*)dW) : go((const bf16_t*)dY, (float*)dW);
+  return dw_bf16 ? go((const float*)dY, (bf16_t*)dW) : go((const float*)dY, (float*)dW);
 }
 
 hipError_t launch_act_encode(const void* x, int bf16, int64_t T, int d, int8_t* codes, uint8_t* exps, hipStream_t st) {
@@ -1088,11 +1593,11 @@ hipError_t launch_norm_backward(const void* dy, int bf16, int64_t T, int d, cons
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  const unsigned blocks = (unsigned)cdiv(nv, 256);
+  const unsigned blocks = (unsigned)cdiv(d, 64);
   if (weight_bf16)
-    norm_dweight_kernel<<<blocks, 256, 0, st>>>(part, (int)groups, nv, (bf16_t*)dweight);
+    norm_dweight_kernel<<<blocks, 1024, 0, st>>>(part, (int)groups, d, (bf16_t*)dweight);
   else
-    norm_dweight_kernel<<<blocks, 256, 0, st>>>(part, (int)groups, nv, (float*)dweight);
+    norm_dweight_kernel<<<blocks, 1024, 0, st>>>(part, (int)groups, d, (float*)dweight);
   return hipGetLastError();
 }
 

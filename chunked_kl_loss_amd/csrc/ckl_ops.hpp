@@ -11,9 +11,10 @@ namespace ckl {
 // ------------------------------------------------------------ teacher top-K --
 // Segments a row of V logits is cut into when there are `rows` of them, and
 // the shifted columns of a segment.
-void topk_plan(int64_t rows, int64_t V, int64_t K, int* segments, int64_t* seg_cols);
-// cand [rows][segments][K] and state [rows][segments] are used when the plan
-// has more than one segment.
+void topk_plan(int64_t rows, int64_t V, int* segments, int64_t* seg_cols);
+// cand [rows][segments][words of a segment] and state [rows][segments] are used
+// when the plan has more than one segment.
+int64_t topk_segment_words(int64_t K);
 hipError_t launch_teacher_topk(const void* logits, int bf16, int64_t rows, int64_t V, int K, int logprob,
                                const uint8_t* mask, int* idx, float* val, float* lse, uint64_t* cand, float2* state,
                                hipStream_t st);
@@ -23,10 +24,10 @@ hipError_t launch_embedding_forward(const void* W, int bf16, int64_t V, int d, i
                                     int tokens64, int64_t T, float scale, void* out, hipStream_t st);
 // Workspace of the backward pass, in bytes from its start.
 struct EmbedWs {
-  size_t key0, key1, pos0, pos1, hist, part, total;
+  size_t key0, key1, pos0, pos1, hist, joins, part, total;
   int64_t chunk, chunks;    // positions a reducing thread walks, and their number
   int passes, digit_bits;   // radix passes (0: the positions are ranked directly)
-  int64_t sort_blocks;
+  int64_t sort_rounds, sort_blocks;  // a sorting workgroup's keys / 1024, and their number
 };
 EmbedWs embed_ws(int64_t T, int64_t V, int64_t d);
 hipError_t launch_embedding_backward(const void* dY, int bf16, int64_t T, int d, const void* tokens, int tokens64,

@@ -54,9 +54,9 @@ TopkWs topk_layout(int64_t T, int64_t V, int64_t K) {
   TopkWs w{};
   int segments = 1;
   int64_t cols = 0;
-  if (T > 0) ckl::topk_plan(T, V, K, &segments, &cols);
+  if (T > 0) ckl::topk_plan(T, V, &segments, &cols);
   if (segments > 1) {
-    w.state = align256((size_t)T * segments * K * 8);
+    w.state = align256((size_t)T * segments * ckl::topk_segment_words(K) * 8);
     w.total = w.state + align256((size_t)T * segments * 8);
   }
   return w;
