@@ -107,16 +107,21 @@ Units units(int64_t n) {
 // segment of the row in tiles of 8192 columns held in registers.  From the
 // first it takes a key with at least K elements at or above it, found by
 // counting the keys of a range in 256 bins; from then on only elements above
-// that key go into a buffer in shared memory: those with the very key come later
-// than K others and lose.  A filling buffer is cut in the same way, which raises
-// the key.  Where too many elements share one key for a cut by keys, a radix
-// selection over the words decides by index.  What remains is sorted.  Per
-// vector of eight the common path is eight exponentials, one running maximum
-// and one comparison.
+// that key are wanted: those with the very key come later than K others and
+// lose.  A vector of eight whose maximum is wanted is put on its wave's list;
+// when lists fill up, their vectors are read again, one to a lane, and what is
+// wanted of them goes into a buffer in shared memory.  (Taking elements where
+// they are found costs each wave three times the common path's instructions
+// for one lane's sake: 245 us against 185 at 2048 x 201088.)  A filling buffer
+// is cut as the first tile was, which raises the key.  Where too many elements
+// share one key for a cut by keys, a radix selection over the words decides by
+// index.  What remains is sorted.  The common path, per vector of eight: eight
+// exponentials, one running maximum and one comparison.
 constexpr int kTopkThreads = 256;
 constexpr int kTopkVecs = 4;                                 // vectors of eight a thread holds
 constexpr int kTopkStep = kTopkThreads * 8;                  // columns of one vector each
 constexpr int kTopkTile = kTopkVecs * kTopkStep;
+constexpr int kTopkList = 64 * kTopkVecs + 64;               // vectors on a wave's list: a tile's, and 64
 constexpr uint32_t kNanKey = 0xfffffffeu;                    // every key lies below 2^32 - 1
 
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -134,6 +139,7 @@ struct TopkShared {
   uint32_t hist[256];
   uint32_t wave_n[4];
   uint32_t range[2][4];
+  uint32_t pending[2][4];
   float wave_m[4], wave_s[4];
   uint32_t count, sel, need, bin;
 };
@@ -260,18 +266,21 @@ __device__ __forceinline__ void topk_cut_exact(uint64_t* buf, int n, int K, Topk
   __syncthreads();
 }
 
-// Cuts the n > limit >= K words of buf (n < 64 kTopkThreads), none with a key
-// below `floor_key`, to at most `limit` of the largest, at least K, in any
-// order.  Returns their number and sets *key to a key that at least K of them,
+// Cuts the n > limit >= K words of buf to at most `limit` of the largest, at
+// least K, in any order.  Returns their number and sets *key to a key that at least K of them,
 // and none less, reach.  Begins and ends with a barrier.
-__device__ __forceinline__ int topk_cut(uint64_t* buf, int n, int K, int limit, uint32_t floor_key, TopkShared& sh,
+__device__ __forceinline__ int topk_cut(uint64_t* buf, int n, int K, int limit, TopkShared& sh,
                                         uint32_t* key) {
   const int tid = threadIdx.x;
   const uint32_t* keys = reinterpret_cast<const uint32_t*>(buf) + 1;
   __syncthreads();
-  uint32_t least = 0, most = 0;
+  uint32_t least = ~0u, most = 0;
 #pragma unroll 4
-  for (int i = tid; i < n; i += kTopkThreads) most = keys[2 * i] > most ? keys[2 * i] : most;
+  for (int i = tid; i < n; i += kTopkThreads) {
+    const uint32_t k = keys[2 * i];
+    most = k > most ? k : most;
+    least = k < least ? k : least;
+  }
   topk_range(least, most, sh);
   int kept;
   const uint32_t t = topk_select(
@@ -279,7 +288,7 @@ __device__ __forceinline__ int topk_cut(uint64_t* buf, int n, int K, int limit, 
 #pragma unroll 4
         for (int i = tid; i < n; i += kTopkThreads) f(keys[2 * i]);
       },
-      floor_key, most + 1, n, K, limit, sh, &kept);
+      least, most + 1, n, K, limit, sh, &kept);
   *key = t;
   if (kept > limit) {
     topk_cut_exact(buf, n, K, sh);
@@ -478,10 +487,7 @@ template <>
 struct Raw8<bf16_t> {
   u32x4 a;
   __device__ __forceinline__ void load(const bf16_t* p) { a = *reinterpret_cast<const u32x4*>(p); }
-  __device__ __forceinline__ void take(bool c, const Raw8& o) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] = c ? (uint32_t)o.a[i] : (uint32_t)a[i];
-  }
+  __device__ __forceinline__ void clear() { a = u32x4{0, 0, 0, 0}; }
   __device__ __forceinline__ void from(const float* f) {
     a = u32x4{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])};
   }
@@ -502,10 +508,7 @@ struct Raw8<float> {
     a[0] = reinterpret_cast<const f32x4*>(p)[0];
     a[1] = reinterpret_cast<const f32x4*>(p)[1];
   }
-  __device__ __forceinline__ void take(bool c, const Raw8& o) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) a[i >> 2][i & 3] = c ? (float)o.a[i >> 2][i & 3] : (float)a[i >> 2][i & 3];
-  }
+  __device__ __forceinline__ void clear() { a[0] = a[1] = f32x4{0.f, 0.f, 0.f, 0.f}; }
   __device__ __forceinline__ void from(const float* f) {
     a[0] = f32x4{f[0], f[1], f[2], f[3]};
     a[1] = f32x4{f[4], f[5], f[6], f[7]};
@@ -530,7 +533,8 @@ __global__ __launch_bounds__(kTopkThreads) void topk_rows_kernel(const T* __rest
                                                                  float2* __restrict__ state) {
   __shared__ __attribute__((aligned(16))) uint64_t buf[CAP];
   __shared__ TopkShared sh;
-  const int tid = threadIdx.x;
+  __shared__ uint32_t lists[kTopkThreads / 64][kTopkList];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t row = blockIdx.x / segments;
   const int seg = (int)(blockIdx.x - row * segments);
   if (mask != nullptr && mask[row] == 0) {
@@ -546,12 +550,10 @@ __global__ __launch_bounds__(kTopkThreads) void topk_rows_kernel(const T* __rest
   const int hi = (lo + seg_cols < V + shift) ? lo + seg_cols : V + shift;
   const int mid_limit = K + K / 4 + 64;  // what a cut on the way may leave: at most CAP - kTopkStep
   const int cut_at = 2 * mid_limit < CAP - 1024 ? 2 * mid_limit : CAP - 1024;
-  uint32_t after = 0;
 
   const int end = row + 1 < rows ? V + shift + 8 : V + shift;  // columns that can be read
-  // Vector u of a tile, with -infinity outside [first, hi).
-  auto fetch = [&](int t0, int u) {
-    const int j = t0 + u * kTopkStep + tid * 8;
+  // The vector at shifted column j, with -infinity outside [first, hi).
+  auto fetch = [&](int j) {
     Raw8<T> r;
     if (j + 8 <= hi && j >= first) {
       r.load(base + j);
@@ -592,30 +594,20 @@ __global__ __launch_bounds__(kTopkThreads) void topk_rows_kernel(const T* __rest
     }
     return hits;
   };
-  auto append = [&](const Raw8<T>& r, int j) {
-    int hits = wanted(r, j);
-    if (!__ballot(hits)) return;
-    int at = topk_place(__popc(hits), sh);
-    while (hits) {
-      const int i = __ffs(hits) - 1;
-      hits &= hits - 1;
-      if (at < CAP) buf[at] = ((uint64_t)order_key(r.pick(i)) << 32) | ~(uint32_t)(j - shift + i);
-      ++at;
-    }
-  };
 
   if (tid == 0) sh.count = 0;
   Raw8<T> raw[kTopkVecs], next[kTopkVecs];
   // sum of 2^(x log2 e + neg), neg = -m log2 e rounded, for a reference m
   float m = -INFINITY, neg = 0.f, s = 0.f;
-  int n = 0;
+  int n = 0, listed = 0, side = 0;
+  uint32_t after = 0;  // what is wanted at least once all lists are read
   for (int t0 = lo - kTopkTile; t0 < hi; t0 += kTopkTile) {
-    if (t0 + kTopkTile < hi) {
+    const bool last = t0 + kTopkTile >= hi;
+    if (!last) {
 #pragma unroll
-      for (int u = 0; u < kTopkVecs; ++u) next[u] = fetch(t0 + kTopkTile, u);
+      for (int u = 0; u < kTopkVecs; ++u) next[u] = fetch(t0 + kTopkTile + u * kTopkStep + tid * 8);
     }
     if (t0 >= lo) {
-      uint32_t hot = 0;  // vectors in which some lane of the wave has something wanted
 #pragma unroll
       for (int u = 0; u < kTopkVecs; ++u) {
         float vm = raw[u].get(0), sum = 0.f;
@@ -639,49 +631,61 @@ __global__ __launch_bounds__(kTopkThreads) void topk_rows_kernel(const T* __rest
         }
         s += sum;
         // (NaN: fmaxf passes it over, the sum does not)
-        if (__ballot(!(vm < need_value) || sum != sum)) hot |= 1u << u;
-      }
-      auto vec = [&](int u) {
-        Raw8<T> r = raw[0];
-#pragma unroll
-        for (int k = 1; k < kTopkVecs; ++k) r.take(u == k, raw[k]);
-        return r;
-      };
-#pragma unroll 1
-      for (int u = 0; u < kTopkVecs; ++u)
-        if (hot & (1u << u)) append(vec(u), t0 + u * kTopkStep + tid * 8);
-      __syncthreads();
-      const int now = (int)sh.count;
-      __syncthreads();
-      // Words above the key come at a rate that the key's age sets: the buffer
-      // is cut when it holds twice what a cut leaves.  Where not all fitted,
-      // the tile is taken once more, a vector (2048 consecutive columns) at a
-      // time, with room made for each.
-      const bool again = now > CAP;
-      if (again) {
-        if (tid == 0) sh.count = (uint32_t)n;
-        __syncthreads();
-      } else {
-        n = now;
-        need = after > need ? after : need;
-      }
-#pragma unroll 1
-      for (int u = 0; u < (again ? kTopkVecs : 1); ++u) {
-        if (n > (again ? CAP - kTopkStep : cut_at) && (again || t0 + kTopkTile < hi)) {
-          uint32_t key;
-          n = topk_cut(buf, n, K, mid_limit, need > 0 ? need - 1 : 0, sh, &key);
-          need = key + 1 > need ? key + 1 : need;
-          need_value = key_value(need);
+        const bool hot = !(vm < need_value) || sum != sum;
+        const uint64_t who = __ballot(hot);
+        if (who) {
+          if (hot)
+            lists[wave][listed + __builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32),
+                                                           __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0))] =
+                (uint32_t)((t0 + u * kTopkStep) / 8 + tid);
+          listed += __popcll(who);
         }
-        if (again) {
-          append(vec(u), t0 + u * kTopkStep + tid * 8);
+      }
+      if (lane == 0) sh.pending[side][wave] = (uint32_t)listed;
+      __syncthreads();  // (the other side is written only after everyone has passed the next barrier)
+      uint32_t most = 0;
+#pragma unroll
+      for (int w = 0; w < kTopkThreads / 64; ++w) most = sh.pending[side][w] > most ? sh.pending[side][w] : most;
+      side ^= 1;
+      if (most > kTopkList - 64 * kTopkVecs || last) {
+        uint32_t key;
+#pragma unroll 1
+        for (int i0 = 0; i0 < (int)most; i0 += 64) {
+          if (n > CAP - kTopkStep) {
+            // (elements with this very key may still be on the lists with lower indices)
+            n = topk_cut(buf, n, K, mid_limit, sh, &key);
+            need = key > need ? key : need;
+            after = key + 1 > after ? key + 1 : after;
+            need_value = key_value(need);
+          }
+          int hits = 0, j = 0;
+          Raw8<T> r;
+          r.clear();
+          if (i0 + lane < listed) {
+            j = (int)lists[wave][i0 + lane] * 8;
+            r = fetch(j);
+            hits = wanted(r, j);
+          }
+          int at = topk_place(__popc(hits), sh);
+          while (hits) {
+            const int i = __ffs(hits) - 1;
+            hits &= hits - 1;
+            buf[at++] = ((uint64_t)order_key(r.pick(i)) << 32) | ~(uint32_t)(j - shift + i);
+          }
           __syncthreads();
           n = (int)sh.count;
           __syncthreads();
         }
+        listed = 0;
+        // words above the key come at a rate that the key's age sets: the
+        // buffer is cut when it holds twice what a cut leaves
+        if (n > cut_at && !last) {
+          n = topk_cut(buf, n, K, mid_limit, sh, &key);
+          after = key + 1 > after ? key + 1 : after;
+        }
+        need = after > need ? after : need;
+        need_value = key_value(need);
       }
-      need = after > need ? after : need;
-      need_value = key_value(need);
     }
 #pragma unroll
     for (int u = 0; u < kTopkVecs; ++u) raw[u] = next[u];
@@ -726,7 +730,7 @@ __global__ __launch_bounds__(kTopkThreads) void topk_rows_kernel(const T* __rest
   const int limit = segments == 1 ? topk_sort_limit(K) : topk_slots(K);
   if (n > limit) {
     uint32_t key;
-    n = topk_cut(buf, n, K, limit, need > 0 ? need - 1 : 0, sh, &key);
+    n = topk_cut(buf, n, K, limit, sh, &key);
   }
   topk_reduce_state(m, s, sh);
   if (segments == 1) {
@@ -766,7 +770,7 @@ __global__ __launch_bounds__(kTopkThreads) void topk_merge_kernel(const uint64_t
     if (n > CAP - kTopkStep) {
       // (the words of a segment are in no order, so one with this very key may
       // still come with a lower index)
-      n = topk_cut(buf, n, K, K + K / 4 + 64, need, sh, &need);
+      n = topk_cut(buf, n, K, K + K / 4 + 64, sh, &need);
     }
     uint64_t w[8];
     int hits = 0;
@@ -784,7 +788,7 @@ __global__ __launch_bounds__(kTopkThreads) void topk_merge_kernel(const uint64_t
     n = (int)sh.count;
     __syncthreads();
   }
-  if (n > topk_sort_limit(K)) n = topk_cut(buf, n, K, topk_sort_limit(K), need, sh, &key);
+  if (n > topk_sort_limit(K)) n = topk_cut(buf, n, K, topk_sort_limit(K), sh, &key);
   float m = -INFINITY, s = 0.f;
   for (int i = tid; i < segments; i += kTopkThreads) {
     const float2 st = state[row * segments + i];
