@@ -142,6 +142,7 @@ struct TopkShared {
   uint32_t pending[2][4];
   float wave_m[4], wave_s[4];
   uint32_t count, sel, need, bin;
+  uint32_t start[257];
 };
 
 // Places for a lane's `mine` words behind those in the buffer: one addition to
@@ -309,23 +310,6 @@ __device__ __forceinline__ int topk_cut(uint64_t* buf, int n, int K, int limit, 
   return kept;
 }
 
-// Descending order of the n words in buf, by the place a word has among them:
-// the words that are larger, counted.  For n up to kTopkThreads.
-__device__ __forceinline__ void topk_sort_by_rank(uint64_t* buf, int n) {
-  const int tid = threadIdx.x;
-  const uint64_t mine = tid < n ? buf[tid] : 0;
-  if (tid >= n && tid < ((n + 7) & ~7)) buf[tid] = 0;  // (no word is zero)
-  __syncthreads();
-  int rank = 0;
-  for (int i = 0; i < n; i += 8) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) rank += buf[i + k] > mine ? 1 : 0;
-  }
-  __syncthreads();
-  if (tid < n) buf[rank] = mine;
-  __syncthreads();
-}
-
 // The value of lane ^ LANES.
 template <int LANES>
 __device__ __forceinline__ uint32_t lane_xor(uint32_t x) {
@@ -407,24 +391,6 @@ __device__ __forceinline__ void topk_sort_bitonic(uint64_t* buf, int n) {
   __syncthreads();
 }
 
-// (a buffer of 4096 words serves K up to 1024, whose sort takes at most 2048)
-template <int CAP>
-__device__ __forceinline__ void topk_sort(uint64_t* buf, int n) {
-  if (CAP <= 4096 && n <= kTopkThreads)
-    topk_sort_by_rank(buf, n);
-  else if (CAP <= 4096 || n <= 2048)
-    topk_sort_bitonic<8>(buf, n);
-  else
-    topk_sort_bitonic<CAP / kTopkThreads>(buf, n);
-}
-
-// Words that the final sort takes without a cut before it: what the sort that K
-// and an eighth of it need holds.
-__device__ __forceinline__ int topk_sort_limit(int K) {
-  const int k = K + K / 8;
-  return k <= 256 ? 256 : k <= 2048 ? 2048 : 8192;
-}
-
 // Merge of two (reference m, sum of exp(x - m)) states.
 __device__ __forceinline__ void exp_merge(float& m, float& s, float m2, float s2) {
   const float mn = fmaxf(m, m2);
@@ -453,23 +419,82 @@ __device__ __forceinline__ void topk_reduce_state(float& m, float& s, TopkShared
   for (int w = 1; w < 4; ++w) exp_merge(m, s, sh.wave_m[w], sh.wave_s[w]);
 }
 
-// The sorted words of a row and its state, as the row's results.
-__device__ __forceinline__ void topk_write(const uint64_t* buf, int K, float m, float s, int logprob, int* idx, float* val,
-                           float* lse) {
-  const float top = key_value((uint32_t)(buf[0] >> 32));
-  float l;
-  if (top != top || top == INFINITY || top == -INFINITY)
-    l = top;  // a NaN anywhere in the row comes first, then an infinity
-  else
-    l = m + logf(s);
-  for (int k = threadIdx.x; k < K; k += kTopkThreads) {
-    const uint64_t c = buf[k];
-    float v = key_value((uint32_t)(c >> 32));
-    if (logprob && v != -INFINITY) v -= l;  // a logit of -inf has log-probability -inf in every row
-    idx[k] = (int)~(uint32_t)c;
-    val[k] = v;
+// The K largest of a row's n words in order, and its state, as the row's
+// results.  The words are put in order by counting: 256 bins over the range of
+// their keys, then in its bin a word's place is the number of larger words
+// there; `order` lists the words bin by bin.  Where a bin that matters holds
+// more than 64 words (keys that are mostly equal, or a far outlier), or K is
+// beyond what `order` holds, a bitonic sort does it.  (301 rows of 50021 fp32
+// logits, K = 1000: a cut and a bitonic sort of 1024 words 28 us of the call,
+// this 6.)
+template <int CAP>
+__device__ __forceinline__ void topk_finish(uint64_t* buf, uint16_t* order, int order_cap, int n, int K, float m,
+                                            float s, int logprob, int* idx, float* val, float* lse, TopkShared& sh) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  constexpr int limit = CAP <= 4096 ? 2048 : CAP;
+  const int most_words = K <= order_cap / 2 ? order_cap : limit;
+  uint32_t key;
+  if (n > most_words) n = topk_cut(buf, n, K, most_words, sh, &key);
+  __syncthreads();
+  sh.hist[tid] = 0;
+  if (tid == 0) sh.bin = 0;
+  const uint32_t* keys = reinterpret_cast<const uint32_t*>(buf) + 1;
+  uint32_t least = ~0u, most = 0;
+#pragma unroll 4
+  for (int i = tid; i < n; i += kTopkThreads) {
+    const uint32_t k = keys[2 * i];
+    most = k > most ? k : most;
+    least = k < least ? k : least;
   }
-  if (threadIdx.x == 0) *lse = l;
+  topk_range(least, most, sh);
+  const float top = key_value(most);
+  // a NaN anywhere in the row comes first, then an infinity
+  const float l = (top != top || top == INFINITY || top == -INFINITY) ? top : m + logf(s);
+  if (tid == 0) *lse = l;
+  auto put = [&](int place, uint64_t word) {
+    float v = key_value((uint32_t)(word >> 32));
+    if (logprob && v != -INFINITY) v -= l;  // a logit of -inf has log-probability -inf in every row
+    idx[place] = (int)~(uint32_t)word;
+    val[place] = v;
+  };
+  const int bits = 32 - __clz((int)((most - least) | 1)), shift = bits > 8 ? bits - 8 : 0;
+  if (n <= order_cap) {
+#pragma unroll 4
+    for (int i = tid; i < n; i += kTopkThreads) atomicAdd(&sh.hist[(most - keys[2 * i]) >> shift], 1u);
+    __syncthreads();
+    const uint32_t own = sh.hist[tid];
+    const uint32_t inc = (uint32_t)wave_scan((int)own);
+    if (lane == 63) sh.wave_n[wave] = inc;
+    __syncthreads();
+    uint32_t at = inc - own;
+    for (int w = 0; w < wave; ++w) at += sh.wave_n[w];
+    sh.start[tid] = at;
+    sh.hist[tid] = at;  // the bin's next place
+    if (tid == kTopkThreads - 1) sh.start[kTopkThreads] = (uint32_t)n;
+    if (own > 64 && at < (uint32_t)K) sh.bin = 1;
+    __syncthreads();
+  }
+  if (n > order_cap || sh.bin) {
+    if (n > limit) n = topk_cut(buf, n, K, limit, sh, &key);
+    if (n <= 2048)
+      topk_sort_bitonic<8>(buf, n);
+    else
+      topk_sort_bitonic<limit / kTopkThreads>(buf, n);
+    for (int k = tid; k < K; k += kTopkThreads) put(k, buf[k]);
+    return;
+  }
+  for (int i = tid; i < n; i += kTopkThreads)
+    order[atomicAdd(&sh.hist[(most - keys[2 * i]) >> shift], 1u)] = (uint16_t)i;
+  __syncthreads();
+  for (int i = tid; i < n; i += kTopkThreads) {
+    const uint64_t word = buf[i];
+    const uint32_t b = (most - (uint32_t)(word >> 32)) >> shift;
+    const uint32_t from = sh.start[b], to = sh.start[b + 1];
+    if (from >= (uint32_t)K) continue;
+    uint32_t p = from;
+    for (uint32_t j = from; j < to; ++j) p += buf[order[j]] > word ? 1 : 0;
+    if (p < (uint32_t)K) put((int)p, word);
+  }
 }
 
 __device__ __forceinline__ void topk_masked_row(int K, int* idx, float* val, float* lse) {
@@ -525,7 +550,7 @@ struct Raw8<float> {
 __host__ __device__ inline int topk_slots(int K) { return K + K / 8 + 32; }
 
 template <typename T, int CAP>
-__global__ __launch_bounds__(kTopkThreads) void topk_rows_kernel(const T* __restrict__ logits, int64_t rows, int V, int K,
+__global__ __launch_bounds__(kTopkThreads, CAP <= 4096 ? 4 : 2) void topk_rows_kernel(const T* __restrict__ logits, int64_t rows, int V, int K,
                                                                  int segments, int seg_cols, int logprob,
                                                                  const uint8_t* __restrict__ mask,
                                                                  int* __restrict__ idx, float* __restrict__ val,
@@ -595,7 +620,6 @@ __global__ __launch_bounds__(kTopkThreads) void topk_rows_kernel(const T* __rest
     return hits;
   };
 
-  if (tid == 0) sh.count = 0;
   Raw8<T> raw[kTopkVecs], next[kTopkVecs];
   // sum of 2^(x log2 e + neg), neg = -m log2 e rounded, for a reference m
   float m = -INFINITY, neg = 0.f, s = 0.f;
@@ -651,13 +675,6 @@ __global__ __launch_bounds__(kTopkThreads) void topk_rows_kernel(const T* __rest
         uint32_t key;
 #pragma unroll 1
         for (int i0 = 0; i0 < (int)most; i0 += 64) {
-          if (n > CAP - kTopkStep) {
-            // (elements with this very key may still be on the lists with lower indices)
-            n = topk_cut(buf, n, K, mid_limit, sh, &key);
-            need = key > need ? key : need;
-            after = key + 1 > after ? key + 1 : after;
-            need_value = key_value(need);
-          }
           int hits = 0, j = 0;
           Raw8<T> r;
           r.clear();
@@ -666,15 +683,32 @@ __global__ __launch_bounds__(kTopkThreads) void topk_rows_kernel(const T* __rest
             r = fetch(j);
             hits = wanted(r, j);
           }
-          int at = topk_place(__popc(hits), sh);
+          int inc = wave_scan(__popc(hits));
+          if (lane == 63) sh.pending[side][wave] = (uint32_t)inc;
+          __syncthreads();
+          int at = n + inc - __popc(hits), all = 0;
+#pragma unroll
+          for (int w = 0; w < kTopkThreads / 64; ++w) {
+            const int c = (int)sh.pending[side][w];
+            all += c;
+            at += w < wave ? c : 0;
+          }
+          side ^= 1;
+          if (n + all > CAP) {
+            // (elements with this very key may still be on the lists with lower indices)
+            const int before = n;
+            n = topk_cut(buf, n, K, mid_limit, sh, &key);
+            at -= before - n;
+            need = key > need ? key : need;
+            after = key + 1 > after ? key + 1 : after;
+            need_value = key_value(need);
+          }
+          n += all;
           while (hits) {
             const int i = __ffs(hits) - 1;
             hits &= hits - 1;
             buf[at++] = ((uint64_t)order_key(r.pick(i)) << 32) | ~(uint32_t)(j - shift + i);
           }
-          __syncthreads();
-          n = (int)sh.count;
-          __syncthreads();
         }
         listed = 0;
         // words above the key come at a rate that the key's age sets: the
@@ -727,25 +761,26 @@ __global__ __launch_bounds__(kTopkThreads) void topk_rows_kernel(const T* __rest
     }
   }
   if (fabsf(neg) < 1e30f && m > -INFINITY) s *= fast_exp2(-fmaf(m, kLog2e, neg));  // the rounding of neg
-  const int limit = segments == 1 ? topk_sort_limit(K) : topk_slots(K);
-  if (n > limit) {
-    uint32_t key;
-    n = topk_cut(buf, n, K, limit, sh, &key);
-  }
   topk_reduce_state(m, s, sh);
   if (segments == 1) {
-    topk_sort<CAP>(buf, n);
-    topk_write(buf, K, m, s, logprob, idx + row * K, val + row * K, lse + row);
+    topk_finish<CAP>(buf, reinterpret_cast<uint16_t*>(lists), (int)(sizeof(lists) / 2), n, K, m, s, logprob,
+                     idx + row * K, val + row * K, lse + row, sh);
   } else {
-    uint64_t* c = cand + (int64_t)blockIdx.x * limit;
-    for (int k = tid; k < limit; k += kTopkThreads) c[k] = k < n ? buf[k] : 0;
+    const int slots = topk_slots(K);
+    if (n > slots) {
+      uint32_t key;
+      n = topk_cut(buf, n, K, slots, sh, &key);
+    }
+    __syncthreads();
+    uint64_t* c = cand + (int64_t)blockIdx.x * slots;
+    for (int k = tid; k < slots; k += kTopkThreads) c[k] = k < n ? buf[k] : 0;
     if (tid == 0) state[blockIdx.x] = make_float2(m, s);
   }
 }
 
 // The segments' words of a row, cut and sorted in the same way.
 template <int CAP>
-__global__ __launch_bounds__(kTopkThreads) void topk_merge_kernel(const uint64_t* __restrict__ cand,
+__global__ __launch_bounds__(kTopkThreads, CAP <= 4096 ? 4 : 2) void topk_merge_kernel(const uint64_t* __restrict__ cand,
                                                                   const float2* __restrict__ state, int K,
                                                                   int segments, int logprob,
                                                                   const uint8_t* __restrict__ mask,
@@ -753,6 +788,7 @@ __global__ __launch_bounds__(kTopkThreads) void topk_merge_kernel(const uint64_t
                                                                   float* __restrict__ lse) {
   __shared__ __attribute__((aligned(16))) uint64_t buf[CAP];
   __shared__ TopkShared sh;
+  __shared__ uint16_t order[CAP];
   const int tid = threadIdx.x;
   const int64_t row = blockIdx.x;
   if (mask != nullptr && mask[row] == 0) {
@@ -764,7 +800,6 @@ __global__ __launch_bounds__(kTopkThreads) void topk_merge_kernel(const uint64_t
   if (tid == 0) sh.count = 0;
   __syncthreads();
   uint32_t need = 1;  // (empty slots are zero)
-  uint32_t key;
   int n = 0;
   for (int t0 = 0; t0 < total; t0 += kTopkStep) {
     if (n > CAP - kTopkStep) {
@@ -788,15 +823,13 @@ __global__ __launch_bounds__(kTopkThreads) void topk_merge_kernel(const uint64_t
     n = (int)sh.count;
     __syncthreads();
   }
-  if (n > topk_sort_limit(K)) n = topk_cut(buf, n, K, topk_sort_limit(K), sh, &key);
   float m = -INFINITY, s = 0.f;
   for (int i = tid; i < segments; i += kTopkThreads) {
     const float2 st = state[row * segments + i];
     exp_merge(m, s, st.x, st.y);
   }
   topk_reduce_state(m, s, sh);
-  topk_sort<CAP>(buf, n);
-  topk_write(buf, K, m, s, logprob, idx + row * K, val + row * K, lse + row);
+  topk_finish<CAP>(buf, order, CAP, n, K, m, s, logprob, idx + row * K, val + row * K, lse + row, sh);
 }
 
 // ---------------------------------------------------------------- embedding --
@@ -1352,14 +1385,26 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 }  // namespace
 
 // -------------------------------------------------------------- launchers --
-// Rows are cut into segments (whole tiles) where there are too few of them for
-// three workgroups on each of the 256 compute units.
+// Segments of whole tiles to a row: as many as make the call shortest when a
+// workgroup takes 2 us a tile by itself, all of them together read 5 bytes a
+// picosecond, and joining segments costs 8 us.  (us at bf16, K = 100: 300 rows
+// of 201088 in 1 / 3 segments 59 / 49; 500 rows of 32000 in 1 / 2 21 / 26; 700
+// rows of 100000 73 / 95.)
 void topk_plan(int64_t rows, int64_t V, int* segments, int64_t* seg_cols) {
   const int64_t tiles = cdiv(V + 7, kTopkTile);
-  const int64_t want = std::max<int64_t>(1, std::min<int64_t>({cdiv(768, std::max<int64_t>(rows, 1)), tiles, 64}));
-  const int64_t per = cdiv(tiles, want);
-  *seg_cols = per * kTopkTile;
-  *segments = (int)cdiv(tiles, per);
+  const double read_us = (double)rows * V * 2 / 5e6;
+  double best = 0;
+  *seg_cols = 0;
+  for (int64_t want = 1; want <= std::min<int64_t>(tiles, 64); ++want) {
+    const int64_t per = cdiv(tiles, want);
+    if (cdiv(tiles, per) != want) continue;  // the same as fewer
+    const double us = std::max(read_us, 2.0 * per) + (want > 1 ? 8.0 : 0.0);
+    if (*seg_cols == 0 || us < best) {
+      best = us;
+      *seg_cols = per * kTopkTile;
+      *segments = (int)want;
+    }
+  }
 }
 int64_t topk_segment_words(int64_t K) { return topk_slots((int)K); }
 
