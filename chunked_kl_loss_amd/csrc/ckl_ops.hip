@@ -270,6 +270,7 @@ __device__ __forceinline__ void topk_cut_exact(uint64_t* buf, int n, int K, Topk
 // Cuts the n > limit >= K words of buf to at most `limit` of the largest, at
 // least K, in any order.  Returns their number and sets *key to a key that at least K of them,
 // and none less, reach.  Begins and ends with a barrier.
+template <int CAP>
 __device__ __forceinline__ int topk_cut(uint64_t* buf, int n, int K, int limit, TopkShared& sh,
                                         uint32_t* key) {
   const int tid = threadIdx.x;
@@ -295,17 +296,24 @@ __device__ __forceinline__ int topk_cut(uint64_t* buf, int n, int K, int limit, 
     topk_cut_exact(buf, n, K, sh);
     return K;
   }
-  __syncthreads();
-  if (tid == 0) sh.count = 0;
-  // in place: the words kept so far never reach past the words read so far
-  for (int i0 = 0; i0 < n; i0 += kTopkThreads) {
-    const int i = i0 + tid;
-    const uint64_t c = i < n ? buf[i] : 0;
-    __syncthreads();
-    const bool keep = i < n && (uint32_t)(c >> 32) >= t;
-    const int at = topk_place(keep ? 1 : 0, sh);
-    if (keep) buf[at] = c;
+  constexpr int W = CAP / kTopkThreads;
+  const int lane = tid & 63, wave = tid >> 6;
+  uint64_t c[W];
+  int mine = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    c[w] = w * kTopkThreads + tid < n ? buf[w * kTopkThreads + tid] : 0;
+    mine += (uint32_t)(c[w] >> 32) >= t ? 1 : 0;
   }
+  const int inc = wave_scan(mine);
+  if (lane == 63) sh.wave_n[wave] = (uint32_t)inc;
+  __syncthreads();  // also: all words have been read
+  int at = inc - mine;
+  for (int w = 0; w < wave; ++w) at += (int)sh.wave_n[w];
+#pragma unroll
+  for (int w = 0; w < W; ++w)
+    if ((uint32_t)(c[w] >> 32) >= t) buf[at++] = c[w];
+  if (tid == 0) sh.count = (uint32_t)kept;
   __syncthreads();
   return kept;
 }
@@ -420,21 +428,18 @@ __device__ __forceinline__ void topk_reduce_state(float& m, float& s, TopkShared
 }
 
 // The K largest of a row's n words in order, and its state, as the row's
-// results.  The words are put in order by counting: 256 bins over the range of
-// their keys, then in its bin a word's place is the number of larger words
-// there; `order` lists the words bin by bin.  Where a bin that matters holds
-// more than 64 words (keys that are mostly equal, or a far outlier), or K is
-// beyond what `order` holds, a bitonic sort does it.  (301 rows of 50021 fp32
-// logits, K = 1000: a cut and a bitonic sort of 1024 words 28 us of the call,
-// this 6.)
+// results.  K up to 1024 (CAP = 4096): the words are put into 256 bins over the
+// range of their keys, and in its bin a word's place is the number of larger
+// words there.  Where a bin that matters holds more than 64 words (keys that are
+// mostly equal, or a far outlier), and for larger K, a bitonic sort does it.
 template <int CAP>
-__device__ __forceinline__ void topk_finish(uint64_t* buf, uint16_t* order, int order_cap, int n, int K, float m,
-                                            float s, int logprob, int* idx, float* val, float* lse, TopkShared& sh) {
+__device__ __forceinline__ void topk_finish(uint64_t* buf, int n, int K, float m, float s, int logprob, int* idx,
+                                            float* val, float* lse, TopkShared& sh) {
+  constexpr bool bins = CAP <= 4096;
+  constexpr int W = bins ? 10 : CAP / kTopkThreads, limit = W * kTopkThreads;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  constexpr int limit = CAP <= 4096 ? 2048 : CAP;
-  const int most_words = K <= order_cap / 2 ? order_cap : limit;
   uint32_t key;
-  if (n > most_words) n = topk_cut(buf, n, K, most_words, sh, &key);
+  if (n > limit) n = topk_cut<CAP>(buf, n, K, limit, sh, &key);
   __syncthreads();
   sh.hist[tid] = 0;
   if (tid == 0) sh.bin = 0;
@@ -457,8 +462,8 @@ __device__ __forceinline__ void topk_finish(uint64_t* buf, uint16_t* order, int 
     idx[place] = (int)~(uint32_t)word;
     val[place] = v;
   };
-  const int bits = 32 - __clz((int)((most - least) | 1)), shift = bits > 8 ? bits - 8 : 0;
-  if (n <= order_cap) {
+  if constexpr (bins) {
+    const int bits = 32 - __clz((int)((most - least) | 1)), shift = bits > 8 ? bits - 8 : 0;
 #pragma unroll 4
     for (int i = tid; i < n; i += kTopkThreads) atomicAdd(&sh.hist[(most - keys[2 * i]) >> shift], 1u);
     __syncthreads();
@@ -472,29 +477,40 @@ __device__ __forceinline__ void topk_finish(uint64_t* buf, uint16_t* order, int 
     sh.hist[tid] = at;  // the bin's next place
     if (tid == kTopkThreads - 1) sh.start[kTopkThreads] = (uint32_t)n;
     if (own > 64 && at < (uint32_t)K) sh.bin = 1;
+    uint64_t x[W];
+#pragma unroll
+    for (int w = 0; w < W; ++w) x[w] = w * kTopkThreads + tid < n ? buf[w * kTopkThreads + tid] : 0;
     __syncthreads();
+    if (!sh.bin) {
+#pragma unroll
+      for (int w = 0; w < W; ++w)
+        if (w * kTopkThreads + tid < n) buf[atomicAdd(&sh.hist[(most - (uint32_t)(x[w] >> 32)) >> shift], 1u)] = x[w];
+      if (tid < 4) buf[n + tid] = 0;
+      __syncthreads();
+#pragma unroll 1
+      for (int i = tid; i < n; i += kTopkThreads) {
+        const uint64_t word = buf[i];
+        const uint32_t b = (most - (uint32_t)(word >> 32)) >> shift;
+        const int from = (int)sh.start[b], to = (int)sh.start[b + 1];
+        if (from >= K) break;  // (the words lie bin by bin)
+        int p = from;
+#pragma unroll 1
+        for (int j = from; j < to; j += 4) {  // (what lies behind the bin is smaller)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) p += buf[j + k] > word ? 1 : 0;
+        }
+        if (p < K) put(p, word);
+      }
+      return;
+    }
+    if (n > 2048) n = topk_cut<CAP>(buf, n, K, 2048, sh, &key);
+    topk_sort_bitonic<8>(buf, n);
+  } else if (n <= 2048) {
+    topk_sort_bitonic<8>(buf, n);
+  } else {
+    topk_sort_bitonic<W>(buf, n);
   }
-  if (n > order_cap || sh.bin) {
-    if (n > limit) n = topk_cut(buf, n, K, limit, sh, &key);
-    if (n <= 2048)
-      topk_sort_bitonic<8>(buf, n);
-    else
-      topk_sort_bitonic<limit / kTopkThreads>(buf, n);
-    for (int k = tid; k < K; k += kTopkThreads) put(k, buf[k]);
-    return;
-  }
-  for (int i = tid; i < n; i += kTopkThreads)
-    order[atomicAdd(&sh.hist[(most - keys[2 * i]) >> shift], 1u)] = (uint16_t)i;
-  __syncthreads();
-  for (int i = tid; i < n; i += kTopkThreads) {
-    const uint64_t word = buf[i];
-    const uint32_t b = (most - (uint32_t)(word >> 32)) >> shift;
-    const uint32_t from = sh.start[b], to = sh.start[b + 1];
-    if (from >= (uint32_t)K) continue;
-    uint32_t p = from;
-    for (uint32_t j = from; j < to; ++j) p += buf[order[j]] > word ? 1 : 0;
-    if (p < (uint32_t)K) put((int)p, word);
-  }
+  for (int k = tid; k < K; k += kTopkThreads) put(k, buf[k]);
 }
 
 __device__ __forceinline__ void topk_masked_row(int K, int* idx, float* val, float* lse) {
@@ -697,7 +713,7 @@ __global__ __launch_bounds__(kTopkThreads, CAP <= 4096 ? 4 : 2) void topk_rows_k
           if (n + all > CAP) {
             // (elements with this very key may still be on the lists with lower indices)
             const int before = n;
-            n = topk_cut(buf, n, K, mid_limit, sh, &key);
+            n = topk_cut<CAP>(buf, n, K, mid_limit, sh, &key);
             at -= before - n;
             need = key > need ? key : need;
             after = key + 1 > after ? key + 1 : after;
@@ -714,7 +730,7 @@ __global__ __launch_bounds__(kTopkThreads, CAP <= 4096 ? 4 : 2) void topk_rows_k
         // words above the key come at a rate that the key's age sets: the
         // buffer is cut when it holds twice what a cut leaves
         if (n > cut_at && !last) {
-          n = topk_cut(buf, n, K, mid_limit, sh, &key);
+          n = topk_cut<CAP>(buf, n, K, mid_limit, sh, &key);
           after = key + 1 > after ? key + 1 : after;
         }
         need = after > need ? after : need;
@@ -763,13 +779,12 @@ __global__ __launch_bounds__(kTopkThreads, CAP <= 4096 ? 4 : 2) void topk_rows_k
   if (fabsf(neg) < 1e30f && m > -INFINITY) s *= fast_exp2(-fmaf(m, kLog2e, neg));  // the rounding of neg
   topk_reduce_state(m, s, sh);
   if (segments == 1) {
-    topk_finish<CAP>(buf, reinterpret_cast<uint16_t*>(lists), (int)(sizeof(lists) / 2), n, K, m, s, logprob,
-                     idx + row * K, val + row * K, lse + row, sh);
+    topk_finish<CAP>(buf, n, K, m, s, logprob, idx + row * K, val + row * K, lse + row, sh);
   } else {
     const int slots = topk_slots(K);
     if (n > slots) {
       uint32_t key;
-      n = topk_cut(buf, n, K, slots, sh, &key);
+      n = topk_cut<CAP>(buf, n, K, slots, sh, &key);
     }
     __syncthreads();
     uint64_t* c = cand + (int64_t)blockIdx.x * slots;
@@ -788,7 +803,6 @@ __global__ __launch_bounds__(kTopkThreads, CAP <= 4096 ? 4 : 2) void topk_merge_
                                                                   float* __restrict__ lse) {
   __shared__ __attribute__((aligned(16))) uint64_t buf[CAP];
   __shared__ TopkShared sh;
-  __shared__ uint16_t order[CAP];
   const int tid = threadIdx.x;
   const int64_t row = blockIdx.x;
   if (mask != nullptr && mask[row] == 0) {
@@ -805,7 +819,7 @@ __global__ __launch_bounds__(kTopkThreads, CAP <= 4096 ? 4 : 2) void topk_merge_
     if (n > CAP - kTopkStep) {
       // (the words of a segment are in no order, so one with this very key may
       // still come with a lower index)
-      n = topk_cut(buf, n, K, K + K / 4 + 64, sh, &need);
+      n = topk_cut<CAP>(buf, n, K, K + K / 4 + 64, sh, &need);
     }
     uint64_t w[8];
     int hits = 0;
@@ -829,7 +843,7 @@ __global__ __launch_bounds__(kTopkThreads, CAP <= 4096 ? 4 : 2) void topk_merge_
     exp_merge(m, s, st.x, st.y);
   }
   topk_reduce_state(m, s, sh);
-  topk_finish<CAP>(buf, order, CAP, n, K, m, s, logprob, idx + row * K, val + row * K, lse + row, sh);
+  topk_finish<CAP>(buf, n, K, m, s, logprob, idx + row * K, val + row * K, lse + row, sh);
 }
 
 // ---------------------------------------------------------------- embedding --
