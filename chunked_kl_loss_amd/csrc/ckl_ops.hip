@@ -44,6 +44,16 @@ __device__ __forceinline__ void store4(bf16_t* p, f32x4 v) {
   *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
 }
 __device__ __forceinline__ void store4(float* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
+// The same without a place in the caches for what is written: for outputs larger
+// than they are (embedding of 32768 x 2880: 71 -> 56 us).
+__device__ __forceinline__ void stream8(bf16_t* p, const float* f) {
+  const u32x4 v = {pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])};
+  __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p));
+}
+__device__ __forceinline__ void stream8(float* p, const float* f) {
+  __builtin_nontemporal_store(f32x4{f[0], f[1], f[2], f[3]}, reinterpret_cast<f32x4*>(p));
+  __builtin_nontemporal_store(f32x4{f[4], f[5], f[6], f[7]}, reinterpret_cast<f32x4*>(p) + 1);
+}
 // A weight of either type, eight columns.
 __device__ __forceinline__ void load8_any(const void* p, int is_bf16, int64_t at, float* f) {
   if (is_bf16)
@@ -848,25 +858,33 @@ __global__ __launch_bounds__(kTopkThreads, CAP <= 4096 ? 4 : 2) void topk_merge_
 
 // ---------------------------------------------------------------- embedding --
 // out[t] = scale W[token_t - v_offset]; a zero row for a token outside the table.
+// A thread takes four vectors, their tokens and then their rows loaded together.
+constexpr int kEmbedUnits = 4;
 template <typename T, typename I>
 __global__ __launch_bounds__(256) void embedding_forward_kernel(const T* __restrict__ W, int64_t V, int64_t v_offset,
                                                                 const I* __restrict__ tokens, int64_t rows, Units q,
                                                                 float scale, T* __restrict__ out) {
-  const int64_t base = (int64_t)blockIdx.x * 1024;
+  const int64_t base = (int64_t)blockIdx.x * (256 * kEmbedUnits);
+  int64_t row[kEmbedUnits], v[kEmbedUnits];
+  uint32_t col[kEmbedUnits];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    int64_t row;
-    uint32_t col;
-    unit_at(q, base, k * 256 + threadIdx.x, &row, &col);
-    if (row >= rows) return;
-    const int64_t v = (int64_t)tokens[row] - v_offset;
-    float f[8] = {};
-    if (v >= 0 && v < V) {
-      load8(W + (v * q.n + col) * 8, f);
+  for (int k = 0; k < kEmbedUnits; ++k) {
+    unit_at(q, base, k * 256 + threadIdx.x, &row[k], &col[k]);
+    v[k] = row[k] < rows ? (int64_t)tokens[row[k]] - v_offset : -1;
+  }
+  float f[kEmbedUnits][8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] *= scale;
-    }
-    store8(out + (row * q.n + col) * 8, f);
+  for (int k = 0; k < kEmbedUnits; ++k) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[k][i] = 0.f;
+    if (v[k] >= 0 && v[k] < V) load8(W + (v[k] * q.n + col[k]) * 8, f[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < kEmbedUnits; ++k) {
+    const bool in = v[k] >= 0 && v[k] < V;  // (a zero row whatever the scale)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[k][i] = in ? f[k][i] * scale : 0.f;
+    if (row[k] < rows) stream8(out + (row[k] * q.n + col[k]) * 8, f[k]);
   }
 }
 
@@ -1101,53 +1119,53 @@ __global__ __launch_bounds__(256) void embedding_sum_kernel(const T* __restrict_
 }
 
 // The runs that cross borders: the listed chunk, where one begins, and the
-// chunks that it goes on through.  A workgroup takes 32 vectors of columns of
-// one run; eight slices share its chunks and are added in order, so the order
-// of the list does not matter.
+// chunks that it goes on through.  A workgroup takes 64 vectors of columns of
+// one run; four slices share its chunks and are added in order, so the order of
+// the list does not matter.
 template <typename G, bool ADD>
-__global__ __launch_bounds__(256) void embedding_join_kernel(const uint32_t* __restrict__ key, int64_t n, int chunk,
+__global__ __launch_bounds__(256) void embedding_join_kernel(const uint32_t* __restrict__ key, int chunk,
                                                              int64_t chunks, int nv, float scale, G* __restrict__ dW,
                                                              const float* __restrict__ part,
                                                              const uint32_t* __restrict__ joins) {
-  __shared__ float sums[8][32][9];
-  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
-  const int slabs = (nv + 31) / 32;
+  __shared__ float sums[3][64][9];
+  const int lane = threadIdx.x & 63, slice = threadIdx.x >> 6;
+  const int slabs = (nv + 63) / 64;
   const int64_t items = (int64_t)joins[0] * slabs;
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
     const int64_t c = joins[1 + it / slabs];
-    const int col = (int)(it % slabs) * 32 + lane;
+    const int col = (int)(it % slabs) * 64 + lane;
     const uint32_t k = key[(c + 1) * chunk];
-    // the chunks after c that begin with this token: [c + 1, end)
-    int64_t lo = c + 2, hi = chunks;
-    while (lo < hi) {
-      const int64_t mid = (lo + hi) >> 1;
-      if (key[mid * chunk] == k)
-        lo = mid + 1;
-      else
-        hi = mid;
+    G* dst = dW + ((int64_t)k * nv + col) * 8;
+    float sum[8] = {}, old[8] = {};
+    if (slice == 0 && col < nv) {
+      load8(part + ((2 * c + 1) * (int64_t)nv + col) * 8, sum);
+      if (ADD) load8(dst, old);
     }
-    float sum[8] = {};
-    if (col < nv) {
-      if (slice == 0) load8(part + ((2 * c + 1) * (int64_t)nv + col) * 8, sum);
+    // the chunks after c that begin with this token, 64 at a time
+    for (int64_t j0 = c + 1; j0 < chunks; j0 += 64) {
+      const uint64_t in = __ballot(j0 + lane < chunks && key[(j0 + lane) * chunk] == k);
+      const int m = in == ~(uint64_t)0 ? 64 : __builtin_ctzll(~in);
+      if (col < nv) {
 #pragma unroll 4
-      for (int64_t j = c + 1 + slice; j < lo; j += 8) {
-        float f[8];
-        load8(part + (2 * j * (int64_t)nv + col) * 8, f);
+        for (int j = slice; j < m; j += 4) {
+          float f[8];
+          load8(part + (2 * (j0 + j) * (int64_t)nv + col) * 8, f);
 #pragma unroll
-        for (int x = 0; x < 8; ++x) sum[x] += f[x];
+          for (int x = 0; x < 8; ++x) sum[x] += f[x];
+        }
       }
+      if (m < 64) break;
     }
+    if (slice > 0) {
 #pragma unroll
-    for (int x = 0; x < 8; ++x) sums[slice][lane][x] = sum[x];
+      for (int x = 0; x < 8; ++x) sums[slice - 1][lane][x] = sum[x];
+    }
     __syncthreads();
     if (slice == 0 && col < nv) {
 #pragma unroll
-      for (int s = 1; s < 8; ++s)
+      for (int s = 0; s < 3; ++s)
 #pragma unroll
         for (int x = 0; x < 8; ++x) sum[x] += sums[s][lane][x];
-      G* dst = dW + ((int64_t)k * nv + col) * 8;
-      float old[8] = {};
-      if (ADD) load8(dst, old);
 #pragma unroll
       for (int x = 0; x < 8; ++x) sum[x] = ADD ? old[x] + scale * sum[x] : scale * sum[x];
       store8(dst, sum);
@@ -1253,7 +1271,7 @@ __global__ __launch_bounds__(256) void act_decode_kernel(const int8_t* __restric
 #pragma unroll
       for (int i = 0; i < 8; ++i) f[i] = f[i] * r * w[i];
     }
-    store8(out + at * 8, f);
+    stream8(out + at * 8, f);
   }
 }
 
@@ -1302,14 +1320,14 @@ __global__ __launch_bounds__(1024) void norm_forward_kernel(const T* __restrict_
       if (v < nv) {
         const int64_t at = row * nv + v;
         if (codes != nullptr) {
-          *reinterpret_cast<u32x2*>(codes + at * 8) = encode8(f[k], e);
+          __builtin_nontemporal_store(encode8(f[k], e), reinterpret_cast<u32x2*>(codes + at * 8));
           if ((v & 3) == 0) exps[row * nb + v / 4] = (uint8_t)e;
         }
         float w[8];
         load8_any(weight, weight_bf16, (int64_t)v * 8, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) w[i] = f[k][i] * r * w[i];
-        store8(y + at * 8, w);
+        stream8(y + at * 8, w);
       }
     }
   }
@@ -1450,7 +1468,7 @@ hipError_t launch_teacher_topk(const void* logits, int bf16, int64_t rows, int64
 hipError_t launch_embedding_forward(const void* W, int bf16, int64_t V, int d, int64_t v_offset, const void* tokens,
                                     int tokens64, int64_t T, float scale, void* out, hipStream_t st) {
   const Units q = units(d / 8);
-  const unsigned blocks = (unsigned)cdiv(T * q.n, 1024);
+  const unsigned blocks = (unsigned)cdiv(T * q.n, 256 * kEmbedUnits);
   auto go = [&](auto* w, auto* tok) {
     using E = std::remove_const_t<std::remove_pointer_t<decltype(w)>>;
     embedding_forward_kernel<<<blocks, 256, 0, st>>>(w, V, v_offset, tok, T, q, scale, (E*)out);
@@ -1470,7 +1488,7 @@ EmbedWs embed_ws(int64_t T, int64_t V, int64_t d) {
     o += (bytes + 255) & ~(size_t)255;
     return at;
   };
-  w.chunk = T <= 4096 ? 8 : 16;
+  w.chunk = T <= 8192 ? 8 : T <= 65536 ? 16 : 32;
   w.chunks = cdiv(T, w.chunk);
   if (T > kRankMax) {
     int bits = 1;
@@ -1504,9 +1522,9 @@ static hipError_t embedding_reduce(const T* dY, int64_t n, int d, int64_t V, flo
       dY, key, pos, n, (int)w.chunk, w.chunks, q, (uint32_t)V, scale, dW, part, joins);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || w.chunks < 2) return e;
-  const int64_t most = (w.chunks - 1) * cdiv(q.n, 32);
-  embedding_join_kernel<G, ADD><<<(unsigned)std::min<int64_t>(most, 1024), 256, 0, st>>>(
-      key, n, (int)w.chunk, w.chunks, (int)q.n, scale, dW, part, joins);
+  const int64_t most = (w.chunks - 1) * cdiv(q.n, 64);
+  embedding_join_kernel<G, ADD><<<(unsigned)std::min<int64_t>(most, 2048), 256, 0, st>>>(
+      key, (int)w.chunk, w.chunks, (int)q.n, scale, dW, part, joins);
   return hipGetLastError();
 }
 
@@ -1601,11 +1619,14 @@ hipError_t launch_act_decode(const int8_t* codes, const uint8_t* exps, int64_t T
   return hipGetLastError();
 }
 
-// Threads and vectors per thread for rows of nv vectors.
+// Threads and vectors per thread for rows of nv vectors.  Two vectors a thread
+// have the loads in flight that one has in twice the threads, and half the waves
+// to wait for at the row's sum.  (32768 x 2880 bf16, forward: one vector in 384
+// threads 106 us, two in 192 84, three in 128 90, six in 64 109; backward 101,
+// 98, 101, 120.)  More than two where a workgroup's 1024 threads need it.
 static void norm_shape(int nv, int* threads, int* per) {
-  *threads = (int)std::min<int64_t>(1024, cdiv(nv, 64) * 64);
-  const int64_t k = cdiv(nv, *threads);
-  *per = k <= 1 ? 1 : k <= 2 ? 2 : k <= 4 ? 4 : 8;
+  *per = nv <= 64 ? 1 : nv <= 2048 ? 2 : nv <= 4096 ? 4 : 8;
+  *threads = (int)cdiv(cdiv(nv, *per), 64) * 64;
 }
 
 hipError_t launch_norm_forward(const void* x, int bf16, int64_t T, int d, const void* weight, int weight_bf16,
@@ -1630,7 +1651,13 @@ hipError_t launch_norm_forward(const void* x, int bf16, int64_t T, int d, const 
   return hipGetLastError();
 }
 
-int64_t norm_backward_groups(int64_t T, int64_t) { return std::min<int64_t>(T, 1024); }
+// Sixteen waves on each of the 256 compute units.  (32768 x 2880: 3 / 4 / 5 / 6 /
+// 8 workgroups of three waves a unit 121 / 103 / 98 / 99 / 115 us.)
+int64_t norm_backward_groups(int64_t T, int64_t d) {
+  int threads, per;
+  norm_shape((int)(d / 8), &threads, &per);
+  return std::min<int64_t>(T, 256 * std::max(1, 1024 / threads));
+}
 
 hipError_t launch_norm_backward(const void* dy, int bf16, int64_t T, int d, const int8_t* codes, const uint8_t* exps,
                                 const float* rstd, const void* weight, int weight_bf16, void* dx, void* dweight,

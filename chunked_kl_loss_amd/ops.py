@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 
 import torch
 
@@ -34,13 +35,19 @@ def _on(device):
 
 
 def _stream(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)  # (a Stream object costs as much as a launch)
 
 
-def _workspace(size_fn, sizes, device):
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(name: str, *sizes) -> int:
     out = ctypes.c_size_t(0)
-    check(size_fn(*sizes, ctypes.byref(out)))
-    return (_empty(out.value, torch.uint8, device) if out.value else None), out.value
+    check(getattr(load_library(), name)(*sizes, ctypes.byref(out)))
+    return out.value
+
+
+def _workspace(device, name: str, *sizes):
+    n = _workspace_bytes(name, *sizes)
+    return (_empty(n, torch.uint8, device) if n else None), n
 
 
 def _rows(shape) -> int:
@@ -68,7 +75,7 @@ def teacher_topk(logits, K: int, mask=None, teacher_form: int = CKL_TEACHER_LOGI
             raise ValueError("mask must be a uint8/bool tensor of the logits' leading shape")
     code = _dtype_code(logits.dtype)
     lib = load_library()
-    ws, ws_bytes = _workspace(lib.ckl_topk_workspace_size, (T, V, K), dev)
+    ws, ws_bytes = _workspace(dev, "ckl_topk_workspace_size", T, V, K)
     idx = _empty((*lead, K), torch.int32, dev)
     values = _empty((*lead, K), torch.float32, dev)
     lse = _empty(lead, torch.float32, dev)
@@ -123,7 +130,7 @@ def embedding_backward(dY, tokens, V: int, scale: float = 1.0, v_offset: int = 0
         dw_code = _dtype_code(dw_dtype)
     T = tokens.numel()
     lib = load_library()
-    ws, ws_bytes = _workspace(lib.ckl_embedding_workspace_size, (T, d, V), dev)
+    ws, ws_bytes = _workspace(dev, "ckl_embedding_workspace_size", T, d, V)
     if add_to is None:
         dW = _empty((V, d), dw_dtype, dev)
     with _on(dev):
@@ -222,7 +229,7 @@ def norm_backward(dy, codes, exps, rstd, weight):
     code, w_code = _dtype_code(dy.dtype), _check_weight(weight, d)
     T = _rows(lead)
     lib = load_library()
-    ws, ws_bytes = _workspace(lib.ckl_norm_workspace_size, (T, d), dev)
+    ws, ws_bytes = _workspace(dev, "ckl_norm_workspace_size", T, d)
     dx = _empty(dy.shape, dy.dtype, dev)
     dweight = _empty(d, weight.dtype, dev)
     with _on(dev):
