@@ -54,6 +54,24 @@ __device__ __forceinline__ void stream8(float* p, const float* f) {
   __builtin_nontemporal_store(f32x4{f[0], f[1], f[2], f[3]}, reinterpret_cast<f32x4*>(p));
   __builtin_nontemporal_store(f32x4{f[4], f[5], f[6], f[7]}, reinterpret_cast<f32x4*>(p) + 1);
 }
+// Eight elements that nothing else will read.
+__device__ __forceinline__ void load8_once(const bf16_t* p, float* f) {
+  const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(v[i] << 16);
+    f[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load8_once(const float* p, float* f) {
+  const f32x4 a = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p));
+  const f32x4 b = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p) + 1);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[i] = a[i];
+    f[4 + i] = b[i];
+  }
+}
 // A weight of either type, eight columns.
 __device__ __forceinline__ void load8_any(const void* p, int is_bf16, int64_t at, float* f) {
   if (is_bf16)
@@ -898,35 +916,104 @@ __device__ __forceinline__ uint32_t token_key(const I* tokens, int64_t t, int64_
   return (v >= 0 && v < V) ? (uint32_t)v : (uint32_t)V;
 }
 
-// Few positions: each one's rank is counted directly.  A workgroup ranks 64
-// positions; its waves share the comparisons, 16 keys at a time.
+// Zeros, by the workgroups of a launch past its own `first`: the rows of dW that
+// no token has are cleared while the positions are being sorted.
+struct Fill {
+  u32x4* p;
+  int64_t n;
+  int first;
+};
+__device__ __forceinline__ bool fill_instead(const Fill& fill) {
+  if ((int)blockIdx.x < fill.first) return false;
+  const int64_t stride = (int64_t)(gridDim.x - fill.first) * blockDim.x;
+  for (int64_t i = (int64_t)(blockIdx.x - fill.first) * blockDim.x + threadIdx.x; i < fill.n; i += stride)
+    fill.p[i] = u32x4{0, 0, 0, 0};
+  return true;
+}
+
+// Very few positions (a prompt): one launch.  Workgroup (t, y) looks for the
+// other positions of its token; the first of them adds their rows.
+constexpr int kFewMax = 256;
+template <typename T, typename G, typename I, bool ADD>
+__global__ __launch_bounds__(256) void embedding_few_kernel(const T* __restrict__ dY, const I* __restrict__ tokens,
+                                                            int n, int64_t V, int64_t v_offset, int nv, float scale,
+                                                            G* __restrict__ dW) {
+  __shared__ uint64_t masks[kFewMax / 64];
+  const int tid = threadIdx.x, t = blockIdx.x;
+  const uint32_t k = token_key(tokens, t, V, v_offset);
+  const uint64_t same = __ballot(tid < n && token_key(tokens, tid < n ? tid : 0, V, v_offset) == k);
+  if ((tid & 63) == 0) masks[tid >> 6] = same;
+  const int col = blockIdx.y * 256 + tid;
+  const bool in = col < nv && k < V;
+  G* dst = dW + ((int64_t)k * nv + col) * 8;
+  float sum[8] = {}, old[8] = {};
+  if (ADD && in) load8(dst, old);
+  __syncthreads();
+  if (!in) return;
+  for (int w = 0; w < kFewMax / 64; ++w) {
+    uint64_t m = masks[w];
+    if (w <= t >> 6 && (m & (w == t >> 6 ? ((uint64_t)1 << (t & 63)) - 1 : ~(uint64_t)0))) return;  // not the first
+    while (m) {
+      float f[4][8];
+      int p[4], c = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        p[j] = m ? w * 64 + __builtin_ctzll(m) : -1;
+        c += m ? 1 : 0;
+        m &= m - 1;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j < c) load8(dY + ((int64_t)p[j] * nv + col) * 8, f[j]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (j < c) {
+#pragma unroll
+          for (int x = 0; x < 8; ++x) sum[x] += f[j][x];
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int x = 0; x < 8; ++x) sum[x] = ADD ? old[x] + scale * sum[x] : scale * sum[x];
+  store8(dst, sum);
+}
+
+// Few positions: each one's rank is counted directly, T^2 comparisons over the
+// whole GPU.  A workgroup ranks 16 positions; 64 slices share the keys, 16 at a
+// time.
 constexpr int kRankMax = 8192;
 constexpr int kRankWaves = 16;
+constexpr int kRankRows = 16;
 template <typename I>
 __global__ __launch_bounds__(64 * kRankWaves) void rank_sort_kernel(const I* __restrict__ tokens, int n, int64_t V,
                                                                      int64_t v_offset, uint32_t* __restrict__ key_out,
                                                                      uint32_t* __restrict__ pos_out,
-                                                                     uint32_t* __restrict__ joins) {
+                                                                     uint32_t* __restrict__ joins, Fill fill) {
   __shared__ __attribute__((aligned(16))) uint32_t keys[kRankMax];
-  __shared__ int part[kRankWaves][64];
+  __shared__ int part[kRankWaves][kRankRows];
+  if (fill_instead(fill)) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int n16 = (n + 15) & ~15;
+  const int padded = (n + 63) & ~63;
   if (blockIdx.x == 0 && threadIdx.x == 0) *joins = 0;
-  for (int i = threadIdx.x; i < n16; i += 64 * kRankWaves)
+  for (int i = threadIdx.x; i < padded; i += 64 * kRankWaves)
     keys[i] = i < n ? token_key(tokens, i, V, v_offset) : 0xffffffffu;
   __syncthreads();
-  const int t = blockIdx.x * 64 + lane;
+  const int t0 = blockIdx.x * kRankRows, t = t0 + (lane & (kRankRows - 1));
   const uint32_t mine = t < n ? keys[t] : 0;
   int less = 0;
-  for (int i = wave * 16; i < n16; i += kRankWaves * 16) {
+  for (int i0 = wave * 64; i0 < padded; i0 += kRankWaves * 64) {
+    const int i = i0 + (lane / kRankRows) * 16;
     u32x4 k[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) k[j] = *reinterpret_cast<const u32x4*>(keys + i + 4 * j);
-    // equal keys count where they come earlier: all of a group before this
-    // workgroup's positions, none of a group after them
-    if (i + 16 <= (int)blockIdx.x * 64) {
+    // equal keys count where they come earlier
+    if (i0 + 64 <= t0) {
 #pragma unroll
       for (int j = 0; j < 16; ++j) less += k[j >> 2][j & 3] <= mine ? 1 : 0;
+    } else if (i0 >= t0 + kRankRows) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) less += k[j >> 2][j & 3] < mine ? 1 : 0;
     } else {
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
@@ -935,9 +1022,11 @@ __global__ __launch_bounds__(64 * kRankWaves) void rank_sort_kernel(const I* __r
       }
     }
   }
-  part[wave][lane] = less;
+  less += __shfl_xor(less, 16);
+  less += __shfl_xor(less, 32);
+  if (lane < kRankRows) part[wave][lane] = less;
   __syncthreads();
-  if (wave == 0 && t < n) {
+  if (threadIdx.x < kRankRows && t < n) {
     int r = 0;
 #pragma unroll
     for (int w = 0; w < kRankWaves; ++w) r += part[w][lane];
@@ -958,9 +1047,10 @@ __global__ __launch_bounds__(64 * kSortWaves) void sort_hist_kernel(const I* __r
                                                                      int64_t v_offset, int bins, int shift,
                                                                      uint32_t* __restrict__ key,
                                                                      uint32_t* __restrict__ hist,
-                                                                     uint32_t* __restrict__ joins) {
+                                                                     uint32_t* __restrict__ joins, Fill fill) {
   // tokens NULL: the keys are there already
   __shared__ uint32_t h[kSortBins];
+  if (fill_instead(fill)) return;
   if (blockIdx.x == 0 && threadIdx.x == 0) *joins = 0;
   if (threadIdx.x < kSortBins) h[threadIdx.x] = 0;
   __syncthreads();
@@ -1092,7 +1182,7 @@ __global__ __launch_bounds__(256) void embedding_sum_kernel(const T* __restrict_
     float f[kSumBatch][8], old[kSumBatch][8];
 #pragma unroll
     for (int j = 0; j < kSumBatch; ++j) {
-      if (k[j] < V) load8(dY + ((int64_t)p[j] * q.n + col) * 8, f[j]);
+      if (k[j] < V) load8_once(dY + ((int64_t)p[j] * q.n + col) * 8, f[j]);
       if (ADD && k[j] < V && k[j] != k[j + 1]) load8(dW + ((int64_t)k[j] * q.n + col) * 8, old[j]);
     }
 #pragma unroll
@@ -1174,9 +1264,7 @@ __global__ __launch_bounds__(256) void embedding_join_kernel(const uint32_t* __r
   }
 }
 
-__global__ __launch_bounds__(256) void zero_kernel(u32x4* __restrict__ p, int64_t n) {
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = u32x4{0, 0, 0, 0};
-}
+__global__ __launch_bounds__(1024) void zero_kernel(Fill fill) { fill_instead(fill); }
 
 // -------------------------------------------------- 8-bit activations, norm --
 // Blocks of 32 columns of a row share a power of two 2^(E - 127), the smallest
@@ -1482,6 +1570,7 @@ hipError_t launch_embedding_forward(const void* W, int bf16, int64_t V, int d, i
 
 EmbedWs embed_ws(int64_t T, int64_t V, int64_t d) {
   EmbedWs w{};
+  if (T <= kFewMax) return w;  // (no workspace)
   size_t o = 0;
   auto take = [&](size_t bytes) {
     size_t at = o;
@@ -1528,17 +1617,21 @@ static hipError_t embedding_reduce(const T* dY, int64_t n, int d, int64_t V, flo
   return hipGetLastError();
 }
 
+// Workgroups of 1024 threads for n 16-byte words of zeros.
+static unsigned fill_blocks(int64_t n) { return (unsigned)std::min<int64_t>(cdiv(n, 4096), 2048); }
+
 template <int ROUNDS, typename I>
 static hipError_t embedding_radix(const I* tokens, int64_t T, int64_t V, int64_t v_offset, const EmbedWs& w, char* ws,
-                                  const uint32_t** key, const uint32_t** pos, hipStream_t st) {
+                                  Fill fill, const uint32_t** key, const uint32_t** pos, hipStream_t st) {
   uint32_t* k[2] = {(uint32_t*)(ws + w.key0), (uint32_t*)(ws + w.key1)};
   uint32_t* p[2] = {(uint32_t*)(ws + w.pos0), (uint32_t*)(ws + w.pos1)};
   uint32_t* hist = (uint32_t*)(ws + w.hist);
   const unsigned blocks = (unsigned)w.sort_blocks, threads = 64 * kSortWaves;
   for (int i = 0; i < w.passes; ++i) {
     const int from = i & 1, shift = i * w.digit_bits;
-    sort_hist_kernel<I, ROUNDS><<<blocks, threads, 0, st>>>(i ? nullptr : tokens, T, V, v_offset, 1 << w.digit_bits,
-                                                            shift, k[from], hist, (uint32_t*)(ws + w.joins));
+    fill.first = (int)blocks;
+    sort_hist_kernel<I, ROUNDS><<<blocks + (i ? 0 : fill_blocks(fill.n)), threads, 0, st>>>(
+        i ? nullptr : tokens, T, V, v_offset, 1 << w.digit_bits, shift, k[from], hist, (uint32_t*)(ws + w.joins), fill);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     sort_scatter_kernel<ROUNDS><<<blocks, threads, 0, st>>>(k[from], i ? p[from] : nullptr, T, shift, w.digit_bits,
@@ -1552,35 +1645,52 @@ static hipError_t embedding_radix(const I* tokens, int64_t T, int64_t V, int64_t
 
 template <typename I>
 static hipError_t embedding_sort(const I* tokens, int64_t T, int64_t V, int64_t v_offset, const EmbedWs& w, char* ws,
-                                 const uint32_t** key, const uint32_t** pos, hipStream_t st) {
+                                 Fill fill, const uint32_t** key, const uint32_t** pos, hipStream_t st) {
   if (w.passes)
-    return w.sort_rounds == 1 ? embedding_radix<1>(tokens, T, V, v_offset, w, ws, key, pos, st)
-                              : embedding_radix<4>(tokens, T, V, v_offset, w, ws, key, pos, st);
+    return w.sort_rounds == 1 ? embedding_radix<1>(tokens, T, V, v_offset, w, ws, fill, key, pos, st)
+                              : embedding_radix<4>(tokens, T, V, v_offset, w, ws, fill, key, pos, st);
   *key = (uint32_t*)(ws + w.key0);
   *pos = (uint32_t*)(ws + w.pos0);
-  rank_sort_kernel<<<(unsigned)cdiv(T, 64), 64 * kRankWaves, 0, st>>>(tokens, (int)T, V, v_offset,
-                                                                      (uint32_t*)(ws + w.key0),
-                                                                      (uint32_t*)(ws + w.pos0),
-                                                                      (uint32_t*)(ws + w.joins));
+  fill.first = (int)cdiv(T, kRankRows);
+  rank_sort_kernel<<<(unsigned)fill.first + fill_blocks(fill.n), 64 * kRankWaves, 0, st>>>(
+      tokens, (int)T, V, v_offset, (uint32_t*)(ws + w.key0), (uint32_t*)(ws + w.pos0), (uint32_t*)(ws + w.joins), fill);
   return hipGetLastError();
 }
 
 hipError_t launch_embedding_backward(const void* dY, int bf16, int64_t T, int d, const void* tokens, int tokens64,
                                      int64_t V, int64_t v_offset, float scale, void* dW, int dw_bf16, int accumulate,
                                      char* ws, hipStream_t st) {
+  const Fill fill{(u32x4*)dW, accumulate ? 0 : V * d * (dw_bf16 ? 2 : 4) / 16, 0};
   hipError_t e;
-  if (!accumulate) {
-    const int64_t n = V * d * (dw_bf16 ? 2 : 4) / 16;
-    zero_kernel<<<(unsigned)std::min<int64_t>(cdiv(n, 256), 8192), 256, 0, st>>>((u32x4*)dW, n);
+  if (T <= kFewMax && fill.n > 0) {
+    zero_kernel<<<fill_blocks(fill.n), 1024, 0, st>>>(fill);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   if (T == 0) return hipSuccess;
+  if (T <= kFewMax) {
+    const dim3 grid((unsigned)T, (unsigned)cdiv(d / 8, 256));
+    auto go = [&](auto* dy, auto* tok, auto* dw) {
+      using A = std::remove_const_t<std::remove_pointer_t<decltype(dy)>>;
+      using I = std::remove_const_t<std::remove_pointer_t<decltype(tok)>>;
+      using G = std::remove_pointer_t<decltype(dw)>;
+      if (accumulate)
+        embedding_few_kernel<A, G, I, true><<<grid, 256, 0, st>>>(dy, tok, (int)T, V, v_offset, d / 8, scale, dw);
+      else
+        embedding_few_kernel<A, G, I, false><<<grid, 256, 0, st>>>(dy, tok, (int)T, V, v_offset, d / 8, scale, dw);
+    };
+    auto with_dw = [&](auto* dy, auto* tok) { dw_bf16 ? go(dy, tok, (bf16_t*)dW) : go(dy, tok, (float*)dW); };
+    auto with_tok = [&](auto* dy) {
+      tokens64 ? with_dw(dy, (const int64_t*)tokens) : with_dw(dy, (const int32_t*)tokens);
+    };
+    bf16 ? with_tok((const bf16_t*)dY) : with_tok((const float*)dY);
+    return hipGetLastError();
+  }
   const EmbedWs w = embed_ws(T, V, d);
   const uint32_t *key, *pos;
   if (tokens64)
-    e = embedding_sort((const int64_t*)tokens, T, V, v_offset, w, ws, &key, &pos, st);
+    e = embedding_sort((const int64_t*)tokens, T, V, v_offset, w, ws, fill, &key, &pos, st);
   else
-    e = embedding_sort((const int32_t*)tokens, T, V, v_offset, w, ws, &key, &pos, st);
+    e = embedding_sort((const int32_t*)tokens, T, V, v_offset, w, ws, fill, &key, &pos, st);
   if (e != hipSuccess) return e;
   auto go = [&](auto* dy, auto* dw) {
     return accumulate ? embedding_reduce<true>(dy, T, d, V, scale, dw, w, ws, key, pos, st)

@@ -81,8 +81,8 @@ def emb_b(lib, dY=P[0], dtype=1, T=10, d=64, tok=P[1], nb=8, V=100, off=0, dW=P[
     (dict(T=-1), INV), (dict(V=0), INV), (dict(d=12), INV), (dict(off=-1), INV), (dict(dtype=3), INV),
     (dict(dwt=2), INV), (dict(acc=2), INV), (dict(nb=1), INV), (dict(dY=None), INV), (dict(tok=None), INV),
     (dict(dW=None), INV), (dict(dW=None, T=0), INV), (dict(dY=P[0] + 4), INV), (dict(dW=P[2] + 4), INV),
-    (dict(tok=P[1] + 4), INV), (dict(ws=None), WSP), (dict(ws_bytes=64), WSP), (dict(dW=P[0]), INV),
-    (dict(ws=P[1]), INV), (dict(ws=P[2]), INV),
+    (dict(tok=P[1] + 4), INV), (dict(T=1000, ws=None), WSP), (dict(T=1000, ws_bytes=64), WSP),
+    (dict(dW=P[0]), INV), (dict(T=1000, ws=P[1]), INV), (dict(T=1000, ws=P[2]), INV),
 ])
 def test_embedding_backward_refusals(lib, kw, status):
     assert emb_b(lib, **kw) == status
@@ -93,7 +93,8 @@ def test_embedding_backward_refusals(lib, kw, status):
 @pytest.mark.parametrize("V", [1, 511, 512, 262143, 262144, 4000000])
 def test_embedding_workspace_grows_with_rows_only(lib, T, V):
     n = size(lib.ckl_embedding_workspace_size, T, 64, V)
-    assert 8 * T <= n <= 200 * T + (1 << 16)
+    # (a prompt of up to 256 tokens needs none)
+    assert (0 if T <= 256 else 8 * T) <= n <= 200 * T + (1 << 16)
 
 
 def test_small_refusals_of_the_8bit_calls(lib):
