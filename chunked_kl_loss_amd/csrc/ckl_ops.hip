@@ -54,23 +54,33 @@ __device__ __forceinline__ void stream8(float* p, const float* f) {
   __builtin_nontemporal_store(f32x4{f[0], f[1], f[2], f[3]}, reinterpret_cast<f32x4*>(p));
   __builtin_nontemporal_store(f32x4{f[4], f[5], f[6], f[7]}, reinterpret_cast<f32x4*>(p) + 1);
 }
-// Eight elements that nothing else will read.
-__device__ __forceinline__ void load8_once(const bf16_t* p, float* f) {
-  const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+// Four elements.
+__device__ __forceinline__ void load4(const bf16_t* p, float* f) {
+  const u32x2 v = *reinterpret_cast<const u32x2*>(p);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 2; ++i) {
     f[2 * i] = __uint_as_float(v[i] << 16);
     f[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
   }
 }
-__device__ __forceinline__ void load8_once(const float* p, float* f) {
-  const f32x4 a = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p));
-  const f32x4 b = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p) + 1);
+__device__ __forceinline__ void load4(const float* p, float* f) {
+  const f32x4 a = *reinterpret_cast<const f32x4*>(p);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[i] = a[i];
-    f[4 + i] = b[i];
+  for (int i = 0; i < 4; ++i) f[i] = a[i];
+}
+// Four elements that nothing else will read.
+__device__ __forceinline__ void load4_once(const bf16_t* p, float* f) {
+  const u32x2 v = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p));
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    f[2 * i] = __uint_as_float(v[i] << 16);
+    f[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
   }
+}
+__device__ __forceinline__ void load4_once(const float* p, float* f) {
+  const f32x4 a = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = a[i];
 }
 // A weight of either type, eight columns.
 __device__ __forceinline__ void load8_any(const void* p, int is_bf16, int64_t at, float* f) {
@@ -1148,7 +1158,7 @@ __global__ __launch_bounds__(64 * kSortWaves) void sort_scatter_kernel(
   }
 }
 
-// A thread sums eight columns over one chunk of the sorted positions, four at a
+// A thread sums four columns over one chunk of the sorted positions, four at a
 // time: their rows, and the old gradients of the tokens that end among them,
 // are loaded together, so that eight loads are under way instead of one (the
 // rows of a token are anywhere in dY).  Runs of one token inside the chunk are
@@ -1168,7 +1178,7 @@ __global__ __launch_bounds__(256) void embedding_sum_kernel(const T* __restrict_
   if (c >= chunks) return;
   const int64_t b = c * chunk, e = b + chunk < n ? b + chunk : n;
   bool from_before = b > 0 && key[b - 1] == key[b];
-  float sum[8] = {};
+  float sum[4] = {};
   for (int64_t i = b; i < e; i += kSumBatch) {
     uint32_t k[kSumBatch + 1], p[kSumBatch];
     const int m = e - i < kSumBatch ? (int)(e - i) : kSumBatch;
@@ -1179,30 +1189,30 @@ __global__ __launch_bounds__(256) void embedding_sum_kernel(const T* __restrict_
     }
     k[kSumBatch] = i + kSumBatch < e ? key[i + kSumBatch] : 0xffffffffu;
     if (k[0] >= V) return;
-    float f[kSumBatch][8], old[kSumBatch][8];
+    float f[kSumBatch][4], old[kSumBatch][4];
 #pragma unroll
     for (int j = 0; j < kSumBatch; ++j) {
-      if (k[j] < V) load8_once(dY + ((int64_t)p[j] * q.n + col) * 8, f[j]);
-      if (ADD && k[j] < V && k[j] != k[j + 1]) load8(dW + ((int64_t)k[j] * q.n + col) * 8, old[j]);
+      if (k[j] < V) load4_once(dY + ((int64_t)p[j] * q.n + col) * 4, f[j]);
+      if (ADD && k[j] < V && k[j] != k[j + 1]) load4(dW + ((int64_t)k[j] * q.n + col) * 4, old[j]);
     }
 #pragma unroll
     for (int j = 0; j < kSumBatch; ++j) {
       if (k[j] >= V) return;
 #pragma unroll
-      for (int x = 0; x < 8; ++x) sum[x] += f[j][x];
+      for (int x = 0; x < 4; ++x) sum[x] += f[j][x];
       if (k[j] != k[j + 1]) {  // the run ends here, or the chunk does
         const bool goes_on = i + j + 1 == e && e < n && key[e] == k[j];
         if (!from_before && !goes_on) {
 #pragma unroll
-          for (int x = 0; x < 8; ++x) sum[x] = ADD ? old[j][x] + scale * sum[x] : scale * sum[x];
-          store8(dW + ((int64_t)k[j] * q.n + col) * 8, sum);
+          for (int x = 0; x < 4; ++x) sum[x] = ADD ? old[j][x] + scale * sum[x] : scale * sum[x];
+          store4(dW + ((int64_t)k[j] * q.n + col) * 4, f32x4{sum[0], sum[1], sum[2], sum[3]});
         } else {
-          store8(part + ((2 * c + (from_before ? 0 : 1)) * (int64_t)q.n + col) * 8, sum);
+          store4(part + ((2 * c + (from_before ? 0 : 1)) * (int64_t)q.n + col) * 4, f32x4{sum[0], sum[1], sum[2], sum[3]});
           if (!from_before && col == 0) joins[1 + atomicAdd(joins, 1u)] = (uint32_t)c;
         }
         from_before = false;
 #pragma unroll
-        for (int x = 0; x < 8; ++x) sum[x] = 0.f;
+        for (int x = 0; x < 4; ++x) sum[x] = 0.f;
       }
     }
   }
@@ -1577,7 +1587,10 @@ EmbedWs embed_ws(int64_t T, int64_t V, int64_t d) {
     o += (bytes + 255) & ~(size_t)255;
     return at;
   };
-  w.chunk = T <= 8192 ? 8 : T <= 65536 ? 16 : 32;
+  // Long chunks leave few borders to join, short ones enough waves: the longest
+  // with 4096 of them, four to a SIMD.  (32768 x 2880 added to fp32, chunks of 16
+  // / 32 / 64: 125 / 129 / 117 us; 16384 x 2880 81 / 71 / 71; 12000 x 768 42 / 51.)
+  for (w.chunk = 64; w.chunk > 8 && cdiv(T, w.chunk) * (d / 4) < 4096 * 64; w.chunk /= 2) {}
   w.chunks = cdiv(T, w.chunk);
   if (T > kRankMax) {
     int bits = 1;
@@ -1604,16 +1617,17 @@ EmbedWs embed_ws(int64_t T, int64_t V, int64_t d) {
 template <bool ADD, typename T, typename G>
 static hipError_t embedding_reduce(const T* dY, int64_t n, int d, int64_t V, float scale, G* dW, const EmbedWs& w,
                                    char* ws, const uint32_t* key, const uint32_t* pos, hipStream_t st) {
-  const Units q = units(d / 8);
+  const Units q = units(d / 4);
   float* part = (float*)(ws + w.part);
   uint32_t* joins = (uint32_t*)(ws + w.joins);
   embedding_sum_kernel<T, G, ADD><<<(unsigned)cdiv(w.chunks * q.n, 256), 256, 0, st>>>(
       dY, key, pos, n, (int)w.chunk, w.chunks, q, (uint32_t)V, scale, dW, part, joins);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || w.chunks < 2) return e;
-  const int64_t most = (w.chunks - 1) * cdiv(q.n, 64);
+  const int nv = d / 8;
+  const int64_t most = (w.chunks - 1) * cdiv(nv, 64);
   embedding_join_kernel<G, ADD><<<(unsigned)std::min<int64_t>(most, 2048), 256, 0, st>>>(
-      key, (int)w.chunk, w.chunks, (int)q.n, scale, dW, part, joins);
+      key, (int)w.chunk, w.chunks, nv, scale, dW, part, joins);
   return hipGetLastError();
 }
 
