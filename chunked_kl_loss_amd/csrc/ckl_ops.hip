@@ -173,19 +173,22 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
 
+template <int BINS>
 struct TopkShared {
-  uint32_t hist[256];
+  static constexpr int bins = BINS;  // of the final order; 256 serve everything else
+  uint32_t hist[BINS];
   uint32_t wave_n[4];
   uint32_t range[2][4];
   uint32_t pending[2][4];
   float wave_m[4], wave_s[4];
   uint32_t count, sel, need, bin;
-  uint32_t start[257];
+  uint32_t start[BINS + 1];
 };
 
 // Places for a lane's `mine` words behind those in the buffer: one addition to
 // the counter a wave.
-__device__ __forceinline__ int topk_place(int mine, TopkShared& sh) {
+template <typename S>
+__device__ __forceinline__ int topk_place(int mine, S& sh) {
   const int inc = wave_scan(mine);
   int at = 0;
   if ((threadIdx.x & 63) == 63) at = (int)atomicAdd(&sh.count, (uint32_t)inc);
@@ -193,7 +196,8 @@ __device__ __forceinline__ int topk_place(int mine, TopkShared& sh) {
 }
 
 // The extremes of a value over the workgroup.
-__device__ __forceinline__ void topk_range(uint32_t& lo, uint32_t& hi, TopkShared& sh) {
+template <typename S>
+__device__ __forceinline__ void topk_range(uint32_t& lo, uint32_t& hi, S& sh) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) {
     const uint32_t a = __shfl_xor(lo, o), b = __shfl_xor(hi, o);
@@ -218,9 +222,9 @@ __device__ __forceinline__ void topk_range(uint32_t& lo, uint32_t& hi, TopkShare
 // it holds one key only; *n = count(t).  No element reaches hi; at_lo =
 // count(lo), or more.  each(f) calls f for a thread's keys.  All threads call
 // it, after a barrier behind the last use of sh.
-template <typename E>
-__device__ __forceinline__ uint32_t topk_select(E each, uint32_t lo, uint32_t hi, int at_lo, int K, int limit,
-                                                TopkShared& sh, int* n) {
+template <typename E, typename S>
+__device__ __forceinline__ uint32_t topk_select(E each, uint32_t lo, uint32_t hi, int at_lo, int K, int limit, S& sh,
+                                                int* n) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   uint32_t above = 0;  // elements that reach hi
   while (at_lo > limit && hi - lo > 1) {
@@ -259,7 +263,8 @@ __device__ __forceinline__ uint32_t topk_select(E each, uint32_t lo, uint32_t hi
 // Cuts the n > K words of buf to exactly the K largest, by radix selection:
 // where keys are equal the index decides.  In any order; begins and ends with a
 // barrier.
-__device__ __forceinline__ void topk_cut_exact(uint64_t* buf, int n, int K, TopkShared& sh) {
+template <typename S>
+__device__ __forceinline__ void topk_cut_exact(uint64_t* buf, int n, int K, S& sh) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   uint64_t prefix = 0, pmask = 0;
   uint32_t need = (uint32_t)K;
@@ -308,9 +313,8 @@ __device__ __forceinline__ void topk_cut_exact(uint64_t* buf, int n, int K, Topk
 // Cuts the n > limit >= K words of buf to at most `limit` of the largest, at
 // least K, in any order.  Returns their number and sets *key to a key that at least K of them,
 // and none less, reach.  Begins and ends with a barrier.
-template <int CAP>
-__device__ __forceinline__ int topk_cut(uint64_t* buf, int n, int K, int limit, TopkShared& sh,
-                                        uint32_t* key) {
+template <int CAP, typename S>
+__device__ __forceinline__ int topk_cut(uint64_t* buf, int n, int K, int limit, S& sh, uint32_t* key) {
   const int tid = threadIdx.x;
   const uint32_t* keys = reinterpret_cast<const uint32_t*>(buf) + 1;
   __syncthreads();
@@ -449,7 +453,8 @@ __device__ __forceinline__ void exp_merge(float& m, float& s, float m2, float s2
 }
 
 // The workgroup's log-sum-exp state, in every thread.
-__device__ __forceinline__ void topk_reduce_state(float& m, float& s, TopkShared& sh) {
+template <typename S>
+__device__ __forceinline__ void topk_reduce_state(float& m, float& s, S& sh) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) {
     const float m2 = __shfl_xor(m, o), s2 = __shfl_xor(s, o);
@@ -466,20 +471,22 @@ __device__ __forceinline__ void topk_reduce_state(float& m, float& s, TopkShared
 }
 
 // The K largest of a row's n words in order, and its state, as the row's
-// results.  K up to 1024 (CAP = 4096): the words are put into 256 bins over the
-// range of their keys, and in its bin a word's place is the number of larger
-// words there.  Where a bin that matters holds more than 64 words (keys that are
-// mostly equal, or a far outlier), and for larger K, a bitonic sort does it.
-template <int CAP>
+// results.  The words are put into bins over the range of their keys, and in its
+// bin a word's place is the number of larger words there.  Where a bin that
+// matters holds more than 256 words (keys that are mostly equal, or a far
+// outlier) a bitonic sort does it.  (2048 rows of 100000 bf16, K = 2048: 352 us
+// a call with this, 580 with the bitonic sort.)
+template <int CAP, typename S>
 __device__ __forceinline__ void topk_finish(uint64_t* buf, int n, int K, float m, float s, int logprob, int* idx,
-                                            float* val, float* lse, TopkShared& sh) {
-  constexpr bool bins = CAP <= 4096;
-  constexpr int W = bins ? 10 : CAP / kTopkThreads, limit = W * kTopkThreads;
+                                            float* val, float* lse, S& sh) {
+  constexpr int W = CAP <= 4096 ? 10 : 24, limit = W * kTopkThreads;  // words that go into the bins
+  constexpr int per = S::bins / kTopkThreads;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   uint32_t key;
   if (n > limit) n = topk_cut<CAP>(buf, n, K, limit, sh, &key);
   __syncthreads();
-  sh.hist[tid] = 0;
+#pragma unroll
+  for (int b = 0; b < per; ++b) sh.hist[b * kTopkThreads + tid] = 0;
   if (tid == 0) sh.bin = 0;
   const uint32_t* keys = reinterpret_cast<const uint32_t*>(buf) + 1;
   uint32_t least = ~0u, most = 0;
@@ -500,55 +507,59 @@ __device__ __forceinline__ void topk_finish(uint64_t* buf, int n, int K, float m
     idx[place] = (int)~(uint32_t)word;
     val[place] = v;
   };
-  if constexpr (bins) {
-    const int bits = 32 - __clz((int)((most - least) | 1)), shift = bits > 8 ? bits - 8 : 0;
+  constexpr int bin_bits = S::bins == 256 ? 8 : 10;
+  const int bits = 32 - __clz((int)((most - least) | 1)), shift = bits > bin_bits ? bits - bin_bits : 0;
 #pragma unroll 4
-    for (int i = tid; i < n; i += kTopkThreads) atomicAdd(&sh.hist[(most - keys[2 * i]) >> shift], 1u);
-    __syncthreads();
-    const uint32_t own = sh.hist[tid];
-    const uint32_t inc = (uint32_t)wave_scan((int)own);
-    if (lane == 63) sh.wave_n[wave] = inc;
-    __syncthreads();
-    uint32_t at = inc - own;
-    for (int w = 0; w < wave; ++w) at += sh.wave_n[w];
-    sh.start[tid] = at;
-    sh.hist[tid] = at;  // the bin's next place
-    if (tid == kTopkThreads - 1) sh.start[kTopkThreads] = (uint32_t)n;
-    if (own > 64 && at < (uint32_t)K) sh.bin = 1;
-    uint64_t x[W];
+  for (int i = tid; i < n; i += kTopkThreads) atomicAdd(&sh.hist[(most - keys[2 * i]) >> shift], 1u);
+  __syncthreads();
+  uint32_t own[per], all = 0;
 #pragma unroll
-    for (int w = 0; w < W; ++w) x[w] = w * kTopkThreads + tid < n ? buf[w * kTopkThreads + tid] : 0;
-    __syncthreads();
-    if (!sh.bin) {
+  for (int b = 0; b < per; ++b) all += own[b] = sh.hist[tid * per + b];
+  const uint32_t inc = (uint32_t)wave_scan((int)all);
+  if (lane == 63) sh.wave_n[wave] = inc;
+  __syncthreads();
+  uint32_t at = inc - all;
+  for (int w = 0; w < wave; ++w) at += sh.wave_n[w];
 #pragma unroll
-      for (int w = 0; w < W; ++w)
-        if (w * kTopkThreads + tid < n) buf[atomicAdd(&sh.hist[(most - (uint32_t)(x[w] >> 32)) >> shift], 1u)] = x[w];
-      if (tid < 4) buf[n + tid] = 0;
-      __syncthreads();
-#pragma unroll 1
-      for (int i = tid; i < n; i += kTopkThreads) {
-        const uint64_t word = buf[i];
-        const uint32_t b = (most - (uint32_t)(word >> 32)) >> shift;
-        const int from = (int)sh.start[b], to = (int)sh.start[b + 1];
-        if (from >= K) break;  // (the words lie bin by bin)
-        int p = from;
-#pragma unroll 1
-        for (int j = from; j < to; j += 4) {  // (what lies behind the bin is smaller)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) p += buf[j + k] > word ? 1 : 0;
-        }
-        if (p < K) put(p, word);
-      }
-      return;
-    }
-    if (n > 2048) n = topk_cut<CAP>(buf, n, K, 2048, sh, &key);
-    topk_sort_bitonic<8>(buf, n);
-  } else if (n <= 2048) {
-    topk_sort_bitonic<8>(buf, n);
-  } else {
-    topk_sort_bitonic<W>(buf, n);
+  for (int b = 0; b < per; ++b) {
+    sh.start[tid * per + b] = at;
+    sh.hist[tid * per + b] = at;  // the bin's next place
+    if (own[b] > 256 && at < (uint32_t)K) sh.bin = 1;
+    at += own[b];
   }
-  for (int k = tid; k < K; k += kTopkThreads) put(k, buf[k]);
+  if (tid == kTopkThreads - 1) sh.start[S::bins] = (uint32_t)n;
+  uint64_t x[W];
+#pragma unroll
+  for (int w = 0; w < W; ++w) x[w] = w * kTopkThreads + tid < n ? buf[w * kTopkThreads + tid] : 0;
+  __syncthreads();
+  if (sh.bin) {
+    if (n > 2048 && K <= 2048) n = topk_cut<CAP>(buf, n, K, 2048, sh, &key);
+    if (n <= 2048)
+      topk_sort_bitonic<8>(buf, n);
+    else if constexpr (CAP > 4096)
+      topk_sort_bitonic<CAP / kTopkThreads>(buf, n);
+    for (int k = tid; k < K; k += kTopkThreads) put(k, buf[k]);
+    return;
+  }
+#pragma unroll
+  for (int w = 0; w < W; ++w)
+    if (w * kTopkThreads + tid < n) buf[atomicAdd(&sh.hist[(most - (uint32_t)(x[w] >> 32)) >> shift], 1u)] = x[w];
+  if (tid < 4) buf[n + tid] = 0;
+  __syncthreads();
+#pragma unroll 1
+  for (int i = tid; i < n; i += kTopkThreads) {
+    const uint64_t word = buf[i];
+    const uint32_t b = (most - (uint32_t)(word >> 32)) >> shift;
+    const int from = (int)sh.start[b], to = (int)sh.start[b + 1];
+    if (from >= K) break;  // (the words lie bin by bin)
+    int p = from;
+#pragma unroll 1
+    for (int j = from; j < to; j += 4) {  // (what lies behind the bin is smaller)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) p += buf[j + k] > word ? 1 : 0;
+    }
+    if (p < K) put(p, word);
+  }
 }
 
 __device__ __forceinline__ void topk_masked_row(int K, int* idx, float* val, float* lse) {
@@ -611,7 +622,7 @@ __global__ __launch_bounds__(kTopkThreads, CAP <= 4096 ? 4 : 2) void topk_rows_k
                                                                  float* __restrict__ lse, uint64_t* __restrict__ cand,
                                                                  float2* __restrict__ state) {
   __shared__ __attribute__((aligned(16))) uint64_t buf[CAP];
-  __shared__ TopkShared sh;
+  __shared__ TopkShared<CAP <= 4096 ? 256 : 1024> sh;
   __shared__ uint32_t lists[kTopkThreads / 64][kTopkList];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t row = blockIdx.x / segments;
@@ -840,7 +851,7 @@ __global__ __launch_bounds__(kTopkThreads, CAP <= 4096 ? 4 : 2) void topk_merge_
                                                                   int* __restrict__ idx, float* __restrict__ val,
                                                                   float* __restrict__ lse) {
   __shared__ __attribute__((aligned(16))) uint64_t buf[CAP];
-  __shared__ TopkShared sh;
+  __shared__ TopkShared<CAP <= 4096 ? 256 : 1024> sh;
   const int tid = threadIdx.x;
   const int64_t row = blockIdx.x;
   if (mask != nullptr && mask[row] == 0) {

@@ -6,7 +6,6 @@ are rows; tensors are contiguous and on one GPU.  Calls run on that GPU's
 current stream."""
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 
@@ -29,13 +28,16 @@ def _check(device, **tensors) -> None:
             raise ValueError(f"{name} must be contiguous")
 
 
-def _on(device):
-    """The library launches on the current GPU: make it the tensors' own."""
-    return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-
-
-def _stream(device) -> int:
-    return torch._C._cuda_getCurrentRawStream(device.index)  # (a Stream object costs as much as a launch)
+def _call(device, fn, *args) -> None:
+    """fn(*args, stream) on the device's current stream.  The library launches on the current GPU: the tensors'
+    own is made current where it is not."""
+    index = device.index
+    if index == torch.cuda.current_device():
+        # (the raw handle: a Stream object costs as much as a launch)
+        check(fn(*args, torch._C._cuda_getCurrentRawStream(index)))
+    else:
+        with torch.cuda.device(device):
+            check(fn(*args, torch._C._cuda_getCurrentRawStream(index)))
 
 
 @functools.lru_cache(maxsize=1024)
@@ -66,6 +68,7 @@ def teacher_topk(logits, K: int, mask=None, teacher_form: int = CKL_TEACHER_LOGI
     0 .. K-1, values 0, lse 0."""
     if logits.dim() < 1:
         raise ValueError("logits must be [..., V]")
+    K = int(K)
     lead, V = logits.shape[:-1], logits.shape[-1]
     T, dev = _rows(lead), logits.device
     _check(dev, logits=logits)
@@ -79,9 +82,8 @@ def teacher_topk(logits, K: int, mask=None, teacher_form: int = CKL_TEACHER_LOGI
     idx = _empty((*lead, K), torch.int32, dev)
     values = _empty((*lead, K), torch.float32, dev)
     lse = _empty(lead, torch.float32, dev)
-    with _on(dev):
-        check(lib.ckl_teacher_topk(_ptr(logits), code, T, V, K, teacher_form, _ptr(mask), _ptr(idx), _ptr(values),
-                                   _ptr(lse), _ptr(ws), ws_bytes, _stream(dev)), lib)
+    _call(dev, lib.ckl_teacher_topk, _ptr(logits), code, T, V, K, teacher_form, _ptr(mask), _ptr(idx), _ptr(values),
+          _ptr(lse), _ptr(ws), ws_bytes)
     return idx, values, lse
 
 
@@ -103,9 +105,8 @@ def embedding_forward(W, tokens, scale: float = 1.0, v_offset: int = 0):
     V, d = W.shape
     out = _empty((*tokens.shape, d), W.dtype, dev)
     lib = load_library()
-    with _on(dev):
-        check(lib.ckl_embedding_forward(_ptr(W), code, V, d, v_offset, _ptr(tokens), nb, tokens.numel(), scale,
-                                        _ptr(out), _stream(dev)), lib)
+    _call(dev, lib.ckl_embedding_forward, _ptr(W), code, V, d, v_offset, _ptr(tokens), nb, tokens.numel(), scale,
+          _ptr(out))
     return out
 
 
@@ -133,9 +134,8 @@ def embedding_backward(dY, tokens, V: int, scale: float = 1.0, v_offset: int = 0
     ws, ws_bytes = _workspace(dev, "ckl_embedding_workspace_size", T, d, V)
     if add_to is None:
         dW = _empty((V, d), dw_dtype, dev)
-    with _on(dev):
-        check(lib.ckl_embedding_backward(_ptr(dY), code, T, d, _ptr(tokens), nb, V, v_offset, scale, _ptr(dW),
-                                         dw_code, int(add_to is not None), _ptr(ws), ws_bytes, _stream(dev)), lib)
+    _call(dev, lib.ckl_embedding_backward, _ptr(dY), code, T, d, _ptr(tokens), nb, V, v_offset, scale, _ptr(dW),
+          dw_code, int(add_to is not None), _ptr(ws), ws_bytes)
     return dW
 
 
@@ -167,8 +167,7 @@ def act_encode(x):
     code = _dtype_code(x.dtype)
     codes, exps = _codes_for(x.shape[:-1], d, dev)
     lib = load_library()
-    with _on(dev):
-        check(lib.ckl_act_encode(_ptr(x), code, _rows(x.shape[:-1]), d, _ptr(codes), _ptr(exps), _stream(dev)), lib)
+    _call(dev, lib.ckl_act_encode, _ptr(x), code, _rows(x.shape[:-1]), d, _ptr(codes), _ptr(exps))
     return codes, exps
 
 
@@ -190,9 +189,8 @@ def act_decode(codes, exps, rstd=None, weight=None, dtype=torch.bfloat16):
     code = _dtype_code(dtype)
     out = _empty(codes.shape, dtype, dev)
     lib = load_library()
-    with _on(dev):
-        check(lib.ckl_act_decode(_ptr(codes), _ptr(exps), _rows(lead), d, _ptr(rstd), _ptr(weight), w_code, _ptr(out),
-                                 code, _stream(dev)), lib)
+    _call(dev, lib.ckl_act_decode, _ptr(codes), _ptr(exps), _rows(lead), d, _ptr(rstd), _ptr(weight), w_code,
+          _ptr(out), code)
     return out
 
 
@@ -210,9 +208,8 @@ def norm_forward(x, weight, eps: float = 1e-6, save: bool = True):
         codes, exps = _codes_for(lead, d, dev)
         rstd = _empty(lead, torch.float32, dev)
     lib = load_library()
-    with _on(dev):
-        check(lib.ckl_norm_forward(_ptr(x), code, _rows(lead), d, _ptr(weight), w_code, eps, _ptr(y), _ptr(codes),
-                                   _ptr(exps), _ptr(rstd), _stream(dev)), lib)
+    _call(dev, lib.ckl_norm_forward, _ptr(x), code, _rows(lead), d, _ptr(weight), w_code, eps, _ptr(y), _ptr(codes),
+          _ptr(exps), _ptr(rstd))
     return y, codes, exps, rstd
 
 
@@ -232,7 +229,6 @@ def norm_backward(dy, codes, exps, rstd, weight):
     ws, ws_bytes = _workspace(dev, "ckl_norm_workspace_size", T, d)
     dx = _empty(dy.shape, dy.dtype, dev)
     dweight = _empty(d, weight.dtype, dev)
-    with _on(dev):
-        check(lib.ckl_norm_backward(_ptr(dy), code, T, d, _ptr(codes), _ptr(exps), _ptr(rstd), _ptr(weight), w_code,
-                                    _ptr(dx), _ptr(dweight), _ptr(ws), ws_bytes, _stream(dev)), lib)
+    _call(dev, lib.ckl_norm_backward, _ptr(dy), code, T, d, _ptr(codes), _ptr(exps), _ptr(rstd), _ptr(weight), w_code,
+          _ptr(dx), _ptr(dweight), _ptr(ws), ws_bytes)
     return dx, dweight
