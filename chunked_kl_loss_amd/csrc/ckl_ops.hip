@@ -251,8 +251,7 @@ __device__ __forceinline__ uint32_t topk_select(E each, uint32_t lo, uint32_t hi
     }
     __syncthreads();
     lo += sh.sel << shift;
-    const uint32_t end = lo + (1u << shift);
-    hi = end < hi ? end : hi;
+    if (hi - lo > (1u << shift)) hi = lo + (1u << shift);  // (the last bin may end past 2^32)
     at_lo = (int)sh.need;
     above = sh.need - sh.bin;
   }

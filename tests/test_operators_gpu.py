@@ -135,6 +135,24 @@ def test_topk_infinities_and_nan():
     check_topk(big[:1100], K, form=0)
 
 
+@pytest.mark.parametrize("K", [40, 700, 1100])
+@pytest.mark.parametrize("T", [2, 1030])
+def test_topk_rows_of_mostly_special_values(T, K):
+    # thousands of NaN or infinite logits: the range of keys reaches the last one
+    z = normal((T, 9001), torch.float32, 3)
+    z[:, ::2] = math.nan
+    check_topk(z, K)
+    z[:, ::2] = math.inf
+    check_topk(z, K)
+    z[:, 1::4] = math.nan
+    check_topk(z, K)
+    z[:, ::2] = -math.inf
+    check_topk(z.bfloat16(), K)
+    z = normal((T, 6000), torch.float32, 4)   # one tile, fewer finite logits than K
+    z[:, 30:] = -math.inf
+    check_topk(z, K)
+
+
 def test_topk_shapes_and_repeatability():
     z = normal((2, 3, 1001), torch.bfloat16, 4).cuda()
     mask = torch.tensor([[1, 0, 1], [1, 1, 0]], dtype=torch.uint8).cuda()
