@@ -640,7 +640,9 @@ __global__ __launch_bounds__(kTopkThreads, CAP <= 4096 ? 4 : 2) void topk_rows_k
   const int mid_limit = K + K / 4 + 64;  // what a cut on the way may leave: at most CAP - kTopkStep
   const int cut_at = 2 * mid_limit < CAP - 1024 ? 2 * mid_limit : CAP - 1024;
 
-  const int end = row + 1 < rows ? V + shift + 8 : V + shift;  // columns that can be read
+  // columns that can be read: a few past the row where other rows follow
+  const int64_t rest = (rows - row) * V;
+  const int end = shift + (int)(rest < V + 8 ? rest : V + 8);
   // The vector at shifted column j, with -infinity outside [first, hi).
   auto fetch = [&](int j) {
     Raw8<T> r;

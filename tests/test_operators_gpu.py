@@ -89,6 +89,13 @@ def test_topk_sizes(T, V, K, dtype):
     check_topk(normal((T, V), DT[dtype], 7 * T + V, 3.0), K, form=(T + V) % 2)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [1, 2, 3, 5, 7, 9])
+def test_topk_rows_shorter_than_a_vector(V, dtype):
+    for T in (1, 2, 5):
+        check_topk(normal((T, V), DT[dtype], V + T, 3.0), V, form=T % 2)
+
+
 @pytest.mark.parametrize("T", [2, 1300])
 @pytest.mark.parametrize("form", [0, 1])
 def test_topk_masks(T, form):
