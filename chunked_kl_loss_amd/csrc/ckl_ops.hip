@@ -791,9 +791,9 @@ __global__ __launch_bounds__(kTopkThreads, CAP <= 4096 ? 4 : 2) void topk_rows_k
     for (int u = 0; u < kTopkVecs; ++u) raw[u] = next[u];
     if (t0 < lo) {
       // the first tile's key: what is wanted of that tile, and `after` of the rest
-      const int total = (int)((hi < lo + kTopkTile ? hi : lo + kTopkTile) - first);
+      const int to = hi < lo + kTopkTile ? hi : lo + kTopkTile, total = to - first;
       if (total > mid_limit) {
-        uint32_t key[kTopkVecs * 8];
+        uint32_t key[kTopkVecs * 8];  // 0 outside the row
         uint32_t most = 0, least_vec = ~0u, least = ~0u;
 #pragma unroll
         for (int u = 0; u < kTopkVecs; ++u) {
@@ -804,14 +804,15 @@ __global__ __launch_bounds__(kTopkThreads, CAP <= 4096 ? 4 : 2) void topk_rows_k
             const uint32_t k = j >= first && j < hi ? order_key(raw[u].get(i)) : 0;
             key[u * 8 + i] = k;
             top = k > top ? k : top;
-            least = k < least ? k : least;
+            least = k != 0 && k < least ? k : least;
           }
           most = top > most ? top : most;
-          least_vec = top < least_vec ? top : least_vec;
+          least_vec = top != 0 && top < least_vec ? top : least_vec;
         }
-        // the least of K or more maxima (of the threads, of the vectors) is
-        // reached by K elements; so is the least element
-        uint32_t from = K <= kTopkThreads ? most : K <= kTopkThreads * kTopkVecs ? least_vec : least;
+        // the least of K or more maxima (of the threads, of the vectors that
+        // hold any of the row) is reached by K elements; so is the least element
+        const int vecs = (to - lo + 7) / 8, busy = vecs < kTopkThreads ? vecs : kTopkThreads;
+        uint32_t from = K <= busy ? (most != 0 ? most : ~0u) : K <= vecs ? least_vec : least;
         topk_range(from, most, sh);
         int got;
         need = topk_select(

@@ -52,11 +52,10 @@ def _workspace(device, name: str, *sizes):
     return (_empty(n, torch.uint8, device) if n else None), n
 
 
-def _rows(shape) -> int:
-    n = 1
-    for s in shape:
-        n *= s
-    return n
+def _rows(t) -> int:
+    """Rows of t [..., d]."""
+    d = t.shape[-1]
+    return t.numel() // d if d else 0
 
 
 # ----------------------------------------------------------- teacher top-K --
@@ -70,7 +69,7 @@ def teacher_topk(logits, K: int, mask=None, teacher_form: int = CKL_TEACHER_LOGI
         raise ValueError("logits must be [..., V]")
     K = int(K)
     lead, V = logits.shape[:-1], logits.shape[-1]
-    T, dev = _rows(lead), logits.device
+    T, dev = _rows(logits), logits.device
     _check(dev, logits=logits)
     if mask is not None:
         _check(dev, mask=mask)
@@ -167,7 +166,7 @@ def act_encode(x):
     code = _dtype_code(x.dtype)
     codes, exps = _codes_for(x.shape[:-1], d, dev)
     lib = load_library()
-    _call(dev, lib.ckl_act_encode, _ptr(x), code, _rows(x.shape[:-1]), d, _ptr(codes), _ptr(exps))
+    _call(dev, lib.ckl_act_encode, _ptr(x), code, _rows(x), d, _ptr(codes), _ptr(exps))
     return codes, exps
 
 
@@ -189,7 +188,7 @@ def act_decode(codes, exps, rstd=None, weight=None, dtype=torch.bfloat16):
     code = _dtype_code(dtype)
     out = _empty(codes.shape, dtype, dev)
     lib = load_library()
-    _call(dev, lib.ckl_act_decode, _ptr(codes), _ptr(exps), _rows(lead), d, _ptr(rstd), _ptr(weight), w_code,
+    _call(dev, lib.ckl_act_decode, _ptr(codes), _ptr(exps), _rows(codes), d, _ptr(rstd), _ptr(weight), w_code,
           _ptr(out), code)
     return out
 
@@ -208,7 +207,7 @@ def norm_forward(x, weight, eps: float = 1e-6, save: bool = True):
         codes, exps = _codes_for(lead, d, dev)
         rstd = _empty(lead, torch.float32, dev)
     lib = load_library()
-    _call(dev, lib.ckl_norm_forward, _ptr(x), code, _rows(lead), d, _ptr(weight), w_code, eps, _ptr(y), _ptr(codes),
+    _call(dev, lib.ckl_norm_forward, _ptr(x), code, _rows(x), d, _ptr(weight), w_code, eps, _ptr(y), _ptr(codes),
           _ptr(exps), _ptr(rstd))
     return y, codes, exps, rstd
 
@@ -224,7 +223,7 @@ def norm_backward(dy, codes, exps, rstd, weight):
     if rstd.shape != lead or rstd.dtype != torch.float32:
         raise ValueError("rstd must be a float32 tensor of the rows' shape")
     code, w_code = _dtype_code(dy.dtype), _check_weight(weight, d)
-    T = _rows(lead)
+    T = _rows(codes)
     lib = load_library()
     ws, ws_bytes = _workspace(dev, "ckl_norm_workspace_size", T, d)
     dx = _empty(dy.shape, dy.dtype, dev)
