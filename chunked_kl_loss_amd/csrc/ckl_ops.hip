@@ -150,11 +150,16 @@ Units units(int64_t n) {
 // when lists fill up, their vectors are read again, one to a lane, and what is
 // wanted of them goes into a buffer in shared memory.  (Taking elements where
 // they are found costs each wave three times the common path's instructions
-// for one lane's sake: 245 us against 185 at 2048 x 201088.)  A filling buffer
+// for one lane's sake: 245 us against 170 at 2048 x 201088.)  A filling buffer
 // is cut as the first tile was, which raises the key.  Where too many elements
 // share one key for a cut by keys, a radix selection over the words decides by
 // index.  What remains is sorted.  The common path, per vector of eight: eight
 // exponentials, one running maximum and one comparison.
+//
+// Bound by memory where there are many rows: 2048 x 201088 bf16, K = 100, 169 us
+// or 4.9 TB/s (four workgroups to a compute unit, the next tile's loads under
+// way while one is looked at).  For one row the steps' latency counts: 32000
+// columns 17 us, of which 3 for the first key, 2 a tile, 2.5 for the order.
 constexpr int kTopkThreads = 256;
 constexpr int kTopkVecs = 4;                                 // vectors of eight a thread holds
 constexpr int kTopkStep = kTopkThreads * 8;                  // columns of one vector each
@@ -310,8 +315,9 @@ __device__ __forceinline__ void topk_cut_exact(uint64_t* buf, int n, int K, S& s
 }
 
 // Cuts the n > limit >= K words of buf to at most `limit` of the largest, at
-// least K, in any order.  Returns their number and sets *key to a key that at least K of them,
-// and none less, reach.  Begins and ends with a barrier.
+// least K, in any order.  Returns their number and sets *key to a key that at
+// least K of them, and none but them, reach.  Begins and ends with a barrier.
+// (3000 words to 1000: 5 us.)
 template <int CAP, typename S>
 __device__ __forceinline__ int topk_cut(uint64_t* buf, int n, int K, int limit, S& sh, uint32_t* key) {
   const int tid = threadIdx.x;
@@ -368,7 +374,8 @@ __device__ __forceinline__ uint32_t lane_xor(uint32_t x) {
     const int up = __builtin_amdgcn_update_dpp((int)x, (int)x, 0x104, 0xf, 0x5, false);
     return (uint32_t)__builtin_amdgcn_update_dpp(up, (int)x, 0x114, 0xf, 0xa, false);
   }
-  if constexpr (LANES == 8) return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x128, 0xf, 0xf, true);  // row turned by 8
+  if constexpr (LANES == 8)  // the row of 16 turned by 8
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x128, 0xf, 0xf, true);
   return (uint32_t)__shfl_xor((int)x, LANES);
 }
 
@@ -614,12 +621,10 @@ struct Raw8<float> {
 __host__ __device__ inline int topk_slots(int K) { return K + K / 8 + 32; }
 
 template <typename T, int CAP>
-__global__ __launch_bounds__(kTopkThreads, CAP <= 4096 ? 4 : 2) void topk_rows_kernel(const T* __restrict__ logits, int64_t rows, int V, int K,
-                                                                 int segments, int seg_cols, int logprob,
-                                                                 const uint8_t* __restrict__ mask,
-                                                                 int* __restrict__ idx, float* __restrict__ val,
-                                                                 float* __restrict__ lse, uint64_t* __restrict__ cand,
-                                                                 float2* __restrict__ state) {
+__global__ __launch_bounds__(kTopkThreads, CAP <= 4096 ? 4 : 2) void topk_rows_kernel(
+    const T* __restrict__ logits, int64_t rows, int V, int K, int segments, int seg_cols, int logprob,
+    const uint8_t* __restrict__ mask, int* __restrict__ idx, float* __restrict__ val, float* __restrict__ lse,
+    uint64_t* __restrict__ cand, float2* __restrict__ state) {
   __shared__ __attribute__((aligned(16))) uint64_t buf[CAP];
   __shared__ TopkShared<CAP <= 4096 ? 256 : 1024> sh;
   __shared__ uint32_t lists[kTopkThreads / 64][kTopkList];
@@ -846,12 +851,9 @@ __global__ __launch_bounds__(kTopkThreads, CAP <= 4096 ? 4 : 2) void topk_rows_k
 
 // The segments' words of a row, cut and sorted in the same way.
 template <int CAP>
-__global__ __launch_bounds__(kTopkThreads, CAP <= 4096 ? 4 : 2) void topk_merge_kernel(const uint64_t* __restrict__ cand,
-                                                                  const float2* __restrict__ state, int K,
-                                                                  int segments, int logprob,
-                                                                  const uint8_t* __restrict__ mask,
-                                                                  int* __restrict__ idx, float* __restrict__ val,
-                                                                  float* __restrict__ lse) {
+__global__ __launch_bounds__(kTopkThreads, CAP <= 4096 ? 4 : 2) void topk_merge_kernel(
+    const uint64_t* __restrict__ cand, const float2* __restrict__ state, int K, int segments, int logprob,
+    const uint8_t* __restrict__ mask, int* __restrict__ idx, float* __restrict__ val, float* __restrict__ lse) {
   __shared__ __attribute__((aligned(16))) uint64_t buf[CAP];
   __shared__ TopkShared<CAP <= 4096 ? 256 : 1024> sh;
   const int tid = threadIdx.x;
@@ -900,6 +902,7 @@ __global__ __launch_bounds__(kTopkThreads, CAP <= 4096 ? 4 : 2) void topk_merge_
 // ---------------------------------------------------------------- embedding --
 // out[t] = scale W[token_t - v_offset]; a zero row for a token outside the table.
 // A thread takes four vectors, their tokens and then their rows loaded together.
+// Bound by memory: 32768 x 2880 bf16 55 us, 4.7 TB/s.
 constexpr int kEmbedUnits = 4;
 template <typename T, typename I>
 __global__ __launch_bounds__(256) void embedding_forward_kernel(const T* __restrict__ W, int64_t V, int64_t v_offset,
@@ -955,7 +958,8 @@ __device__ __forceinline__ bool fill_instead(const Fill& fill) {
 }
 
 // Very few positions (a prompt): one launch.  Workgroup (t, y) looks for the
-// other positions of its token; the first of them adds their rows.
+// other positions of its token; the first of them adds their rows.  (200 x 2048
+// bf16 added to fp32: 4.5 us, ranking and summing in three launches 13.)
 constexpr int kFewMax = 256;
 template <typename T, typename G, typename I, bool ADD>
 __global__ __launch_bounds__(256) void embedding_few_kernel(const T* __restrict__ dY, const I* __restrict__ tokens,
@@ -1004,7 +1008,8 @@ __global__ __launch_bounds__(256) void embedding_few_kernel(const T* __restrict_
 
 // Few positions: each one's rank is counted directly, T^2 comparisons over the
 // whole GPU.  A workgroup ranks 16 positions; 64 slices share the keys, 16 at a
-// time.
+// time.  (4099 positions, 64 to a workgroup: 15 us; so, and with the zeros of 64
+// MB besides, 11.)
 constexpr int kRankMax = 8192;
 constexpr int kRankWaves = 16;
 constexpr int kRankRows = 16;
@@ -1062,6 +1067,7 @@ __global__ __launch_bounds__(64 * kRankWaves) void rank_sort_kernel(const I* __r
 // block of 1024 ROUNDS keys.  hist[block][digit] counts the keys of a block.
 // (Counting the next pass's digits while a pass scatters, by atomics, took
 // 40 us more than a launch of its own: frequent tokens meet on one counter.)
+// 32768 positions, 18 bits of key: two passes of 5 + 5 us, all latency.
 constexpr int kSortWaves = 16;
 constexpr int kSortBins = 512;
 
@@ -1177,7 +1183,9 @@ __global__ __launch_bounds__(64 * kSortWaves) void sort_scatter_kernel(
 // rows of a token are anywhere in dY).  Runs of one token inside the chunk are
 // final; a run that crosses a border leaves its sum in part[chunk][0] (it began
 // before the chunk) or part[chunk][1] (it begins here and goes on; the chunk is
-// then listed for the join).
+// then listed for the join).  Bound by memory: 32768 x 2880 bf16 (an eighth
+// padding, word frequencies) added to fp32 95 us, 4.7 TB/s; eight columns a
+// thread 106.
 constexpr int kSumBatch = 4;
 template <typename T, typename G, bool ADD>
 __global__ __launch_bounds__(256) void embedding_sum_kernel(const T* __restrict__ dY, const uint32_t* __restrict__ key,
@@ -1220,7 +1228,8 @@ __global__ __launch_bounds__(256) void embedding_sum_kernel(const T* __restrict_
           for (int x = 0; x < 4; ++x) sum[x] = ADD ? old[j][x] + scale * sum[x] : scale * sum[x];
           store4(dW + ((int64_t)k[j] * q.n + col) * 4, f32x4{sum[0], sum[1], sum[2], sum[3]});
         } else {
-          store4(part + ((2 * c + (from_before ? 0 : 1)) * (int64_t)q.n + col) * 4, f32x4{sum[0], sum[1], sum[2], sum[3]});
+          store4(part + ((2 * c + (from_before ? 0 : 1)) * (int64_t)q.n + col) * 4,
+                 f32x4{sum[0], sum[1], sum[2], sum[3]});
           if (!from_before && col == 0) joins[1 + atomicAdd(joins, 1u)] = (uint32_t)c;
         }
         from_before = false;
@@ -1234,7 +1243,8 @@ __global__ __launch_bounds__(256) void embedding_sum_kernel(const T* __restrict_
 // The runs that cross borders: the listed chunk, where one begins, and the
 // chunks that it goes on through.  A workgroup takes 64 vectors of columns of
 // one run; four slices share its chunks and are added in order, so the order of
-// the list does not matter.
+// the list does not matter.  (The same sums 5 us; with the run's end found by
+// binary search over the chunks 25.)
 template <typename G, bool ADD>
 __global__ __launch_bounds__(256) void embedding_join_kernel(const uint32_t* __restrict__ key, int chunk,
                                                              int64_t chunks, int nv, float scale, G* __restrict__ dW,
@@ -1293,12 +1303,14 @@ __global__ __launch_bounds__(1024) void zero_kernel(Fill fill) { fill_instead(fi
 // Blocks of 32 columns of a row share a power of two 2^(E - 127), the smallest
 // that brings the block's largest magnitude below 127.5, kept within 2^-126 and
 // 2^121 (127 steps of a larger one are no float); a code is the value divided
-// by it, rounded to the nearest whole number, ties to even, at most 127.  Multiplying by powers of two is exact, so a code depends on nothing
-// but its block, and a restored value (7 bits and a sign) is exact in bf16.
+// by it, rounded to the nearest whole number, ties to even, at most 127.
+// Multiplying by powers of two is exact, so a code depends on nothing but its
+// block, and a restored value (7 bits and a sign) is exact in bf16.
 // E = 255 marks a block that holds an infinity or a NaN: all of it restores to
 // NaN.
 //
-// A thread holds eight columns, four neighbouring lanes a block.
+// A thread holds eight columns, four neighbouring lanes a block.  Encoding and
+// decoding are bound by memory: 131072 x 2880 bf16 195 us each way, 5.8 TB/s.
 __device__ __forceinline__ uint32_t top_bits(const float* f) {
   uint32_t a = 0;
 #pragma unroll
@@ -1400,12 +1412,13 @@ __device__ __forceinline__ float group_sum(float x, float* slots) {
 }
 
 // y = x rstd weight with rstd = 1 / sqrt(mean x^2 + eps), and x in 8 bits for
-// the backward pass.  A workgroup takes a row at a time; a thread holds NV
-// vectors of eight columns (vector v of the row in thread v mod blockDim).
+// the backward pass.  A workgroup takes a row; a thread holds NV vectors of eight
+// columns (vector v of the row in thread v mod blockDim), so that the row is read
+// once.  Bound by memory: 32768 x 2880 bf16 84 us, 5.7 TB/s.
 template <typename T, int NV>
 __global__ __launch_bounds__(1024) void norm_forward_kernel(const T* __restrict__ x, int64_t rows, int nv,
-                                                            const void* __restrict__ weight, int weight_bf16, float eps,
-                                                            T* __restrict__ y, int8_t* __restrict__ codes,
+                                                            const void* __restrict__ weight, int weight_bf16,
+                                                            float eps, T* __restrict__ y, int8_t* __restrict__ codes,
                                                             uint8_t* __restrict__ exps, float* __restrict__ rstd) {
   __shared__ float slots[16];
   const int nb = (nv + 3) / 4;
@@ -1448,6 +1461,7 @@ __global__ __launch_bounds__(1024) void norm_forward_kernel(const T* __restrict_
 //   dx = rstd (dy w - n mean(dy w n)),   dw = sum over rows of dy n.
 // A workgroup walks rows blockIdx, blockIdx + gridDim, ... and keeps its
 // columns' share of dw in registers; norm_dweight_kernel adds the workgroups.
+// Bound by memory: 32768 x 2880 bf16 87 us, 5.5 TB/s.
 template <typename T, int NV>
 __global__ __launch_bounds__(1024) void norm_backward_kernel(const T* __restrict__ dy, int64_t rows, int nv,
                                                              const int8_t* __restrict__ codes,
@@ -1502,7 +1516,7 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(const T* __restrict
 // The workgroups' shares added: 16 lanes of four columns each and 64 slices of
 // the shares, the slices added in a fixed order.  (One thread per eight columns
 // walking all 1024 shares took 282 us at d = 2880, on two workgroups; this
-// takes 6 us.)
+// takes 8 us.)
 template <typename T>
 __global__ __launch_bounds__(1024) void norm_dweight_kernel(const float* __restrict__ part, int groups, int d,
                                                             T* __restrict__ dweight) {
@@ -1530,9 +1544,9 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // -------------------------------------------------------------- launchers --
 // Segments of whole tiles to a row: as many as make the call shortest when a
 // workgroup takes 2 us a tile by itself, all of them together read 5 bytes a
-// picosecond, and joining segments costs 8 us.  (us at bf16, K = 100: 300 rows
-// of 201088 in 1 / 3 segments 59 / 49; 500 rows of 32000 in 1 / 2 21 / 26; 700
-// rows of 100000 73 / 95.)
+// picosecond, and joining segments costs 8 us.  (us at bf16, K = 100, in 1 / 2 / 3
+// segments: 300 rows of 201088 59 / 51 / 48; 500 rows of 32000 21 / 27 / 27; 700
+// rows of 100000 45 / 63 / 64; one row of 201088 51 / 39 / 34, in 25 18.)
 void topk_plan(int64_t rows, int64_t V, int* segments, int64_t* seg_cols) {
   const int64_t tiles = cdiv(V + 7, kTopkTile);
   const double read_us = (double)rows * V * 2 / 5e6;
@@ -1561,8 +1575,8 @@ hipError_t launch_teacher_topk(const void* logits, int bf16, int64_t rows, int64
   auto go = [&](auto* p, auto cap) {
     using E = std::remove_const_t<std::remove_pointer_t<decltype(p)>>;
     constexpr int CAP = decltype(cap)::value;
-    topk_rows_kernel<E, CAP><<<blocks, kTopkThreads, 0, st>>>(p, rows, (int)V, K, segments, (int)seg_cols, logprob, mask, idx, val, lse,
-                                                             cand, state);
+    topk_rows_kernel<E, CAP><<<blocks, kTopkThreads, 0, st>>>(p, rows, (int)V, K, segments, (int)seg_cols, logprob,
+                                                              mask, idx, val, lse, cand, state);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || segments == 1) return e;
     topk_merge_kernel<CAP><<<(unsigned)rows, kTopkThreads, 0, st>>>(cand, state, K, segments, logprob, mask, idx, val,
@@ -1658,7 +1672,8 @@ static hipError_t embedding_radix(const I* tokens, int64_t T, int64_t V, int64_t
     const int from = i & 1, shift = i * w.digit_bits;
     fill.first = (int)blocks;
     sort_hist_kernel<I, ROUNDS><<<blocks + (i ? 0 : fill_blocks(fill.n)), threads, 0, st>>>(
-        i ? nullptr : tokens, T, V, v_offset, 1 << w.digit_bits, shift, k[from], hist, (uint32_t*)(ws + w.joins), fill);
+        i ? nullptr : tokens, T, V, v_offset, 1 << w.digit_bits, shift, k[from], hist, (uint32_t*)(ws + w.joins),
+        fill);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     sort_scatter_kernel<ROUNDS><<<blocks, threads, 0, st>>>(k[from], i ? p[from] : nullptr, T, shift, w.digit_bits,
@@ -1680,7 +1695,8 @@ static hipError_t embedding_sort(const I* tokens, int64_t T, int64_t V, int64_t 
   *pos = (uint32_t*)(ws + w.pos0);
   fill.first = (int)cdiv(T, kRankRows);
   rank_sort_kernel<<<(unsigned)fill.first + fill_blocks(fill.n), 64 * kRankWaves, 0, st>>>(
-      tokens, (int)T, V, v_offset, (uint32_t*)(ws + w.key0), (uint32_t*)(ws + w.pos0), (uint32_t*)(ws + w.joins), fill);
+      tokens, (int)T, V, v_offset, (uint32_t*)(ws + w.key0), (uint32_t*)(ws + w.pos0), (uint32_t*)(ws + w.joins),
+      fill);
   return hipGetLastError();
 }
 
@@ -1756,6 +1772,9 @@ hipError_t launch_act_decode(const int8_t* codes, const uint8_t* exps, int64_t T
   return hipGetLastError();
 }
 
+template <int N>
+using Count = std::integral_constant<int, N>;
+
 // Threads and vectors per thread for rows of nv vectors.  Two vectors a thread
 // have the loads in flight that one has in twice the threads, and half the waves
 // to wait for at the row's sum.  (32768 x 2880 bf16, forward: one vector in 384
@@ -1774,12 +1793,11 @@ hipError_t launch_norm_forward(const void* x, int bf16, int64_t T, int d, const 
   const unsigned blocks = (unsigned)T;
   auto go = [&](auto* p) {
     using E = std::remove_const_t<std::remove_pointer_t<decltype(p)>>;
-    switch (per) {
-      case 1: norm_forward_kernel<E, 1><<<blocks, threads, 0, st>>>(p, T, nv, weight, weight_bf16, eps, (E*)y, codes, exps, rstd); break;
-      case 2: norm_forward_kernel<E, 2><<<blocks, threads, 0, st>>>(p, T, nv, weight, weight_bf16, eps, (E*)y, codes, exps, rstd); break;
-      case 4: norm_forward_kernel<E, 4><<<blocks, threads, 0, st>>>(p, T, nv, weight, weight_bf16, eps, (E*)y, codes, exps, rstd); break;
-      default: norm_forward_kernel<E, 8><<<blocks, threads, 0, st>>>(p, T, nv, weight, weight_bf16, eps, (E*)y, codes, exps, rstd);
-    }
+    auto run = [&](auto n) {
+      norm_forward_kernel<E, decltype(n)::value>
+          <<<blocks, threads, 0, st>>>(p, T, nv, weight, weight_bf16, eps, (E*)y, codes, exps, rstd);
+    };
+    per == 1 ? run(Count<1>{}) : per == 2 ? run(Count<2>{}) : per == 4 ? run(Count<4>{}) : run(Count<8>{});
   };
   if (bf16)
     go((const bf16_t*)x);
@@ -1805,12 +1823,11 @@ hipError_t launch_norm_backward(const void* dy, int bf16, int64_t T, int d, cons
   const unsigned groups = (unsigned)norm_backward_groups(T, d);
   auto go = [&](auto* p) {
     using E = std::remove_const_t<std::remove_pointer_t<decltype(p)>>;
-    switch (per) {
-      case 1: norm_backward_kernel<E, 1><<<groups, threads, 0, st>>>(p, T, nv, codes, exps, rstd, weight, weight_bf16, (E*)dx, part); break;
-      case 2: norm_backward_kernel<E, 2><<<groups, threads, 0, st>>>(p, T, nv, codes, exps, rstd, weight, weight_bf16, (E*)dx, part); break;
-      case 4: norm_backward_kernel<E, 4><<<groups, threads, 0, st>>>(p, T, nv, codes, exps, rstd, weight, weight_bf16, (E*)dx, part); break;
-      default: norm_backward_kernel<E, 8><<<groups, threads, 0, st>>>(p, T, nv, codes, exps, rstd, weight, weight_bf16, (E*)dx, part);
-    }
+    auto run = [&](auto n) {
+      norm_backward_kernel<E, decltype(n)::value>
+          <<<groups, threads, 0, st>>>(p, T, nv, codes, exps, rstd, weight, weight_bf16, (E*)dx, part);
+    };
+    per == 1 ? run(Count<1>{}) : per == 2 ? run(Count<2>{}) : per == 4 ? run(Count<4>{}) : run(Count<8>{});
   };
   if (groups > 0) {
     if (bf16)

@@ -25,7 +25,9 @@ import sys
 
 CLASSES = (("fwd_lse", "fwd_lse"), ("bwd_grad", "bwd_grad"), ("gemm_store", "gemm_dhdw"),
            ("gpass", "g_pass"), ("transpose", "transpose"), ("teacher_prep", "teacher_prep"),
-           ("fwd_finalize", "fwd_finalize"), ("loss_reduce", "fwd_finalize"))
+           ("fwd_finalize", "fwd_finalize"), ("loss_reduce", "fwd_finalize"), ("topk_", "topk"),
+           ("embedding_", "embedding"), ("rank_sort", "embedding"), ("sort_hist", "embedding"),
+           ("sort_scatter", "embedding"), ("act_", "activation"), ("norm_", "activation"))
 
 
 def kernel_class(name: str) -> str:
