@@ -128,9 +128,8 @@ class Embedding(torch.autograd.Function):
 class RMSNorm8Bit(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, eps: float = 1e-6):
-        y, codes, exps, rstd = ops.norm_forward(x, weight, eps, save=any(ctx.needs_input_grad))
-        if codes is not None:
-            ctx.save_for_backward(codes, exps, rstd, weight)
+        y, codes, exps, rstd = ops.norm_forward(x, weight, eps)
+        ctx.save_for_backward(codes, exps, rstd, weight)
         return y
 
     @staticmethod
@@ -144,14 +143,20 @@ class RMSNorm8Bit(torch.autograd.Function):
 def embedding(W, tokens, scale: float = 1.0):
     """scale * W[tokens], differentiable with respect to the table W [V, d] (the output head's, when tied).
     tokens: int32 / int64 of any shape; a token outside [0, V) gives a zero row and no gradient."""
-    return Embedding.apply(W.contiguous(), tokens.contiguous(), scale)
+    W, tokens = W.contiguous(), tokens.contiguous()
+    if not (W.requires_grad and torch.is_grad_enabled()):
+        return ops.embedding_forward(W, tokens, scale)
+    return Embedding.apply(W, tokens, scale)
 
 
 def rms_norm_8bit(x, weight, eps: float = 1e-6):
     """RMS norm of the last dimension, differentiable with respect to x [..., d] and weight [d].  The output is
     that of the exact x; the backward pass reads x from 8 bits (ops.act_encode), so that the norm keeps d bytes a
     row instead of x."""
-    return RMSNorm8Bit.apply(x.contiguous(), weight.contiguous(), eps)
+    x, weight = x.contiguous(), weight.contiguous()
+    if not ((x.requires_grad or weight.requires_grad) and torch.is_grad_enabled()):
+        return ops.norm_forward(x, weight, eps, save=False)[0]
+    return RMSNorm8Bit.apply(x, weight, eps)
 
 
 def chunked_kl_loss(H, W, idx, tlogit, mask=None, chunk: int = 2048, fused: bool = False, teacher_form: int = 0,

@@ -3,7 +3,8 @@ its gradient, activations in 8 bits and the RMS norm that saves its input so.
 
 Argument marshalling over include/ckl.h, as in _binding.  Leading dimensions
 are rows; tensors are contiguous and on one GPU.  Calls run on that GPU's
-current stream."""
+current stream.  Small calls are bound by this layer, so it does little: one
+pass over the arguments, the outputs, the call."""
 from __future__ import annotations
 
 import ctypes
@@ -11,21 +12,46 @@ import functools
 
 import torch
 
-from ._binding import CKL_TEACHER_LOGITS, _dtype_code, _empty, _ptr, check, load_library
+from . import _binding
+from ._binding import CKL_BF16, CKL_F32, CKL_TEACHER_LOGITS, check, load_library
 
 ACT_BLOCK = 32  # columns that share an exponent (CKL_ACT_BLOCK)
 
+_CODES = {torch.bfloat16: CKL_BF16, torch.float32: CKL_F32}
 _TOKEN_BYTES = {torch.int32: 4, torch.int64: 8}
 
 
-def _check(device, **tensors) -> None:
-    for name, t in tensors.items():
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a GPU tensor")
-        if t.device != device:
-            raise ValueError(f"{name} must be on {device}, not {t.device}")
+def _code(dtype) -> int:
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}; use torch.bfloat16 or torch.float32")
+    return code
+
+
+def _token_bytes(tokens) -> int:
+    nb = _TOKEN_BYTES.get(tokens.dtype)
+    if nb is None:
+        raise TypeError("tokens must be int32 or int64")
+    return nb
+
+
+def _check(names, *tensors):
+    """The device of the tensors, which must be contiguous and on one GPU."""
+    device = tensors[0].device
+    for name, t in zip(names, tensors):
+        if t.device != device or not t.is_cuda:
+            raise ValueError(f"{name} must be a GPU tensor on {device if device.type == 'cuda' else 'a GPU'}, "
+                             f"not on {t.device}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
+    return device
+
+
+def _new(shape, dtype, device):
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if _binding.FILL_BYTE is not None and t.numel() > 0:
+        t.view(torch.uint8).fill_(int(_binding.FILL_BYTE))
+    return t
 
 
 def _call(device, fn, *args) -> None:
@@ -34,10 +60,12 @@ def _call(device, fn, *args) -> None:
     index = device.index
     if index == torch.cuda.current_device():
         # (the raw handle: a Stream object costs as much as a launch)
-        check(fn(*args, torch._C._cuda_getCurrentRawStream(index)))
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
-            check(fn(*args, torch._C._cuda_getCurrentRawStream(index)))
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status:
+        check(status)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -48,8 +76,12 @@ def _workspace_bytes(name: str, *sizes) -> int:
 
 
 def _workspace(device, name: str, *sizes):
+    """A workspace (None where the call needs none), its address and its bytes."""
     n = _workspace_bytes(name, *sizes)
-    return (_empty(n, torch.uint8, device) if n else None), n
+    if not n:
+        return None, None, 0
+    ws = _new(n, torch.uint8, device)
+    return ws, ws.data_ptr(), n
 
 
 def _rows(t) -> int:
@@ -69,43 +101,34 @@ def teacher_topk(logits, K: int, mask=None, teacher_form: int = CKL_TEACHER_LOGI
         raise ValueError("logits must be [..., V]")
     K = int(K)
     lead, V = logits.shape[:-1], logits.shape[-1]
-    T, dev = _rows(logits), logits.device
-    _check(dev, logits=logits)
-    if mask is not None:
-        _check(dev, mask=mask)
+    if mask is None:
+        dev, mask_ptr = _check(("logits",), logits), None
+    else:
+        dev, mask_ptr = _check(("logits", "mask"), logits, mask), mask.data_ptr()
         if mask.shape != lead or mask.dtype not in (torch.uint8, torch.bool):
             raise ValueError("mask must be a uint8/bool tensor of the logits' leading shape")
-    code = _dtype_code(logits.dtype)
-    lib = load_library()
-    ws, ws_bytes = _workspace(dev, "ckl_topk_workspace_size", T, V, K)
-    idx = _empty((*lead, K), torch.int32, dev)
-    values = _empty((*lead, K), torch.float32, dev)
-    lse = _empty(lead, torch.float32, dev)
-    _call(dev, lib.ckl_teacher_topk, _ptr(logits), code, T, V, K, teacher_form, _ptr(mask), _ptr(idx), _ptr(values),
-          _ptr(lse), _ptr(ws), ws_bytes)
+    T, code = _rows(logits), _code(logits.dtype)
+    ws, ws_ptr, ws_bytes = _workspace(dev, "ckl_topk_workspace_size", T, V, K)
+    idx = _new((*lead, K), torch.int32, dev)
+    values = _new((*lead, K), torch.float32, dev)
+    lse = _new(lead, torch.float32, dev)
+    _call(dev, load_library().ckl_teacher_topk, logits.data_ptr(), code, T, V, K, teacher_form, mask_ptr,
+          idx.data_ptr(), values.data_ptr(), lse.data_ptr(), ws_ptr, ws_bytes)
     return idx, values, lse
 
 
 # --------------------------------------------------------------- embedding --
-def _token_bytes(tokens) -> int:
-    if tokens.dtype not in _TOKEN_BYTES:
-        raise TypeError("tokens must be int32 or int64")
-    return _TOKEN_BYTES[tokens.dtype]
-
-
 def embedding_forward(W, tokens, scale: float = 1.0, v_offset: int = 0):
     """scale * W[tokens - v_offset] as [*tokens.shape, d] in W's dtype; a zero row for a token outside
     [v_offset, v_offset + V) (padding, or another shard's)."""
     if W.dim() != 2:
         raise ValueError("W must be [V, d]")
-    dev = W.device
-    _check(dev, W=W, tokens=tokens)
-    nb, code = _token_bytes(tokens), _dtype_code(W.dtype)
+    dev = _check(("W", "tokens"), W, tokens)
+    nb, code = _token_bytes(tokens), _code(W.dtype)
     V, d = W.shape
-    out = _empty((*tokens.shape, d), W.dtype, dev)
-    lib = load_library()
-    _call(dev, lib.ckl_embedding_forward, _ptr(W), code, V, d, v_offset, _ptr(tokens), nb, tokens.numel(), scale,
-          _ptr(out))
+    out = _new((*tokens.shape, d), W.dtype, dev)
+    _call(dev, load_library().ckl_embedding_forward, W.data_ptr(), code, V, d, v_offset, tokens.data_ptr(), nb,
+          tokens.numel(), scale, out.data_ptr())
     return out
 
 
@@ -115,26 +138,23 @@ def embedding_backward(dY, tokens, V: int, scale: float = 1.0, v_offset: int = 0
     returned, and rows without a token are not touched."""
     if dY.dim() < 1 or dY.shape[:-1] != tokens.shape:
         raise ValueError("dY must be [*tokens.shape, d]")
-    dev, d = dY.device, dY.shape[-1]
-    _check(dev, dY=dY, tokens=tokens)
-    nb, code = _token_bytes(tokens), _dtype_code(dY.dtype)
-    if add_to is not None:
-        _check(dev, add_to=add_to)
+    d = dY.shape[-1]
+    if add_to is None:
+        dev = _check(("dY", "tokens"), dY, tokens)
+        dw_dtype = torch.float32 if dw_dtype is None else dw_dtype
+    else:
+        dev = _check(("dY", "tokens", "add_to"), dY, tokens, add_to)
         if add_to.shape != (V, d):
             raise ValueError("add_to must be [V, d]")
         if dw_dtype is not None and dw_dtype != add_to.dtype:
             raise TypeError("dw_dtype differs from add_to's")
-        dW, dw_code = add_to, _dtype_code(add_to.dtype)
-    else:
-        dw_dtype = torch.float32 if dw_dtype is None else dw_dtype
-        dw_code = _dtype_code(dw_dtype)
+        dw_dtype = add_to.dtype
+    nb, code, dw_code = _token_bytes(tokens), _code(dY.dtype), _code(dw_dtype)
     T = tokens.numel()
-    lib = load_library()
-    ws, ws_bytes = _workspace(dev, "ckl_embedding_workspace_size", T, d, V)
-    if add_to is None:
-        dW = _empty((V, d), dw_dtype, dev)
-    _call(dev, lib.ckl_embedding_backward, _ptr(dY), code, T, d, _ptr(tokens), nb, V, v_offset, scale, _ptr(dW),
-          dw_code, int(add_to is not None), _ptr(ws), ws_bytes)
+    ws, ws_ptr, ws_bytes = _workspace(dev, "ckl_embedding_workspace_size", T, d, V)
+    dW = _new((V, d), dw_dtype, dev) if add_to is None else add_to
+    _call(dev, load_library().ckl_embedding_backward, dY.data_ptr(), code, T, d, tokens.data_ptr(), nb, V, v_offset,
+          scale, dW.data_ptr(), dw_code, int(add_to is not None), ws_ptr, ws_bytes)
     return dW
 
 
@@ -146,14 +166,15 @@ def _check_codes(codes, exps):
         raise ValueError("exps must be [..., ceil(d / 32)] for codes [..., d]")
 
 
-def _check_weight(weight, d):
+def _check_rstd(rstd, lead):
+    if rstd.shape != lead or rstd.dtype != torch.float32:
+        raise ValueError("rstd must be a float32 tensor of the rows' shape")
+
+
+def _weight_code(weight, d) -> int:
     if weight.shape != (d,):
         raise ValueError("weight must be [d]")
-    return _dtype_code(weight.dtype)
-
-
-def _codes_for(lead, d, dev):
-    return (_empty((*lead, d), torch.int8, dev), _empty((*lead, -(-d // ACT_BLOCK)), torch.uint8, dev))
+    return _code(weight.dtype)
 
 
 def act_encode(x):
@@ -161,35 +182,31 @@ def act_encode(x):
     for code * 2^(E - 127) with the E of its 32 columns: within max|x| / 127.5 of x over them."""
     if x.dim() < 1:
         raise ValueError("x must be [..., d]")
-    dev, d = x.device, x.shape[-1]
-    _check(dev, x=x)
-    code = _dtype_code(x.dtype)
-    codes, exps = _codes_for(x.shape[:-1], d, dev)
-    lib = load_library()
-    _call(dev, lib.ckl_act_encode, _ptr(x), code, _rows(x), d, _ptr(codes), _ptr(exps))
+    dev, shape, code = _check(("x",), x), x.shape, _code(x.dtype)
+    d = shape[-1]
+    codes = _new(shape, torch.int8, dev)
+    exps = _new((*shape[:-1], -(-d // ACT_BLOCK)), torch.uint8, dev)
+    _call(dev, load_library().ckl_act_encode, x.data_ptr(), code, _rows(x), d, codes.data_ptr(), exps.data_ptr())
     return codes, exps
 
 
 def act_decode(codes, exps, rstd=None, weight=None, dtype=torch.bfloat16):
     """The values the codes stand for (exact in bf16 and fp32); with rstd [...] and weight [d], the RMS norm's
     output rebuilt from them: value * rstd * weight, rounded once."""
-    dev = codes.device
-    _check(dev, codes=codes, exps=exps)
-    _check_codes(codes, exps)
-    lead, d = codes.shape[:-1], codes.shape[-1]
     if (rstd is None) != (weight is None):
         raise ValueError("rstd and weight go together")
-    w_code = 0
-    if rstd is not None:
-        _check(dev, rstd=rstd, weight=weight)
-        w_code = _check_weight(weight, d)
-        if rstd.shape != lead or rstd.dtype != torch.float32:
-            raise ValueError("rstd must be a float32 tensor of the rows' shape")
-    code = _dtype_code(dtype)
-    out = _empty(codes.shape, dtype, dev)
-    lib = load_library()
-    _call(dev, lib.ckl_act_decode, _ptr(codes), _ptr(exps), _rows(codes), d, _ptr(rstd), _ptr(weight), w_code,
-          _ptr(out), code)
+    code, rstd_ptr, weight_ptr, w_code = _code(dtype), None, None, 0
+    if rstd is None:
+        dev = _check(("codes", "exps"), codes, exps)
+        _check_codes(codes, exps)
+    else:
+        dev = _check(("codes", "exps", "rstd", "weight"), codes, exps, rstd, weight)
+        _check_codes(codes, exps)
+        _check_rstd(rstd, codes.shape[:-1])
+        rstd_ptr, weight_ptr, w_code = rstd.data_ptr(), weight.data_ptr(), _weight_code(weight, codes.shape[-1])
+    out = _new(codes.shape, dtype, dev)
+    _call(dev, load_library().ckl_act_decode, codes.data_ptr(), exps.data_ptr(), _rows(codes), codes.shape[-1],
+          rstd_ptr, weight_ptr, w_code, out.data_ptr(), code)
     return out
 
 
@@ -198,36 +215,36 @@ def norm_forward(x, weight, eps: float = 1e-6, save: bool = True):
     8 bits for norm_backward; save=False: y alone is computed and the others are None."""
     if x.dim() < 1:
         raise ValueError("x must be [..., d]")
-    dev, lead, d = x.device, x.shape[:-1], x.shape[-1]
-    _check(dev, x=x, weight=weight)
-    code, w_code = _dtype_code(x.dtype), _check_weight(weight, d)
-    y = _empty(x.shape, x.dtype, dev)
-    codes = exps = rstd = None
+    dev, shape, code = _check(("x", "weight"), x, weight), x.shape, _code(x.dtype)
+    d = shape[-1]
+    w_code = _weight_code(weight, d)
+    y = _new(shape, x.dtype, dev)
     if save:
-        codes, exps = _codes_for(lead, d, dev)
-        rstd = _empty(lead, torch.float32, dev)
-    lib = load_library()
-    _call(dev, lib.ckl_norm_forward, _ptr(x), code, _rows(x), d, _ptr(weight), w_code, eps, _ptr(y), _ptr(codes),
-          _ptr(exps), _ptr(rstd))
+        codes = _new(shape, torch.int8, dev)
+        exps = _new((*shape[:-1], -(-d // ACT_BLOCK)), torch.uint8, dev)
+        rstd = _new(shape[:-1], torch.float32, dev)
+        saved = codes.data_ptr(), exps.data_ptr(), rstd.data_ptr()
+    else:
+        codes = exps = rstd = None
+        saved = None, None, None
+    _call(dev, load_library().ckl_norm_forward, x.data_ptr(), code, _rows(x), d, weight.data_ptr(), w_code, eps,
+          y.data_ptr(), *saved)
     return y, codes, exps, rstd
 
 
 def norm_backward(dy, codes, exps, rstd, weight):
     """Gradients (dx in dy's dtype, dweight in weight's) of the norm from what norm_forward saved."""
-    dev = dy.device
-    _check(dev, dy=dy, codes=codes, exps=exps, rstd=rstd, weight=weight)
+    dev = _check(("dy", "codes", "exps", "rstd", "weight"), dy, codes, exps, rstd, weight)
     _check_codes(codes, exps)
-    lead, d = codes.shape[:-1], codes.shape[-1]
-    if dy.shape != codes.shape:
+    shape = codes.shape
+    if dy.shape != shape:
         raise ValueError("dy must have the codes' shape")
-    if rstd.shape != lead or rstd.dtype != torch.float32:
-        raise ValueError("rstd must be a float32 tensor of the rows' shape")
-    code, w_code = _dtype_code(dy.dtype), _check_weight(weight, d)
-    T = _rows(codes)
-    lib = load_library()
-    ws, ws_bytes = _workspace(dev, "ckl_norm_workspace_size", T, d)
-    dx = _empty(dy.shape, dy.dtype, dev)
-    dweight = _empty(d, weight.dtype, dev)
-    _call(dev, lib.ckl_norm_backward, _ptr(dy), code, T, d, _ptr(codes), _ptr(exps), _ptr(rstd), _ptr(weight), w_code,
-          _ptr(dx), _ptr(dweight), _ptr(ws), ws_bytes)
+    _check_rstd(rstd, shape[:-1])
+    d, T, code = shape[-1], _rows(codes), _code(dy.dtype)
+    w_code = _weight_code(weight, d)
+    ws, ws_ptr, ws_bytes = _workspace(dev, "ckl_norm_workspace_size", T, d)
+    dx = _new(shape, dy.dtype, dev)
+    dweight = _new(weight.shape, weight.dtype, dev)
+    _call(dev, load_library().ckl_norm_backward, dy.data_ptr(), code, T, d, codes.data_ptr(), exps.data_ptr(),
+          rstd.data_ptr(), weight.data_ptr(), w_code, dx.data_ptr(), dweight.data_ptr(), ws_ptr, ws_bytes)
     return dx, dweight
