@@ -32,8 +32,8 @@ def normal(shape, dtype, seed, std=1.0):
 
 
 def same_bits(a, b):
-    return a.shape == b.shape and a.dtype == b.dtype and torch.equal(a.contiguous().view(torch.uint8),
-                                                                     b.contiguous().view(torch.uint8))
+    return a.shape == b.shape and a.dtype == b.dtype and torch.equal(a.contiguous().reshape(-1).view(torch.uint8),
+                                                                     b.contiguous().reshape(-1).view(torch.uint8))
 
 
 # ----------------------------------------------------------- teacher top-K --
@@ -255,6 +255,21 @@ def check_embedding_grad(T, V, d, kind, dtype, grad, add, scale=1.5, off=0, tok_
 def test_embedding_grad_lengths(T, kind):
     check_embedding_grad(T, 1000, 24, kind, "bf16", "f32", add=T % 2 == 0)
     check_embedding_grad(T, 513, 64, kind, "f32", "bf16", add=T % 2 == 1, tok_dtype=torch.int32)
+
+
+@pytest.mark.parametrize("kind", ["zipf", "one", "padded"])
+@pytest.mark.parametrize("T", [127, 255, 256, 257, 272, 513])
+def test_embedding_grad_where_the_way_changes(T, kind):
+    # up to 256 positions in one launch, ranked beyond; every type, several workgroups to a row
+    for dtype, grad in (("bf16", "f32"), ("bf16", "bf16"), ("f32", "f32"), ("f32", "bf16")):
+        check_embedding_grad(T, 300, 2056, kind, dtype, grad, add=dtype == grad, tok_dtype=torch.int32)
+        check_embedding_grad(T, 300, 8, kind, dtype, grad, add=dtype != grad)
+
+
+def test_embedding_grad_of_one_token_many_times():
+    # one run through hundreds of chunks, and one that ends with the last chunk
+    check_embedding_grad(70000, 5, 520, "one", "bf16", "f32", add=True)
+    check_embedding_grad(65536, 1, 16, "uniform", "f32", "bf16", add=False)
 
 
 @pytest.mark.parametrize("V", [1, 2, 511, 512, 32000, 262143, 262144, 300000])
@@ -595,7 +610,7 @@ def step_inputs(seed, T, V=700, d=64):
             torch.zeros(V, d, device="cuda"))
 
 
-@pytest.mark.parametrize("T", [5, 9000])
+@pytest.mark.parametrize("T", [5, 600, 9000])
 def test_captured_step_replays_with_new_inputs(T):
     ins = step_inputs(1, T)
     side = torch.cuda.Stream()
@@ -611,6 +626,42 @@ def test_captured_step_replays_with_new_inputs(T):
         for a, b in zip(ins[:4], new[:4]):
             a.copy_(b)
         want = [t.clone() for t in step(*new)]   # eager work between the replays
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(outs, want):
+            assert same_bits(a, b)
+
+
+def test_captured_gradients_replay_with_new_inputs():
+    # forward and backward through autograd in one graph; the leaves have no other graph alive
+    T, d, V, K = 300, 72, 500, 9
+
+    def inputs(seed):
+        idx, vals, _ = ckl.teacher_topk(normal((T, V), torch.bfloat16, seed, 2.0).cuda(), K)
+        return [normal((V, d), torch.bfloat16, seed + 1, 0.2).cuda(), tokens_of("padded", T, V, seed + 2).cuda(),
+                (1 + normal((d,), torch.bfloat16, seed + 3, 0.1)).cuda(), idx, vals]
+
+    def grads(W, tok, nw, idx, vals):
+        W, nw = W.detach().requires_grad_(True), nw.detach().requires_grad_(True)
+        x = ckl.embedding(W, tok, 4.0)
+        loss = ckl.chunked_kl_loss(x, W, idx, vals, chunk=128, save_8bit=True, norm_weight=nw)
+        more = ckl.rms_norm_8bit(x, nw).float().sum()
+        return [loss.detach(), *torch.autograd.grad(loss + 0.01 * more, (W, nw))]
+    ins = inputs(1)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        grads(*ins)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = grads(*ins)
+    for seed in (1, 40, 80, 40):
+        new = inputs(seed)
+        for a, b in zip(ins, new):
+            a.copy_(b)
+        want = grads(*new)
         torch.cuda.synchronize()
         graph.replay()
         torch.cuda.synchronize()
