@@ -128,16 +128,16 @@ class Embedding(torch.autograd.Function):
 class RMSNorm8Bit(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, eps: float = 1e-6):
-        y, codes, exps, rstd = ops.norm_forward(x, weight, eps)
-        ctx.save_for_backward(codes, exps, rstd, weight)
+        y, saved = ops.norm_forward_saving(x, weight, eps)
+        ctx.save_for_backward(saved, weight)
         return y
 
     @staticmethod
     @once_differentiable
     def backward(ctx, grad):
-        codes, exps, rstd, weight = ctx.saved_tensors
-        dx, dweight = ops.norm_backward(grad.contiguous(), codes, exps, rstd, weight)
-        return (dx if ctx.needs_input_grad[0] else None), (dweight if ctx.needs_input_grad[1] else None), None
+        saved, weight = ctx.saved_tensors
+        dx, dweight = ops.norm_backward_saved(grad.contiguous(), saved, weight)
+        return dx, dweight, None
 
 
 def embedding(W, tokens, scale: float = 1.0):

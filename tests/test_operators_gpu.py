@@ -466,6 +466,30 @@ def test_norm_rows_of_zeros_nan_and_none():
     assert y.shape == dx.shape == (0, 72) and not dw.any()
 
 
+@pytest.mark.parametrize("lead,d", [((1,), 8), ((3,), 24), ((5, 7), 520), ((0,), 72), ((2, 0), 8), ((13,), 8200)])
+@pytest.mark.parametrize("dtype,wtype", [("bf16", "f32"), ("f32", "bf16")])
+def test_norm_autograd_is_the_direct_calls(lead, d, dtype, wtype):
+    # what is saved lies in one tensor, at offsets that depend on the rows: the same bits all the same
+    x, dy = normal((*lead, d), DT[dtype], 1).cuda(), normal((*lead, d), DT[dtype], 2).cuda()
+    w = normal((d,), DT[wtype], 3).cuda()
+    y, codes, exps, rstd = ckl.norm_forward(x, w, 1e-5)
+    dx, dw = ckl.norm_backward(dy, codes, exps, rstd, w)
+    X, Wt = x.clone().requires_grad_(), w.clone().requires_grad_()
+    out = ckl.rms_norm_8bit(X, Wt, 1e-5)
+    assert same_bits(out.detach(), y)
+    for _ in range(2):  # the saved tensor outlives a backward pass that retains it
+        a, b = torch.autograd.grad(out, (X, Wt), dy, retain_graph=True)
+        assert same_bits(a, dx) and same_bits(b, dw)
+    only, = torch.autograd.grad(ckl.rms_norm_8bit(X, w, 1e-5), (X,), dy)
+    assert same_bits(only, dx)
+    only, = torch.autograd.grad(ckl.rms_norm_8bit(x, Wt, 1e-5), (Wt,), dy)
+    assert same_bits(only, dw)
+    one = torch.ones((), dtype=DT[dtype], device="cuda").expand(*lead, d)  # a gradient with strides of zero
+    a, b = torch.autograd.grad(out, (X, Wt), one)
+    dx, dw = ckl.norm_backward(one.contiguous(), codes, exps, rstd, w)
+    assert same_bits(a, dx) and same_bits(b, dw)
+
+
 def test_norm_gradient_against_differences():
     # x on the codes' grid: the 8-bit form is exact, so the gradient is that of the norm itself
     T, d = 5, 72
