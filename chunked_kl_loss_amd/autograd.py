@@ -198,6 +198,9 @@ def chunked_kl_loss(H, W, idx, tlogit, mask=None, chunk: int = 2048, fused: bool
         H = rms_norm_8bit(H, norm_weight, norm_eps)
     if save_8bit and not fused:
         nw = None if norm_weight is None else norm_weight.contiguous()
+        if not torch.is_grad_enabled():  # nothing is saved (a Function sees the leaves' requires_grad all the same)
+            H = H if nw is None else ops.norm_forward(H, nw, norm_eps, save=False)[0]
+            return ChunkedKLLoss.apply(H, W, idx, tlogit, mask, chunk, teacher_form)
         return ChunkedKLLoss8Bit.apply(H, W, idx, tlogit, mask, chunk, teacher_form, nw, norm_eps)
     if fused:
         return FusedChunkedKLLoss.apply(H, W, idx, tlogit, mask, chunk, teacher_form, dw_group_rows)

@@ -13,6 +13,7 @@ import torch
 
 import chunked_kl_loss_amd as ckl
 from chunked_kl_loss_amd import _binding as B
+from chunked_kl_loss_amd import ops
 
 pytestmark = pytest.mark.gpu
 
@@ -571,6 +572,21 @@ def test_loss_with_the_norm_before_the_head(dtype):
     only = nw.clone().requires_grad_(True)
     ckl.chunked_kl_loss(X, W, idx, tl, mask, chunk=128, save_8bit=True, norm_weight=only, norm_eps=1e-5).backward()
     assert same_bits(only.grad, dn)
+
+
+@pytest.mark.parametrize("norm", [False, True])
+def test_loss_without_a_backward_pass_saves_nothing(norm, monkeypatch):
+    X, W, idx, tl, mask = loss_inputs(seed=21)
+    nw = (1 + normal((72,), torch.float32, 9, 0.2)).cuda().requires_grad_(True) if norm else None
+    leaves = [t.clone().requires_grad_(True) for t in (X, W)]
+    loss = ckl.chunked_kl_loss(*leaves, idx, tl, mask, chunk=128, save_8bit=True, norm_weight=nw)
+    forward, saves = ops.norm_forward, []
+    monkeypatch.setattr(ops, "act_encode", lambda x: saves.append("encode"))
+    monkeypatch.setattr(ops, "norm_forward", lambda x, w, eps, save=True: saves.append(save) or forward(x, w, eps, save))
+    with torch.no_grad():
+        again = ckl.chunked_kl_loss(*leaves, idx, tl, mask, chunk=128, save_8bit=True, norm_weight=nw)
+    assert saves == [False] * norm and not again.requires_grad
+    assert same_bits(again, loss.detach())
 
 
 def dense_step(emb, nw, tok, teacher, K, scale, eps, mask):
