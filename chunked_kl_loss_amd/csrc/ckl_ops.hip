@@ -166,6 +166,12 @@ constexpr int kTopkStep = kTopkThreads * 8;                  // columns of one v
 constexpr int kTopkTile = kTopkVecs * kTopkStep;
 constexpr int kTopkList = 64 * kTopkVecs + 64;               // vectors on a wave's list: a tile's, and 64
 constexpr uint32_t kNanKey = 0xfffffffeu;                    // every key lies below 2^32 - 1
+// Exponentials are taken as 2^(x log2 e + neg) with neg = -m log2 e rounded, and
+// the rounding is divided out of their sum later.  Below this limit it is at
+// most half of neg's last place, 4, so both factors are ordinary numbers (past 2^31
+// they may overflow).  Larger references, which only masks have, take
+// 2^((x - m) log2 e).
+constexpr float kTopkNegLimit = 1e8f;
 
 __device__ __forceinline__ uint32_t order_key(float x) {
   if (x != x) return kNanKey;
@@ -713,14 +719,14 @@ __global__ __launch_bounds__(kTopkThreads, CAP <= 4096 ? 4 : 2) void topk_rows_k
         if (vm > m + 40.f) {
           const float to = -vm * kLog2e;
           s *= fast_exp2((m - vm) * kLog2e);
-          if (fabsf(neg) < 1e30f && m > -INFINITY) s *= fast_exp2(-fmaf(m, kLog2e, neg));  // the old neg's rounding
+          if (fabsf(neg) < kTopkNegLimit && m > -INFINITY) s *= fast_exp2(-fmaf(m, kLog2e, neg));  // the old neg's rounding
           m = vm;
           neg = to;
         }
-        if (fabsf(neg) < 1e30f) {
+        if (fabsf(neg) < kTopkNegLimit) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) sum += fast_exp2(fmaf(raw[u].get(i), kLog2e, neg));
-        } else {  // rows of a type's lowest value, infinities: the products above would overflow
+        } else {  // masks of a large or the lowest value, infinities
 #pragma unroll
           for (int i = 0; i < 8; ++i) sum += fast_exp2((raw[u].get(i) - m) * kLog2e);
         }
@@ -832,7 +838,7 @@ __global__ __launch_bounds__(kTopkThreads, CAP <= 4096 ? 4 : 2) void topk_rows_k
       __syncthreads();
     }
   }
-  if (fabsf(neg) < 1e30f && m > -INFINITY) s *= fast_exp2(-fmaf(m, kLog2e, neg));  // the rounding of neg
+  if (fabsf(neg) < kTopkNegLimit && m > -INFINITY) s *= fast_exp2(-fmaf(m, kLog2e, neg));  // the rounding of neg
   topk_reduce_state(m, s, sh);
   if (segments == 1) {
     topk_finish<CAP>(buf, n, K, m, s, logprob, idx + row * K, val + row * K, lse + row, sh);
