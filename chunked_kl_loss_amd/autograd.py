@@ -18,6 +18,7 @@ norm that saves its input in 8 bits."""
 from __future__ import annotations
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import _binding, ops
@@ -140,11 +141,17 @@ class RMSNorm8Bit(torch.autograd.Function):
         return dx, dweight, None
 
 
+def _needs_function(requires_grad: bool) -> bool:
+    """Whether a call whose inputs require a gradient or not has to go through its Function: where a gradient is
+    asked for, and in a forward-mode context, where the Function refuses tangents (the raw call would drop them)."""
+    return forward_ad._current_level >= 0 or (requires_grad and torch.is_grad_enabled())
+
+
 def embedding(W, tokens, scale: float = 1.0):
     """scale * W[tokens], differentiable with respect to the table W [V, d] (the output head's, when tied).
     tokens: int32 / int64 of any shape; a token outside [0, V) gives a zero row and no gradient."""
     W, tokens = W.contiguous(), tokens.contiguous()
-    if not (W.requires_grad and torch.is_grad_enabled()):
+    if not _needs_function(W.requires_grad):
         return ops.embedding_forward(W, tokens, scale)
     return Embedding.apply(W, tokens, scale)
 
@@ -154,7 +161,7 @@ def rms_norm_8bit(x, weight, eps: float = 1e-6):
     that of the exact x; the backward pass reads x from 8 bits (ops.act_encode), so that the norm keeps d bytes a
     row instead of x."""
     x, weight = x.contiguous(), weight.contiguous()
-    if not ((x.requires_grad or weight.requires_grad) and torch.is_grad_enabled()):
+    if not _needs_function(x.requires_grad or weight.requires_grad):
         return ops.norm_forward(x, weight, eps, save=False)[0]
     return RMSNorm8Bit.apply(x, weight, eps)
 
@@ -199,7 +206,7 @@ def chunked_kl_loss(H, W, idx, tlogit, mask=None, chunk: int = 2048, fused: bool
     if save_8bit and not fused:
         nw = None if norm_weight is None else norm_weight.contiguous()
         if not torch.is_grad_enabled():  # nothing is saved (a Function sees the leaves' requires_grad all the same)
-            H = H if nw is None else ops.norm_forward(H, nw, norm_eps, save=False)[0]
+            H = H if nw is None else rms_norm_8bit(H, nw, norm_eps)
             return ChunkedKLLoss.apply(H, W, idx, tlogit, mask, chunk, teacher_form)
         return ChunkedKLLoss8Bit.apply(H, W, idx, tlogit, mask, chunk, teacher_form, nw, norm_eps)
     if fused:

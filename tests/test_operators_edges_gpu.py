@@ -13,7 +13,7 @@ import torch
 
 import chunked_kl_loss_amd as ckl
 from chunked_kl_loss_amd import _binding as B
-from tests.test_operators_gpu import DT, EPS, check_topk, normal
+from tests.test_operators_gpu import DT, EPS, check_topk, normal, same_bits
 
 pytestmark = pytest.mark.gpu
 
@@ -33,3 +33,30 @@ def test_topk_of_logits_far_from_zero(T, form, dtype):
         z[2, :2048:3] = m                # some of the columns of every thread's first vector
         z[2, 8500:8700] = m              # and of a later segment
         check_topk(z.to(DT[dtype]), K, form)
+
+
+# ------------------------------------------------------ forward-mode tangents --
+def test_forward_mode_tangents_are_refused_not_lost():
+    fw = torch.autograd.forward_ad
+    W, tok = normal((50, 16), torch.float32, 1).cuda(), torch.tensor([1, -1, 49, 7], device="cuda")
+    x, w = normal((4, 16), torch.float32, 2).cuda(), normal((16,), torch.float32, 3).cuda()
+    idx, tl = torch.arange(2, device="cuda", dtype=torch.int32).repeat(4, 1), normal((4, 2), torch.float32, 4).cuda()
+    kl = ckl.chunked_kl_loss
+    calls = [lambda W, x, w: ckl.embedding(W, tok, 2.0), lambda W, x, w: ckl.rms_norm_8bit(x, w),
+             lambda W, x, w: kl(x, W, idx, tl), lambda W, x, w: kl(x, W, idx, tl, save_8bit=True),
+             lambda W, x, w: kl(x, W, idx, tl, save_8bit=True, norm_weight=w),
+             lambda W, x, w: kl(x, W, idx, tl, fused=True, save_8bit=True, norm_weight=w)]
+    uses = ["W", "xw", "Wx", "Wx", "Wxw", "Wxw"]
+    plain = [f(W, x, w) for f in calls]
+    with fw.dual_level():
+        dual = {n: fw.make_dual(t, torch.ones_like(t)) for n, t in (("W", W), ("x", x), ("w", w))}
+        for f, names, want in zip(calls, uses, plain):
+            for grad_mode in (True, False):
+                with torch.set_grad_enabled(grad_mode):
+                    for n in names:
+                        args = dict(W=W, x=x, w=w)
+                        args[n] = dual[n]
+                        with pytest.raises(NotImplementedError, match="jvp"):
+                            f(**args)
+                    got = f(W, x, w)  # without a tangent as ever
+                    assert not got.requires_grad and same_bits(got, want)
