@@ -352,7 +352,10 @@ ckl_status ckl_act_encode(const void* x, int32_t dtype, int64_t T, int64_t d, in
 
 /* The values the codes stand for, in out_dtype; or, with rstd [T] float32 and
  * weight [d] weight_dtype (both or neither), value * rstd[t] * weight[i]
- * rounded once: the output of ckl_norm_forward rebuilt from its codes. */
+ * rounded once: the output of ckl_norm_forward rebuilt from its codes.  Where
+ * ckl_backward is given rebuilt states, its lse has to be theirs too (from
+ * ckl_forward on them): that of the exact states leaves a row's probabilities
+ * off from one by more than the gradient where the student is sure. */
 ckl_status ckl_act_decode(const int8_t* codes, const uint8_t* exps, int64_t T, int64_t d, const float* rstd,
                           const void* weight, int32_t weight_dtype, void* out, int32_t out_dtype, void* stream);
 

@@ -13,7 +13,7 @@ import torch
 
 import chunked_kl_loss_amd as ckl
 from chunked_kl_loss_amd import _binding as B
-from tests.test_operators_gpu import DT, EPS, check_topk, normal, same_bits
+from tests.test_operators_gpu import DT, EPS, HALF, check_topk, loss_inputs, normal, same_bits
 
 pytestmark = pytest.mark.gpu
 
@@ -60,3 +60,118 @@ def test_forward_mode_tangents_are_refused_not_lost():
                             f(**args)
                     got = f(W, x, w)  # without a tangent as ever
                     assert not got.requires_grad and same_bits(got, want)
+
+
+# ------------------------------------- the loss's gradient from 8-bit states --
+def sure_student(dtype, lean, big, d=256, T=200, V=4000, K=50, noise=0.1):
+    """States that lean on one word a row, a teacher that is the student's logits and a little noise, a mask."""
+    W = normal((V, d), torch.float32, 1, d ** -0.5)
+    word = torch.randint(0, V, (T,), generator=torch.Generator().manual_seed(2))
+    H = lean * W[word] + normal((T, d), torch.float32, 3)
+    if big > 1:  # a few large columns, as residual streams have them
+        H[:, [5, 100]] *= big
+        W[:, [5, 100]] /= big
+    H, W = H.to(dtype), W.to(dtype)
+    teacher = H.double() @ W.double().t() + noise * normal((T, V), torch.float64, 4)
+    vals, idx = torch.topk(teacher, K, 1)
+    mask = torch.rand(T, generator=torch.Generator().manual_seed(5)) < 0.8
+    return H, W, idx.int(), vals.float(), mask
+
+
+def loss_gradient(h, W, idx, vals, mask, half):
+    """Of the mean KL at states h, in 64 bits: (dH, dW) with a bound on each element's error.  half: one rounding of
+    G and of the results."""
+    T, d = h.shape
+    V = W.shape[0]
+    z = h @ W.t()
+    lse = torch.logsumexp(z, 1, keepdim=True)
+    q = torch.zeros_like(z).scatter_(1, idx.long(), torch.softmax(vals.double(), 1))
+    p = torch.exp(z - lse)
+    s = mask.double()[:, None] / mask.sum()
+    G = s * (p - q)
+    # a logit is a sum of d products; the log-sum-exp adds V exponentials and rounds with its size, and carries its
+    # largest logit's error; an exponential is good to 2^-22 and to the rounding of its argument; q likewise
+    e_z = 2 * d * EPS * (h.abs() @ W.abs().t())
+    e_lse = (p * e_z).sum(1, keepdim=True) + (V + 8) * EPS + 4 * EPS * lse.abs()
+    e_p = p * (e_z + e_lse + 4 * EPS * (z - lse).abs() + 2.0 ** -22)
+    e_q = q * (64 * EPS + 4 * EPS * vals.abs().max())
+    e_G = s * (e_p + e_q) + G.abs() * half + 4 * EPS * s * (p + q)
+    dH, dW = G @ W, G.t() @ h
+    e_H = e_G @ W.abs() + (V + 8) * EPS * (G.abs() @ W.abs())
+    e_W = e_G.t() @ h.abs() + (T + 8) * EPS * (G.abs().t() @ h.abs())
+    return dH, e_H + dH.abs() * half, dW, e_W + dW.abs() * half
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lean,big", [(0, 1), (9, 1), (12, 1), (15, 1), (15, 30), (40, 1)])
+def test_gradient_from_saved_states_of_a_sure_student(lean, big, dtype):
+    t = DT[dtype]
+    H, W, idx, vals, mask = sure_student(t, lean, big)
+    Hp, Wp = H.cuda().requires_grad_(True), W.cuda().requires_grad_(True)
+    args = idx.cuda(), vals.cuda(), mask.cuda()
+    ckl.chunked_kl_loss(Hp, Wp, *args, chunk=128, save_8bit=True).backward()
+    held = ckl.act_decode(*ckl.act_encode(H.cuda()), dtype=t).double().cpu()
+    dH, e_H, dW, e_W = loss_gradient(held, W.double(), idx, vals, mask, HALF[t] * (1 + 2.0 ** -6))
+    assert ((Hp.grad.double().cpu() - dH).abs() <= e_H).all()
+    assert ((Wp.grad.double().cpu() - dW).abs() <= e_W).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lean,big", [(0, 1), (12, 1), (15, 1), (15, 30)])
+def test_gradient_through_the_norm_of_a_sure_student(lean, big, dtype):
+    t = DT[dtype]
+    X, W, idx, vals, mask = sure_student(t, lean, big)
+    W = (W.float() * (X.double() ** 2).mean().sqrt()).to(t)  # logits of the same size behind the norm
+    nw = (1 + normal((X.shape[1],), torch.float32, 9, 0.1)).to(t)
+    leaves = [v.cuda().requires_grad_(True) for v in (X, W, nw)]
+    ckl.chunked_kl_loss(leaves[0], leaves[1], idx.cuda(), vals.cuda(), mask.cuda(), chunk=128, save_8bit=True,
+                        norm_weight=leaves[2]).backward()
+    _, codes, exps, rstd = ckl.norm_forward(X.cuda(), nw.cuda())
+    h = ckl.act_decode(codes, exps, rstd, nw.cuda(), dtype=t).double().cpu()
+    half = HALF[t] * (1 + 2.0 ** -6)
+    dH, e_H, dW, e_W = loss_gradient(h, W.double(), idx, vals, mask, half)
+    assert ((leaves[1].grad.double().cpu() - dW).abs() <= e_W).all()
+    # the norm's own gradient, linear in dH: its error passes through, and the norm's sums add theirs
+    r, w = rstd.double().cpu()[:, None], nw.double()
+    n = ckl.act_decode(codes, exps, dtype=torch.float32).double().cpu() * r
+    dX = r * (dH * w - n * (dH * w * n).mean(1, keepdim=True))
+    e_X = r * (e_H * w.abs() + n.abs() * (e_H * w.abs() * n.abs()).mean(1, keepdim=True))
+    mag = r * ((dH * w).abs() + n.abs() * (dH * w * n).abs().mean(1, keepdim=True))
+    assert ((leaves[0].grad.double().cpu() - dX).abs() <= e_X + mag * 240 * EPS + dX.abs() * half).all()
+    dn = (dH * n).sum(0)
+    e_n = (e_H * n.abs()).sum(0) + (len(X) + 56) * EPS * (dH * n).abs().sum(0) + dn.abs() * half
+    assert ((leaves[2].grad.double().cpu() - dn).abs() <= e_n).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("norm", [False, True])
+def test_saved_states_are_the_direct_calls_with_their_own_lse(norm, masked, dtype):
+    X, W, idx, tl, mask = loss_inputs(dtype=DT[dtype], seed=20)
+    mask = mask if masked else None
+    nw = (1 + normal((72,), torch.float32, 9, 0.2)).to(DT[dtype]).cuda() if norm else None
+    leaves = [t.clone().requires_grad_(True) for t in (X, W)] + ([nw.clone().requires_grad_(True)] if norm else [])
+    kw = dict(chunk=128, save_8bit=True, norm_weight=leaves[2] if norm else None)
+    loss = ckl.chunked_kl_loss(leaves[0], leaves[1], idx, tl, mask, **kw)
+    (3.0 * loss).backward()
+    g = torch.tensor([3.0], device="cuda")
+    if norm:
+        y, codes, exps, rstd = ckl.norm_forward(X, nw)
+        held = ckl.act_decode(codes, exps, rstd, nw, dtype=X.dtype)
+    else:
+        y, (codes, exps) = X, ckl.act_encode(X)
+        held = ckl.act_decode(codes, exps, dtype=X.dtype)
+    plain, _, _ = ckl.forward(y, W, idx, tl, mask, chunk=128)
+    assert same_bits(loss.detach().reshape(1), plain)  # the loss is that of the exact states
+    with torch.no_grad():
+        assert same_bits(ckl.chunked_kl_loss(leaves[0], leaves[1], idx, tl, mask, **kw).reshape(1), plain)
+    _, lse, _ = ckl.forward(held, W, idx, tl, mask, chunk=128)
+    dH, dW = ckl.backward(held, W, idx, tl, mask, lse, g, chunk=128, dh_dtype=X.dtype, dw_dtype=W.dtype)
+    want = [*ckl.norm_backward(dH, codes, exps, rstd, nw)] if norm else [dH]
+    want.insert(1, dW)
+    for leaf, ref in zip(leaves, want):
+        assert same_bits(leaf.grad, ref)
+    if norm:  # only the norm's weight asked for
+        only = nw.clone().requires_grad_(True)
+        (3.0 * ckl.chunked_kl_loss(X, W, idx, tl, mask, chunk=128, save_8bit=True, norm_weight=only)).backward()
+        assert same_bits(only.grad, want[2])
