@@ -92,6 +92,8 @@ class ChunkedKLLoss8Bit(torch.autograd.Function):
             codes, exps = ops.act_encode(H)
         loss, _, _ = _binding.forward(H, W, idx, tlogit, mask, chunk=chunk, teacher_form=teacher_form)
         if need:
+            if norm_weight is not None and mask is not None:
+                ops.norm_drop_rows(exps, rstd, mask)
             ctx.save_for_backward(codes, exps, rstd, norm_weight, W, idx, tlogit, mask)
         ctx.chunk, ctx.teacher_form, ctx.dtype = chunk, teacher_form, dtype
         return loss[0]
@@ -133,8 +135,8 @@ class Embedding(torch.autograd.Function):
 
 class RMSNorm8Bit(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, weight, eps: float = 1e-6):
-        y, saved = ops.norm_forward_saving(x, weight, eps)
+    def forward(ctx, x, weight, eps: float = 1e-6, mask=None):
+        y, saved = ops.norm_forward_saving(x, weight, eps, mask)
         ctx.save_for_backward(saved, weight)
         return y
 
@@ -143,7 +145,7 @@ class RMSNorm8Bit(torch.autograd.Function):
     def backward(ctx, grad):
         saved, weight = ctx.saved_tensors
         dx, dweight = ops.norm_backward_saved(grad.contiguous(), saved, weight)
-        return dx, dweight, None
+        return dx, dweight, None, None
 
 
 def _needs_function(requires_grad: bool) -> bool:
@@ -161,14 +163,20 @@ def embedding(W, tokens, scale: float = 1.0):
     return Embedding.apply(W, tokens, scale)
 
 
+def _norm(x, weight, eps, mask=None):
+    """rms_norm_8bit; with a mask [T], rows of x [T, d] that are masked out add nothing to the weight's gradient
+    whatever they hold (their gradients have to be zero)."""
+    x, weight = x.contiguous(), weight.contiguous()
+    if not _needs_function(x.requires_grad or weight.requires_grad):
+        return ops.norm_forward(x, weight, eps, save=False)[0]
+    return RMSNorm8Bit.apply(x, weight, eps, mask)
+
+
 def rms_norm_8bit(x, weight, eps: float = 1e-6):
     """RMS norm of the last dimension, differentiable with respect to x [..., d] and weight [d].  The output is
     that of the exact x; the backward pass reads x from 8 bits (ops.act_encode), so that the norm keeps d bytes a
     row instead of x."""
-    x, weight = x.contiguous(), weight.contiguous()
-    if not _needs_function(x.requires_grad or weight.requires_grad):
-        return ops.norm_forward(x, weight, eps, save=False)[0]
-    return RMSNorm8Bit.apply(x, weight, eps)
+    return _norm(x, weight, eps)
 
 
 def chunked_kl_loss(H, W, idx, tlogit, mask=None, chunk: int = 2048, fused: bool = False, teacher_form: int = 0,
@@ -189,7 +197,7 @@ def chunked_kl_loss(H, W, idx, tlogit, mask=None, chunk: int = 2048, fused: bool
     save_8bit): H is the input of an RMS norm before the head, whose input is
     saved instead, once for both; differentiable with respect to norm_weight
     too.  fused=True keeps gradients instead of H, so there save_8bit goes with
-    norm_weight only.
+    norm_weight only.  Masked rows of H may hold anything.
 
     Leading batch dimensions are flattened into rows: H [..., d], idx and
     tlogit [..., K], mask [...].  The library takes contiguous tensors, int32
@@ -209,11 +217,11 @@ def chunked_kl_loss(H, W, idx, tlogit, mask=None, chunk: int = 2048, fused: bool
     if fused and save_8bit:
         if norm_weight is None:
             raise ValueError("fused=True keeps no hidden states: save_8bit there needs norm_weight")
-        H = rms_norm_8bit(H, norm_weight, norm_eps)
+        H = _norm(H, norm_weight, norm_eps, mask)
     if save_8bit and not fused:
         nw = None if norm_weight is None else norm_weight.contiguous()
         if not torch.is_grad_enabled():  # nothing is saved (a Function sees the leaves' requires_grad all the same)
-            H = H if nw is None else rms_norm_8bit(H, nw, norm_eps)
+            H = H if nw is None else _norm(H, nw, norm_eps)
             return ChunkedKLLoss.apply(H, W, idx, tlogit, mask, chunk, teacher_form)
         return ChunkedKLLoss8Bit.apply(H, W, idx, tlogit, mask, chunk, teacher_form, nw, norm_eps)
     if fused:

@@ -258,11 +258,13 @@ def _norm_saved(T, d):
     return codes, codes + T * d, codes + T * (d + -(-d // ACT_BLOCK))
 
 
-def norm_forward_saving(x, weight, eps: float):
-    """norm_forward as (y, saved)."""
+def norm_forward_saving(x, weight, eps: float, mask=None):
+    """norm_forward as (y, saved); rows whose mask is 0 are saved as rows of zeros (norm_drop_rows)."""
     if x.dim() < 1:
         raise ValueError("x must be [..., d]")
     dev, d, code = _check(("x", "weight"), x, weight), x.shape[-1], _code(x.dtype)
+    if mask is not None:
+        _check(("x", "mask"), x, mask)
     w_code, T = _weight_code(weight, d), _rows(x)
     codes, exps, size = _norm_saved(T, d)
     y = _new(x.shape, x.dtype, dev)
@@ -270,7 +272,17 @@ def norm_forward_saving(x, weight, eps: float):
     at = saved.data_ptr()
     _call(dev, load_library().ckl_norm_forward, x.data_ptr(), code, T, d, weight.data_ptr(), w_code, eps, y.data_ptr(),
           at + codes, at + exps, at)
+    if mask is not None:
+        norm_drop_rows(saved[exps:].view(T, -(-d // ACT_BLOCK)), saved[:4 * T].view(torch.float32), mask)
     return y, saved
+
+
+def norm_drop_rows(exps, rstd, mask) -> None:
+    """Rows of exps [T, ...] and rstd [T] whose mask [T] is 0 become those of zeros: a row that nothing reads may
+    hold infinities or NaN, which a gradient of zero would not keep out of the weight's gradient."""
+    drop = mask == 0
+    exps.masked_fill_(drop[:, None], 1)
+    rstd.masked_fill_(drop, 0.0)
 
 
 def norm_backward_saved(dy, saved, weight):

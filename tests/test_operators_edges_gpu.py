@@ -175,3 +175,34 @@ def test_saved_states_are_the_direct_calls_with_their_own_lse(norm, masked, dtyp
         only = nw.clone().requires_grad_(True)
         (3.0 * ckl.chunked_kl_loss(X, W, idx, tl, mask, chunk=128, save_8bit=True, norm_weight=only)).backward()
         assert same_bits(only.grad, want[2])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("fused", [False, True])
+@pytest.mark.parametrize("norm", [False, True])
+def test_masked_rows_may_hold_anything(norm, fused, dtype):
+    # a masked row contributes nothing, whatever the padding of a batch left in it
+    if fused and not norm:
+        pytest.skip("the one-call loss keeps no hidden states")
+    X, W, idx, tl, mask = loss_inputs(dtype=DT[dtype], seed=30)
+    nw = (1 + normal((72,), torch.float32, 9, 0.2)).to(DT[dtype]).cuda()
+
+    def grads(x, m):
+        leaves = [x.clone().requires_grad_(True), W.clone().requires_grad_(True), nw.clone().requires_grad_(True)]
+        loss = ckl.chunked_kl_loss(leaves[0], leaves[1], idx, tl, m, chunk=128, fused=fused, save_8bit=True,
+                                   norm_weight=leaves[2] if norm else None)
+        loss.backward()
+        return [loss.detach(), *(v.grad for v in leaves[:3 if norm else 2])]
+    for m in (mask, mask.to(torch.uint8), torch.zeros_like(mask)):
+        want = grads(X, m)
+        for bad in (math.nan, math.inf, -math.inf, torch.finfo(X.dtype).max, 0.0):
+            x = X.clone()
+            x[m == 0, ::2] = bad
+            got = grads(x, m)
+            assert not got[1][m == 0].any()
+            for a, b in zip(got, want):
+                assert same_bits(a, b)
+    for off in (mask.cpu(), mask.float()):
+        with pytest.raises(ValueError):
+            ckl.chunked_kl_loss(X.clone().requires_grad_(True), W, idx, tl, off, chunk=128, fused=fused,
+                                save_8bit=True, norm_weight=nw if norm else None)
