@@ -2,8 +2,9 @@
 its gradient, activations in 8 bits and the RMS norm that saves its input so.
 
 Argument marshalling over include/ckl.h, as in _binding.  Leading dimensions
-are rows; tensors are contiguous and on one GPU.  Calls run on that GPU's
-current stream.  Small calls are bound by this layer, so it does little: one
+are rows; tensors are contiguous and on one GPU.  The library takes arrays from
+a 16-byte boundary: an input that begins off one (a slice of rows of an odd
+width) is copied first.  Calls run on that GPU's current stream.  Small calls are bound by this layer, so it does little: one
 pass over the arguments, the outputs, the call."""
 from __future__ import annotations
 
@@ -45,6 +46,10 @@ def _check(names, *tensors):
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
     return device
+
+
+def _aligned(t):
+    return t.clone() if t.data_ptr() & 15 else t
 
 
 def _new(shape, dtype, device):
@@ -108,6 +113,7 @@ def teacher_topk(logits, K: int, mask=None, teacher_form: int = CKL_TEACHER_LOGI
         if mask.shape != lead or mask.dtype not in (torch.uint8, torch.bool):
             raise ValueError("mask must be a uint8/bool tensor of the logits' leading shape")
     T, code = _rows(logits), _code(logits.dtype)
+    logits = _aligned(logits)
     ws, ws_ptr, ws_bytes = _workspace(dev, "ckl_topk_workspace_size", T, V, K)
     idx = _new((*lead, K), torch.int32, dev)
     values = _new((*lead, K), torch.float32, dev)
@@ -126,6 +132,7 @@ def embedding_forward(W, tokens, scale: float = 1.0, v_offset: int = 0):
     dev = _check(("W", "tokens"), W, tokens)
     nb, code = _token_bytes(tokens), _code(W.dtype)
     V, d = W.shape
+    W = _aligned(W)
     out = _new((*tokens.shape, d), W.dtype, dev)
     _call(dev, load_library().ckl_embedding_forward, W.data_ptr(), code, V, d, v_offset, tokens.data_ptr(), nb,
           tokens.numel(), scale, out.data_ptr())
@@ -134,8 +141,8 @@ def embedding_forward(W, tokens, scale: float = 1.0, v_offset: int = 0):
 
 def embedding_backward(dY, tokens, V: int, scale: float = 1.0, v_offset: int = 0, dw_dtype=None, add_to=None):
     """dW[v] = scale * the sum of dY [..., d] over the positions of token v + v_offset, as [V, d] in dw_dtype
-    (default float32).  add_to: a [V, d] gradient (the tied head's) the sums are added to in place; it is
-    returned, and rows without a token are not touched."""
+    (default float32).  add_to: a [V, d] gradient (the tied head's, from a 16-byte boundary) the sums are added to
+    in place; it is returned, and rows without a token are not touched."""
     if dY.dim() < 1 or dY.shape[:-1] != tokens.shape:
         raise ValueError("dY must be [*tokens.shape, d]")
     d = dY.shape[-1]
@@ -151,6 +158,7 @@ def embedding_backward(dY, tokens, V: int, scale: float = 1.0, v_offset: int = 0
         dw_dtype = add_to.dtype
     nb, code, dw_code = _token_bytes(tokens), _code(dY.dtype), _code(dw_dtype)
     T = tokens.numel()
+    dY = _aligned(dY)
     ws, ws_ptr, ws_bytes = _workspace(dev, "ckl_embedding_workspace_size", T, d, V)
     dW = _new((V, d), dw_dtype, dev) if add_to is None else add_to
     _call(dev, load_library().ckl_embedding_backward, dY.data_ptr(), code, T, d, tokens.data_ptr(), nb, V, v_offset,
@@ -183,7 +191,7 @@ def act_encode(x):
     if x.dim() < 1:
         raise ValueError("x must be [..., d]")
     dev, shape, code = _check(("x",), x), x.shape, _code(x.dtype)
-    d = shape[-1]
+    d, x = shape[-1], _aligned(x)
     codes = _new(shape, torch.int8, dev)
     exps = _new((*shape[:-1], -(-d // ACT_BLOCK)), torch.uint8, dev)
     _call(dev, load_library().ckl_act_encode, x.data_ptr(), code, _rows(x), d, codes.data_ptr(), exps.data_ptr())
@@ -203,7 +211,9 @@ def act_decode(codes, exps, rstd=None, weight=None, dtype=torch.bfloat16):
         dev = _check(("codes", "exps", "rstd", "weight"), codes, exps, rstd, weight)
         _check_codes(codes, exps)
         _check_rstd(rstd, codes.shape[:-1])
+        weight = _aligned(weight)
         rstd_ptr, weight_ptr, w_code = rstd.data_ptr(), weight.data_ptr(), _weight_code(weight, codes.shape[-1])
+    codes = _aligned(codes)
     out = _new(codes.shape, dtype, dev)
     _call(dev, load_library().ckl_act_decode, codes.data_ptr(), exps.data_ptr(), _rows(codes), codes.shape[-1],
           rstd_ptr, weight_ptr, w_code, out.data_ptr(), code)
@@ -218,6 +228,7 @@ def norm_forward(x, weight, eps: float = 1e-6, save: bool = True):
     dev, shape, code = _check(("x", "weight"), x, weight), x.shape, _code(x.dtype)
     d = shape[-1]
     w_code = _weight_code(weight, d)
+    x, weight = _aligned(x), _aligned(weight)
     y = _new(shape, x.dtype, dev)
     if save:
         codes = _new(shape, torch.int8, dev)
@@ -242,6 +253,7 @@ def norm_backward(dy, codes, exps, rstd, weight):
     _check_rstd(rstd, shape[:-1])
     d, T, code = shape[-1], _rows(codes), _code(dy.dtype)
     w_code = _weight_code(weight, d)
+    dy, codes, weight = _aligned(dy), _aligned(codes), _aligned(weight)
     ws, ws_ptr, ws_bytes = _workspace(dev, "ckl_norm_workspace_size", T, d)
     dx = _new(shape, dy.dtype, dev)
     dweight = _new(weight.shape, weight.dtype, dev)
@@ -266,6 +278,7 @@ def norm_forward_saving(x, weight, eps: float, mask=None):
     if mask is not None:
         _check(("x", "mask"), x, mask)
     w_code, T = _weight_code(weight, d), _rows(x)
+    x, weight = _aligned(x), _aligned(weight)
     codes, exps, size = _norm_saved(T, d)
     y = _new(x.shape, x.dtype, dev)
     saved = _new(size, torch.uint8, dev)
@@ -288,6 +301,7 @@ def norm_drop_rows(exps, rstd, mask) -> None:
 def norm_backward_saved(dy, saved, weight):
     """norm_backward from what norm_forward_saving saved for rows of dy's shape and type."""
     dev, d, T = dy.device, dy.shape[-1], _rows(dy)
+    dy, weight = _aligned(dy), _aligned(weight)
     codes, exps, _ = _norm_saved(T, d)
     ws, ws_ptr, ws_bytes = _workspace(dev, "ckl_norm_workspace_size", T, d)
     dx = _new(dy.shape, dy.dtype, dev)

@@ -206,3 +206,68 @@ def test_masked_rows_may_hold_anything(norm, fused, dtype):
         with pytest.raises(ValueError):
             ckl.chunked_kl_loss(X.clone().requires_grad_(True), W, idx, tl, off, chunk=128, fused=fused,
                                 save_8bit=True, norm_weight=nw if norm else None)
+
+
+# ------------------------------------------------------ off a 16-byte boundary --
+def off_by(t, n):
+    """t's values in a contiguous tensor that begins n elements behind a 16-byte boundary."""
+    flat = torch.full((t.numel() + n,), math.nan if t.is_floating_point() else 1, dtype=t.dtype, device="cuda")
+    flat[n:] = t.reshape(-1)
+    out = flat[n:].view(t.shape)
+    assert out.is_contiguous() and out.data_ptr() % 16 == n * t.element_size() % 16
+    return out
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_topk_of_row_slices(dtype):
+    # rows of an odd vocabulary begin anywhere: a slice of them is contiguous all the same
+    for T, V, K in ((5, 333, 7), (9, 50021, 40)):
+        z = normal((T, V), DT[dtype], V, 2.0).cuda()
+        mask = torch.tensor([True, False, True] * 3, device="cuda")[:T]
+        whole = ckl.teacher_topk(z, K, mask, 1)
+        for i in range(T):
+            for part in (slice(i, i + 1), slice(i, T)):
+                for a, b in zip(ckl.teacher_topk(z[part], K, mask[part], 1), whole):
+                    # a log-sum-exp (here below 13) may move by its roundings where the split is another one, and
+                    # the values (below 25) with it: twice check_topk's bound
+                    if a.dtype == torch.int32:
+                        assert torch.equal(a, b[part])
+                    else:
+                        torch.testing.assert_close(a, b[part], rtol=0, atol=2 * (V / 256 + 40 + 4 + 26 + 50) * EPS)
+        one = ckl.teacher_topk(z.view(1, T, V)[:, -1], K)
+        assert torch.equal(one[0][0], ckl.teacher_topk(z, K)[0][-1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [1, 2, 3])
+def test_inputs_off_a_boundary(n, dtype):
+    t, T, V, d = DT[dtype], 300, 77, 40
+    W, x, dy = (normal(s, t, i).cuda() for i, s in enumerate(((V, d), (T, d), (T, d))))
+    w = (1 + normal((d,), torch.float32, 4, 0.1)).to(t).cuda()
+    tok = torch.randint(-1, V + 1, (T,), generator=torch.Generator().manual_seed(1)).cuda()
+    o = lambda v: off_by(v, n)  # noqa: E731
+    assert same_bits(ckl.embedding_forward(o(W), o(tok), 2.0), ckl.embedding_forward(W, tok, 2.0))
+    assert same_bits(ckl.embedding_backward(o(dy), o(tok), V), ckl.embedding_backward(dy, tok, V))
+    codes, exps = ckl.act_encode(x)
+    for a, b in zip(ckl.act_encode(o(x)), (codes, exps)):
+        assert same_bits(a, b)
+    y, _, _, rstd = want = ckl.norm_forward(x, w)
+    for a, b in zip(ckl.norm_forward(o(x), o(w)), want):
+        assert same_bits(a, b)
+    assert same_bits(ckl.act_decode(o(codes), o(exps), o(rstd), o(w), dtype=t),
+                     ckl.act_decode(codes, exps, rstd, w, dtype=t))
+    dx, dw = ckl.norm_backward(dy, codes, exps, rstd, w)
+    for a, b in zip(ckl.norm_backward(o(dy), o(codes), o(exps), o(rstd), o(w)), (dx, dw)):
+        assert same_bits(a, b)
+    # through autograd, with a gradient that begins off a boundary (a slice of a larger one)
+    X, Wt = o(x).requires_grad_(True), o(w).requires_grad_(True)
+    out = ckl.rms_norm_8bit(X, Wt)
+    assert same_bits(out.detach(), y)
+    for a, b in zip(torch.autograd.grad(out, (X, Wt), o(dy)), (dx, dw)):
+        assert same_bits(a, b)
+    E = o(W).requires_grad_(True)
+    got, = torch.autograd.grad(ckl.embedding(E, o(tok), 2.0), E, o(dy))
+    assert same_bits(got, ckl.embedding_backward(dy, tok, V, 2.0, dw_dtype=t))
+    # what is written in place cannot be a copy
+    with pytest.raises(B.CklError, match="aligned"):
+        ckl.embedding_backward(dy, tok, V, add_to=o(torch.zeros(V, d, device="cuda")))
