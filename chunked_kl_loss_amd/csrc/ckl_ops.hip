@@ -906,6 +906,14 @@ __global__ __launch_bounds__(kTopkThreads, CAP <= 4096 ? 4 : 2) void topk_merge_
 }
 
 // ---------------------------------------------------------------- embedding --
+// The table's row of a token, V where it is outside [v_offset, v_offset + V).  The
+// difference is taken modulo 2^64: v_offset + V fits 63 bits, so no token at
+// either end of its type comes out below V.
+__device__ __forceinline__ int64_t token_row(int64_t token, int64_t V, int64_t v_offset) {
+  const uint64_t v = (uint64_t)token - (uint64_t)v_offset;
+  return v < (uint64_t)V ? (int64_t)v : V;
+}
+
 // out[t] = scale W[token_t - v_offset]; a zero row for a token outside the table.
 // A thread takes four vectors, their tokens and then their rows loaded together.
 // Bound by memory: 32768 x 2880 bf16 55 us, 4.7 TB/s.
@@ -920,18 +928,18 @@ __global__ __launch_bounds__(256) void embedding_forward_kernel(const T* __restr
 #pragma unroll
   for (int k = 0; k < kEmbedUnits; ++k) {
     unit_at(q, base, k * 256 + threadIdx.x, &row[k], &col[k]);
-    v[k] = row[k] < rows ? (int64_t)tokens[row[k]] - v_offset : -1;
+    v[k] = row[k] < rows ? token_row(tokens[row[k]], V, v_offset) : V;
   }
   float f[kEmbedUnits][8];
 #pragma unroll
   for (int k = 0; k < kEmbedUnits; ++k) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[k][i] = 0.f;
-    if (v[k] >= 0 && v[k] < V) load8(W + (v[k] * q.n + col[k]) * 8, f[k]);
+    if (v[k] < V) load8(W + (v[k] * q.n + col[k]) * 8, f[k]);
   }
 #pragma unroll
   for (int k = 0; k < kEmbedUnits; ++k) {
-    const bool in = v[k] >= 0 && v[k] < V;  // (a zero row whatever the scale)
+    const bool in = v[k] < V;  // (a zero row whatever the scale)
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[k][i] = in ? f[k][i] * scale : 0.f;
     if (row[k] < rows) stream8(out + (row[k] * q.n + col[k]) * 8, f[k]);
@@ -944,8 +952,7 @@ __global__ __launch_bounds__(256) void embedding_forward_kernel(const T* __restr
 // V, which sorts last and is never summed.
 template <typename I>
 __device__ __forceinline__ uint32_t token_key(const I* tokens, int64_t t, int64_t V, int64_t v_offset) {
-  const int64_t v = (int64_t)tokens[t] - v_offset;
-  return (v >= 0 && v < V) ? (uint32_t)v : (uint32_t)V;
+  return (uint32_t)token_row(tokens[t], V, v_offset);
 }
 
 // Zeros, by the workgroups of a launch past its own `first`: the rows of dW that

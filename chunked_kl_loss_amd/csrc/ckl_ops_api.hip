@@ -67,7 +67,8 @@ ckl_status check_embedding(int64_t T, int64_t d, int64_t V, int64_t v_offset) {
   if (s == CKL_OK) s = check_hidden(d);
   if (s == CKL_OK) s = check_vocab(V);
   if (s != CKL_OK) return s;
-  if (v_offset < 0) return fail(CKL_ERR_INVALID_ARG, "v_offset must be >= 0");
+  if (v_offset < 0 || v_offset > INT64_MAX - V)
+    return fail(CKL_ERR_INVALID_ARG, "v_offset must be >= 0 and v_offset + V at most 2^63 - 1");
   return CKL_OK;
 }
 

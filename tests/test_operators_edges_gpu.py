@@ -271,3 +271,22 @@ def test_inputs_off_a_boundary(n, dtype):
     # what is written in place cannot be a copy
     with pytest.raises(B.CklError, match="aligned"):
         ckl.embedding_backward(dy, tok, V, add_to=o(torch.zeros(V, d, device="cuda")))
+
+
+# ------------------------------------------------------ ids at their type's ends --
+@pytest.mark.parametrize("T", [9, 300, 9000])
+def test_ids_and_offsets_at_the_ends_of_their_type(T):
+    V, d, big = 100, 16, 2 ** 63 - 1
+    W, dY = normal((V, d), torch.float32, 1).cuda(), normal((T, d), torch.float32, 2).cuda()
+    for off, inside in ((big - V, [0, V - 1]), (2 ** 62, [5]), (0, [0, V - 1])):
+        tok = [-2 ** 63, -2 ** 63 + 1, -1, big, -2 ** 63 + off % 2, big - 1]
+        tok = [t for t in tok if not off <= t < off + V] + [off + i for i in inside]
+        tok = torch.tensor((tok * T)[:T], device="cuda")
+        at = torch.tensor([t - off if off <= t < off + V else -1 for t in tok.tolist()], device="cuda")
+        assert same_bits(ckl.embedding_forward(W, tok, 2.0, v_offset=off), ckl.embedding_forward(W, at, 2.0))
+        assert same_bits(ckl.embedding_backward(dY, tok, V, 2.0, v_offset=off), ckl.embedding_backward(dY, at, V, 2.0))
+    for off in (big, big - V + 1):
+        with pytest.raises(B.CklError, match="v_offset"):
+            ckl.embedding_forward(W, tok, v_offset=off)
+        with pytest.raises(B.CklError, match="v_offset"):
+            ckl.embedding_backward(dY, tok, V, v_offset=off)
