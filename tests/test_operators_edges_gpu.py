@@ -290,3 +290,88 @@ def test_ids_and_offsets_at_the_ends_of_their_type(T):
             ckl.embedding_forward(W, tok, v_offset=off)
         with pytest.raises(B.CklError, match="v_offset"):
             ckl.embedding_backward(dY, tok, V, v_offset=off)
+
+
+# ------------------------------------------- around workspaces and outputs --
+class Guarded:
+    """Arrays between guard bytes, from a 16-byte boundary that is not a page's."""
+
+    def __init__(self):
+        self.buffers = []
+
+    def __call__(self, shape, dtype, fill=0xAB):
+        n = math.prod(shape) * torch.empty((), dtype=dtype).element_size()
+        buf = torch.full((n + 2 * 4096,), 0xAB, dtype=torch.uint8, device="cuda")
+        body = buf[4112:4112 + n]
+        body.fill_(fill)
+        self.buffers.append((buf, n))
+        return body.view(dtype).view(shape)
+
+    def check(self):
+        torch.cuda.synchronize()
+        for buf, n in self.buffers:
+            assert (buf[:4112] == 0xAB).all() and (buf[4112 + n:] == 0xAB).all()
+
+
+def workspace(guarded, fn, *sizes):
+    need = ctypes.c_size_t(0)
+    B.check(fn(*sizes, ctypes.byref(need)))
+    return guarded((need.value,), torch.uint8, 0xFF), need.value
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,V,K", [(1, 201088, 4096), (3, 8200, 100), (7, 50021, 1000), (1030, 301, 17)])
+def test_topk_writes_its_own_arrays_only(T, V, K, dtype):
+    lib, g = B.load_library(), Guarded()
+    z = g((T, V), DT[dtype])
+    z.copy_(normal((T, V), DT[dtype], T + V, 2.0))
+    idx, val, lse = g((T, K), torch.int32), g((T, K), torch.float32), g((T,), torch.float32)
+    ws, n = workspace(g, lib.ckl_topk_workspace_size, T, V, K)
+    assert (n > 0) == (V > 50000)  # several segments to a row
+    B.check(lib.ckl_teacher_topk(z.data_ptr(), int(dtype == "bf16"), T, V, K, 0, None, idx.data_ptr(), val.data_ptr(),
+                                 lse.data_ptr(), ws.data_ptr(), n, None))
+    g.check()
+    for a, b in zip((idx, val, lse), ckl.teacher_topk(z.clone(), K)):
+        assert same_bits(a, b)
+
+
+@pytest.mark.parametrize("add", [0, 1])
+@pytest.mark.parametrize("dtype,grad", [("bf16", "f32"), ("f32", "bf16")])
+@pytest.mark.parametrize("T,V,d", [(200, 333, 40), (257, 333, 40), (8193, 333, 8), (70001, 50, 2056), (300, 1, 16)])
+def test_embedding_grad_writes_its_own_arrays_only(T, V, d, dtype, grad, add):
+    lib, g = B.load_library(), Guarded()
+    dY, tok = g((T, d), DT[dtype]), g((T,), torch.int64)
+    dY.copy_(normal((T, d), DT[dtype], T))
+    tok.copy_(torch.randint(-2, V + 2, (T,), generator=torch.Generator().manual_seed(T)))
+    dW = g((V, d), DT[grad], 0)
+    ws, n = workspace(g, lib.ckl_embedding_workspace_size, T, d, V)
+    B.check(lib.ckl_embedding_backward(dY.data_ptr(), int(dtype == "bf16"), T, d, tok.data_ptr(), 8, V, 0, 1.5,
+                                       dW.data_ptr(), int(grad == "bf16"), add, ws.data_ptr(), n, None))
+    g.check()
+    want = ckl.embedding_backward(dY.clone(), tok.clone(), V, 1.5, dw_dtype=DT[grad])
+    assert torch.equal(dW, want)  # (added to zeros: the same sums)
+
+
+@pytest.mark.parametrize("dtype,wtype", [("bf16", "f32"), ("f32", "bf16")])
+@pytest.mark.parametrize("T,d", [(1, 8), (1025, 72), (2050, 520), (5, 8200), (3, 32776)])
+def test_norm_writes_its_own_arrays_only(T, d, dtype, wtype):
+    lib, g = B.load_library(), Guarded()
+    t, bf, wbf, nb = DT[dtype], int(dtype == "bf16"), int(wtype == "bf16"), -(-d // 32)
+    x, dy, w = g((T, d), t), g((T, d), t), g((d,), DT[wtype])
+    for i, v in enumerate((x, dy, w)):
+        v.copy_(normal(tuple(v.shape), v.dtype, i))
+    y, codes, exps, rstd = g((T, d), t), g((T, d), torch.int8), g((T, nb), torch.uint8), g((T,), torch.float32)
+    B.check(lib.ckl_norm_forward(x.data_ptr(), bf, T, d, w.data_ptr(), wbf, 1e-6, y.data_ptr(), codes.data_ptr(),
+                                 exps.data_ptr(), rstd.data_ptr(), None))
+    dx, dw, out = g((T, d), t), g((d,), DT[wtype]), g((T, d), t)
+    ws, n = workspace(g, lib.ckl_norm_workspace_size, T, d)
+    B.check(lib.ckl_norm_backward(dy.data_ptr(), bf, T, d, codes.data_ptr(), exps.data_ptr(), rstd.data_ptr(),
+                                  w.data_ptr(), wbf, dx.data_ptr(), dw.data_ptr(), ws.data_ptr(), n, None))
+    B.check(lib.ckl_act_decode(codes.data_ptr(), exps.data_ptr(), T, d, rstd.data_ptr(), w.data_ptr(), wbf,
+                               out.data_ptr(), bf, None))
+    g.check()
+    for a, b in zip((y, codes, exps, rstd), ckl.norm_forward(x.clone(), w.clone())):
+        assert same_bits(a, b)
+    for a, b in zip((dx, dw), ckl.norm_backward(dy.clone(), codes.clone(), exps.clone(), rstd.clone(), w.clone())):
+        assert same_bits(a, b)
+    assert same_bits(out, ckl.act_decode(codes.clone(), exps.clone(), rstd.clone(), w.clone(), dtype=t))
