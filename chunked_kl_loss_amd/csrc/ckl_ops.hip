@@ -156,7 +156,7 @@ Units units(int64_t n) {
 // index.  What remains is sorted.  The common path, per vector of eight: eight
 // exponentials, one running maximum and one comparison.
 //
-// Bound by memory where there are many rows: 2048 x 201088 bf16, K = 100, 169 us
+// Bound by memory where there are many rows: 2048 x 201088 bf16, K = 100, 168 us
 // or 4.9 TB/s (four workgroups to a compute unit, the next tile's loads under
 // way while one is looked at).  For one row the steps' latency counts: 32000
 // columns 17 us, of which 3 for the first key, 2 a tile, 2.5 for the order.
@@ -916,7 +916,7 @@ __device__ __forceinline__ int64_t token_row(int64_t token, int64_t V, int64_t v
 
 // out[t] = scale W[token_t - v_offset]; a zero row for a token outside the table.
 // A thread takes four vectors, their tokens and then their rows loaded together.
-// Bound by memory: 32768 x 2880 bf16 55 us, 4.7 TB/s.
+// Bound by memory: 32768 x 2880 bf16 56 us, 4.6 TB/s.
 constexpr int kEmbedUnits = 4;
 template <typename T, typename I>
 __global__ __launch_bounds__(256) void embedding_forward_kernel(const T* __restrict__ W, int64_t V, int64_t v_offset,
@@ -1323,7 +1323,7 @@ __global__ __launch_bounds__(1024) void zero_kernel(Fill fill) { fill_instead(fi
 // NaN.
 //
 // A thread holds eight columns, four neighbouring lanes a block.  Encoding and
-// decoding are bound by memory: 131072 x 2880 bf16 195 us each way, 5.8 TB/s.
+// decoding are bound by memory: 131072 x 2880 bf16 192 and 208 us, 6.0 and 5.5 TB/s.
 __device__ __forceinline__ uint32_t top_bits(const float* f) {
   uint32_t a = 0;
 #pragma unroll
@@ -1427,7 +1427,9 @@ __device__ __forceinline__ float group_sum(float x, float* slots) {
 // y = x rstd weight with rstd = 1 / sqrt(mean x^2 + eps), and x in 8 bits for
 // the backward pass.  A workgroup takes a row; a thread holds NV vectors of eight
 // columns (vector v of the row in thread v mod blockDim), so that the row is read
-// once.  Bound by memory: 32768 x 2880 bf16 84 us, 5.7 TB/s.
+// once.  Bound by memory: 32768 x 2880 bf16 85 to 92 us by board, 5.2 to 5.6 TB/s;
+// not on rows below 512 columns, where most lanes of the row's wave have nothing
+// (262144 x 64: 78 us, 1.1 TB/s).
 template <typename T, int NV>
 __global__ __launch_bounds__(1024) void norm_forward_kernel(const T* __restrict__ x, int64_t rows, int nv,
                                                             const void* __restrict__ weight, int weight_bf16,
@@ -1474,7 +1476,11 @@ __global__ __launch_bounds__(1024) void norm_forward_kernel(const T* __restrict_
 //   dx = rstd (dy w - n mean(dy w n)),   dw = sum over rows of dy n.
 // A workgroup walks rows blockIdx, blockIdx + gridDim, ... and keeps its
 // columns' share of dw in registers; norm_dweight_kernel adds the workgroups.
-// Bound by memory: 32768 x 2880 bf16 87 us, 5.5 TB/s.
+// Bound by memory: 32768 x 2880 bf16 87 us, 5.5 TB/s.  Not on narrow rows, which
+// follow one another without the next one's loads under way (262144 x 64: 86 us,
+// 1.0 TB/s), nor on the widest, where four and eight vectors in each of 1024
+// threads leave few registers or too few (4096 x 32768: 227 us, 3.0 TB/s; 2048 x
+// 65536: 587 us, 1.2 TB/s).
 template <typename T, int NV>
 __global__ __launch_bounds__(1024) void norm_backward_kernel(const T* __restrict__ dy, int64_t rows, int nv,
                                                              const int8_t* __restrict__ codes,
@@ -1556,10 +1562,14 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // -------------------------------------------------------------- launchers --
 // Segments of whole tiles to a row: as many as make the call shortest when a
-// workgroup takes 2 us a tile by itself, all of them together read 5 bytes a
-// picosecond, and joining segments costs 8 us.  (us at bf16, K = 100, in 1 / 2 / 3
-// segments: 300 rows of 201088 59 / 51 / 48; 500 rows of 32000 21 / 27 / 27; 700
-// rows of 100000 45 / 63 / 64; one row of 201088 51 / 39 / 34, in 25 18.)
+// workgroup takes 2 us a tile by itself, all of them together read 2500 columns a
+// nanosecond, and joining segments costs 8 us.  (us at bf16, K = 100, in 1 / 2 / 3
+// segments: 300 rows of 201088 58 / 50 / 48; 600 rows of 32000 23 / 35 / 34; 600
+// rows of 201088 69 / 80 / 80; one row of 201088 51 / 39 / 34, in 25 20.)
+// The rule knows neither the type nor K, with which tiles and joining take
+// longer.  fp32: 300 rows of 201088 66 in the 3 it takes, 68 whole.  K = 1000: one
+// row 49 in 25, 46 in 13; 300 rows 87 in 3, 88 in 2, 96 whole.  It is off at
+// K = 4096: one row 140 in 25, 118 in 9; 300 rows 235 in 3, 178 whole.
 void topk_plan(int64_t rows, int64_t V, int* segments, int64_t* seg_cols) {
   const int64_t tiles = cdiv(V + 7, kTopkTile);
   const double read_us = (double)rows * V * 2 / 5e6;
@@ -1791,8 +1801,8 @@ using Count = std::integral_constant<int, N>;
 // Threads and vectors per thread for rows of nv vectors.  Two vectors a thread
 // have the loads in flight that one has in twice the threads, and half the waves
 // to wait for at the row's sum.  (32768 x 2880 bf16, forward: one vector in 384
-// threads 106 us, two in 192 84, three in 128 90, six in 64 109; backward 101,
-// 98, 101, 120.)  More than two where a workgroup's 1024 threads need it.
+// threads 110 us, two in 192 85, three in 128 91, six in 64 110; backward 134,
+// 98, 101, 308.)  More than two where a workgroup's 1024 threads need it.
 static void norm_shape(int nv, int* threads, int* per) {
   *per = nv <= 64 ? 1 : nv <= 2048 ? 2 : nv <= 4096 ? 4 : 8;
   *threads = (int)cdiv(cdiv(nv, *per), 64) * 64;

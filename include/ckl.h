@@ -361,7 +361,9 @@ ckl_status ckl_act_decode(const int8_t* codes, const uint8_t* exps, int64_t T, i
 
 /* RMS norm that saves its input in 8 bits: rstd[t] = 1 / sqrt(mean_i x[t,i]^2 + eps),
  * y = x * rstd * weight (in fp32, rounded once), codes and exps of x as
- * ckl_act_encode writes them.
+ * ckl_act_encode writes them.  The mean of squares is an fp32 sum: rows with values
+ * past 1.8e19 overflow it (y is then 0, NaN where x is infinite), and eps should
+ * keep rows of values below 1e-19 from vanishing in it.
  *   x, y: [T, d] dtype.  weight: [d] weight_dtype.  rstd: [T] float32.
  *   codes, exps and rstd may all be NULL where no backward pass follows. */
 ckl_status ckl_norm_forward(const void* x, int32_t dtype, int64_t T, int64_t d, const void* weight,
