@@ -375,3 +375,37 @@ def test_norm_writes_its_own_arrays_only(T, d, dtype, wtype):
     for a, b in zip((dx, dw), ckl.norm_backward(dy.clone(), codes.clone(), exps.clone(), rstd.clone(), w.clone())):
         assert same_bits(a, b)
     assert same_bits(out, ckl.act_decode(codes.clone(), exps.clone(), rstd.clone(), w.clone(), dtype=t))
+
+
+# --------------------------------------------------------------- captured --
+@pytest.mark.parametrize("fused", [False, True])
+def test_masked_gradients_replay_with_new_inputs(fused):
+    # the norm before the loss with a mask, forward and backward in one graph
+    def inputs(seed):
+        X, W, idx, tl, mask = loss_inputs(seed=seed)
+        X[~mask, ::3] = math.nan
+        return [X, W, idx, tl, mask, (1 + normal((72,), torch.float32, seed + 5, 0.1)).cuda()]
+
+    def grads(X, W, idx, tl, mask, nw):
+        leaves = [v.detach().requires_grad_(True) for v in (X, W, nw)]
+        loss = ckl.chunked_kl_loss(leaves[0], leaves[1], idx, tl, mask, chunk=128, fused=fused, save_8bit=True,
+                                   norm_weight=leaves[2])
+        return [loss.detach(), *torch.autograd.grad(loss, leaves)]
+    ins = inputs(1)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        grads(*ins)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = grads(*ins)
+    for seed in (1, 40, 80, 40):
+        for a, b in zip(ins, inputs(seed)):
+            a.copy_(b)
+        want = [t.clone() for t in grads(*inputs(seed))]
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(outs, want):
+            assert bool(torch.isfinite(a).all()) and same_bits(a, b)
