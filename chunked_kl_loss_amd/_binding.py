@@ -22,6 +22,8 @@ CKL_F32 = 0
 CKL_BF16 = 1
 CKL_TEACHER_LOGITS = 0
 CKL_TEACHER_LOGPROBS = 1
+CKL_QUANT_INT8 = 1
+CKL_QUANT_E4M3 = 2
 
 EXPORTED = (
     "ckl_workspace_size",
@@ -44,6 +46,17 @@ EXPORTED = (
     "ckl_norm_forward",
     "ckl_norm_workspace_size",
     "ckl_norm_backward",
+    "ckl_logprob_workspace_size",
+    "ckl_token_logprobs",
+    "ckl_token_logprobs_backward",
+    "ckl_head_workspace_size",
+    "ckl_head_logprobs",
+    "ckl_head_logprobs_backward",
+    "ckl_dropout",
+    "ckl_add_norm_forward",
+    "ckl_add_norm_workspace_size",
+    "ckl_add_norm_backward",
+    "ckl_add_norm_quant",
     "ckl_timing_enable",
     "ckl_timing_read",
     "ckl_status_string",
@@ -134,6 +147,31 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.ckl_norm_workspace_size.restype = i32
     lib.ckl_norm_backward.argtypes = [vp, i32, i64, i64, vp, vp, vp, vp, i32, vp, vp, vp, sz, vp]
     lib.ckl_norm_backward.restype = i32
+    f64, u64 = ctypes.c_double, ctypes.c_uint64
+    lib.ckl_logprob_workspace_size.argtypes = [i64, i64, i64, szp]
+    lib.ckl_logprob_workspace_size.restype = i32
+    lib.ckl_token_logprobs.argtypes = [vp, i32, i64, i64, vp, i32, i64, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.ckl_token_logprobs.restype = i32
+    lib.ckl_token_logprobs_backward.argtypes = [vp, i32, i64, i64, vp, i32, vp, vp, vp, vp, vp, vp, vp]
+    lib.ckl_token_logprobs_backward.restype = i32
+    lib.ckl_head_workspace_size.argtypes = [i64, i64, i64, i64, i32, i32, i32, i32, ctypes.c_int, szp]
+    lib.ckl_head_workspace_size.restype = i32
+    lib.ckl_head_logprobs.argtypes = [vp, vp, i32, i64, i64, i64, vp, i32, vp, i64, vp, vp, vp, vp, sz, vp]
+    lib.ckl_head_logprobs.restype = i32
+    lib.ckl_head_logprobs_backward.argtypes = [vp, vp, i32, i64, i64, i64, vp, i32, vp, i64, vp, vp, vp, vp, vp, i32,
+                                               vp, i32, vp, sz, vp]
+    lib.ckl_head_logprobs_backward.restype = i32
+    lib.ckl_dropout.argtypes = [vp, i32, i64, f64, u64, u64, vp, vp, vp]
+    lib.ckl_dropout.restype = i32
+    lib.ckl_add_norm_forward.argtypes = [vp, i32, vp, i32, i64, i64, vp, i32, f32, f64, u64, u64, vp, vp, vp, vp, vp]
+    lib.ckl_add_norm_forward.restype = i32
+    lib.ckl_add_norm_workspace_size.argtypes = [i64, i64, szp]
+    lib.ckl_add_norm_workspace_size.restype = i32
+    lib.ckl_add_norm_backward.argtypes = [vp, i32, vp, i32, i64, i64, vp, vp, vp, i32, f64, u64, u64, vp, vp, vp, vp,
+                                          vp, sz, vp]
+    lib.ckl_add_norm_backward.restype = i32
+    lib.ckl_add_norm_quant.argtypes = [vp, i32, vp, i32, i64, i64, vp, i32, f32, i32, vp, vp, vp, vp]
+    lib.ckl_add_norm_quant.restype = i32
     lib.ckl_timing_enable.argtypes = [ctypes.c_int]
     lib.ckl_timing_enable.restype = i32
     lib.ckl_timing_read.argtypes = [ctypes.c_int, ctypes.POINTER(ctypes.c_double), i64p]

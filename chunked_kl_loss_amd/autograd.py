@@ -15,7 +15,11 @@ their log-sum-exp; with a norm before the head, the norm's input is what is
 saved, once for the norm's gradient and the head's.
 
 Embedding and RMSNorm8Bit: the embedding by a table of the head's shape, and the
-norm that saves its input in 8 bits."""
+norm that saves its input in 8 bits.
+
+TokenLogprobs and HeadLogprobs: log probabilities of given tokens and entropies,
+from logits and from states and head.  Dropout and AddRMSNorm: dropout with a mask
+that is formed again in the backward pass, and the norm with the residual's addition."""
 from __future__ import annotations
 
 import torch
@@ -148,6 +152,95 @@ class RMSNorm8Bit(torch.autograd.Function):
         return dx, dweight, None, None
 
 
+class TokenLogprobs(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, tokens, top, mask):
+        logprob, entropy, lse, top_idx, top_logprob = ops.token_logprobs_forward(logits, tokens, top, mask)
+        ctx.save_for_backward(logits, tokens, mask, lse, entropy)
+        ctx.mark_non_differentiable(top_idx, top_logprob)
+        ctx.set_materialize_grads(False)
+        return logprob, entropy, top_idx, top_logprob
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dlogprob, dentropy, _idx, _top):
+        if dlogprob is None and dentropy is None:
+            return None, None, None, None
+        logits, tokens, mask, lse, entropy = ctx.saved_tensors
+        return ops.token_logprobs_backward(_contiguous(dlogprob), _contiguous(dentropy), logits, tokens, lse, entropy,
+                                           mask), None, None, None
+
+
+class HeadLogprobs(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, H, W, tokens, mask, chunk):
+        logprob, entropy, lse = ops.head_logprobs_forward(H, W, tokens, mask, chunk)
+        ctx.save_for_backward(H, W, tokens, mask, lse, entropy)
+        ctx.set_materialize_grads(False)
+        ctx.chunk = chunk
+        return logprob, entropy
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dlogprob, dentropy):
+        if dlogprob is None and dentropy is None:
+            return None, None, None, None, None
+        H, W, tokens, mask, lse, entropy = ctx.saved_tensors
+        dH, dW = ops.head_logprobs_backward(_contiguous(dlogprob), _contiguous(dentropy), H, W, tokens, lse, entropy,
+                                            mask, ctx.chunk, dw_dtype=W.dtype, need_dh=ctx.needs_input_grad[0],
+                                            need_dw=ctx.needs_input_grad[1])
+        return dH, dW, None, None, None
+
+
+class Dropout(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, p, seed, offset):
+        ctx.p, ctx.offset = p, offset
+        ctx.seed, state = _saved_seed(seed)
+        ctx.save_for_backward(state)
+        return ops.dropout_forward(x, p, seed, offset)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad):
+        (state,) = ctx.saved_tensors
+        return ops.dropout_forward(grad.contiguous(), ctx.p, ctx.seed if state is None else state, ctx.offset), \
+            None, None, None
+
+
+class AddRMSNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, weight, eps, p, seed, offset):
+        y, h, rstd = ops.add_norm_forward(x, residual, weight, eps, p, seed, offset)
+        ctx.p, ctx.offset, ctx.x_dtype = p, offset, x.dtype
+        ctx.seed, state = _saved_seed(seed) if p else (0, None)
+        ctx.save_for_backward(h, rstd, weight, state)
+        ctx.set_materialize_grads(False)
+        return y, h
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dh):
+        h, rstd, weight, state = ctx.saved_tensors
+        if dy is None and dh is None:
+            return None, None, None, None, None, None, None
+        if dy is None:  # the norm's output was not used
+            dy = torch.zeros_like(h, dtype=ctx.x_dtype)
+        dx, dresidual, dweight = ops.add_norm_backward(dy.contiguous(), _contiguous(dh), h, rstd, weight, ctx.p,
+                                                       ctx.seed if state is None else state, ctx.offset)
+        return dx, dresidual, dweight, None, None, None, None
+
+
+def _contiguous(t):
+    return None if t is None else t.contiguous()
+
+
+def _saved_seed(seed):
+    """(seed, state) to keep for a backward pass: an integer, or a copy of the tensor as it is now (the caller's may
+    move on before the backward pass runs)."""
+    return (0, seed.clone()) if isinstance(seed, torch.Tensor) else (seed, None)
+
+
 def _needs_function(requires_grad: bool) -> bool:
     """Whether a call whose inputs require a gradient or not has to go through its Function: where a gradient is
     asked for, and in a forward-mode context, where the Function refuses tangents (the raw call would drop them)."""
@@ -177,6 +270,56 @@ def rms_norm_8bit(x, weight, eps: float = 1e-6):
     that of the exact x; the backward pass reads x from 8 bits (ops.act_encode), so that the norm keeps d bytes a
     row instead of x."""
     return _norm(x, weight, eps)
+
+
+def token_logprobs(logits, tokens, top: int = 0, mask=None):
+    """(logprob, entropy, top_idx, top_logprob) of rows of logits [..., V]: the log probability of tokens [...] (int32 /
+    int64; 0 for a token outside [0, V), such as padding) and the entropy of the row's softmax, float32 [...] and
+    differentiable with respect to the logits; and the `top` most likely columns in descending order (equal ones by
+    index) with their log probabilities, [..., top], without gradient (top 0: empty).  Rows whose mask (uint8 / bool
+    [...]) is 0 are not read; they get 0 and no gradient.  A logit of -inf is a forbidden token: log probability
+    -inf, no entropy, no gradient; a row of nothing else has entropy 0."""
+    logits, tokens, mask = logits.contiguous(), tokens.contiguous(), _contiguous(mask)
+    if not _needs_function(logits.requires_grad):
+        logprob, entropy, _, top_idx, top_logprob = ops.token_logprobs_forward(logits, tokens, top, mask)
+        return logprob, entropy, top_idx, top_logprob
+    return TokenLogprobs.apply(logits, tokens, top, mask)
+
+
+def head_logprobs(H, W, tokens, mask=None, chunk: int = 2048):
+    """(logprob, entropy) of tokens [...] under softmax(H W^T), float32 [...], differentiable with respect to H [..., d]
+    and W [V, d] (bf16 or fp32), whose logits are never stored: the cross entropy of hard labels beside the
+    distillation loss, a policy's log probabilities, the score of a text.  Masked rows (mask uint8 / bool [...] 0)
+    are not computed, whatever H holds there; they get 0 and no gradient.  A token outside [0, V) gets a log
+    probability of 0 and no gradient through it.  chunk bounds what the backward pass holds (about chunk x V logit
+    gradients), which multiplies the logits again."""
+    H, W, tokens, mask = H.contiguous(), W.contiguous(), tokens.contiguous(), _contiguous(mask)
+    if not _needs_function(H.requires_grad or W.requires_grad):
+        return ops.head_logprobs_forward(H, W, tokens, mask, chunk)[:2]
+    return HeadLogprobs.apply(H, W, tokens, mask, chunk)
+
+
+def dropout(x, p: float, seed=0, offset: int = 0):
+    """x / (1 - p) where kept, 0 elsewhere, differentiable; the mask is a function of (seed, offset, element), formed
+    again in the backward pass and never stored.  Different layers or steps take different seeds or offsets.  p is
+    taken to the nearest multiple of 2^-16.  seed: an integer, or an int64 tensor (seed, offset) on the GPU, read
+    when the kernels run (a captured graph draws anew when the tensor changes between replays); its offset is added
+    to this one."""
+    x = x.contiguous()
+    if not _needs_function(x.requires_grad):
+        return ops.dropout_forward(x, p, seed, offset)
+    return Dropout.apply(x, p, seed, offset)
+
+
+def add_rms_norm(x, residual, weight, eps: float = 1e-6, p: float = 0.0, seed=0, offset: int = 0):
+    """(y, h): h = residual + dropout(x, p, seed, offset), the residual stream, and y its RMS norm over the last
+    dimension times weight [d]; differentiable with respect to x, residual [..., d] and weight.  h has the residual's
+    type (x's, or float32 with x in bf16), y x's; the norm is that of the rounded h, which is what the backward
+    pass keeps (4 bytes a row besides it)."""
+    x, residual, weight = x.contiguous(), residual.contiguous(), weight.contiguous()
+    if not _needs_function(x.requires_grad or residual.requires_grad or weight.requires_grad):
+        return ops.add_norm_forward(x, residual, weight, eps, p, seed, offset, save=False)[:2]
+    return AddRMSNorm.apply(x, residual, weight, eps, p, seed, offset)
 
 
 def chunked_kl_loss(H, W, idx, tlogit, mask=None, chunk: int = 2048, fused: bool = False, teacher_form: int = 0,

@@ -13,7 +13,9 @@ import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SOURCES = [os.path.join(HERE, "csrc", f) for f in ("ckl_kernels.hip", "ckl_api.hip", "ckl_ops.hip", "ckl_ops_api.hip")]
+SOURCES = [os.path.join(HERE, "csrc", f)
+           for f in ("ckl_kernels.hip", "ckl_api.hip", "ckl_ops.hip", "ckl_ops_api.hip", "ckl_logprob.hip", "ckl_head.hip",
+                     "ckl_logprob_api.hip", "ckl_residual.hip", "ckl_residual_api.hip")]
 LIB = os.path.join(HERE, "libckl.so")
 ARCH = os.environ.get("CKL_OFFLOAD_ARCH", "gfx950")
 

@@ -1,0 +1,454 @@
+// gfx950 kernels of the log probabilities of given tokens, and of the rows'
+// entropies, straight from hidden states and the output head: the logits never
+// leave the MFMA accumulators.
+//   head_tokens   the rows' tokens as columns, in the order of the (packed) rows
+//   head_rows     z^T = W H^T by tiles; a row's log sum exp and sum of p log p
+//                 behind a running maximum, the token's logit where it falls
+//   head_finish   splits merged; log probability, entropy, log sum exp
+// Backward (the logits are multiplied again, G = dloss / dz by blocks):
+//   head_consts   what a row's gradient needs
+//   head_grad     G = 1[v = token] a - q (a + b (log q + entropy))
+// and the contractions dH = G W, dW = G^T H of the distillation loss.
+#include "ckl_head.hpp"
+
+#include <type_traits>
+
+#include "ckl_tile.hpp"
+
+namespace ckl {
+
+namespace {
+
+using CfgWide = Dma64Cfg<256, 256, 128, 64>;
+using CfgF32 = TileCfg<float, 128, 128, 64, 64>;
+
+constexpr float kExpZero = -1e4f;  // 2^x is zero from here on, and its product with x too
+
+// A shift of (m, s, e) and its sum with another, in base 2: s = sum of 2^(x - m),
+// e = sum of (x - m) 2^(x - m).
+__device__ __forceinline__ void ent2_merge(float& m, float& s, float& e, float m2, float s2, float e2) {
+  const float mn = fmaxf(m, m2);
+  const float d1 = m == mn ? 0.f : fmaxf(m - mn, kExpZero), d2 = m2 == mn ? 0.f : fmaxf(m2 - mn, kExpZero);
+  const float f1 = fast_exp2(d1), f2 = fast_exp2(d2);
+  e = f1 * (e + d1 * s) + f2 * (e2 + d2 * s2);
+  s = f1 * s + f2 * s2;
+  m = mn;
+}
+
+// tok[i] = the column of row i's token, -1 where it is none (or row i is past the
+// rows).  perm not NULL: row i is row perm[i] of the call, for i < *n.
+__global__ __launch_bounds__(256) void head_tokens_kernel(const void* __restrict__ tokens, int tokens64, int T, int Tp,
+                                                          int V, const int* __restrict__ perm,
+                                                          const int* __restrict__ n, int* __restrict__ tok) {
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= Tp) return;
+  int c = -1;
+  if (i < (n != nullptr ? *n : T)) {
+    const int t = perm != nullptr ? perm[i] : i;
+    const int64_t v = tokens64 ? reinterpret_cast<const int64_t*>(tokens)[t]
+                               : (int64_t)reinterpret_cast<const int32_t*>(tokens)[t];
+    if (v >= 0 && v < V) c = (int)v;
+  }
+  tok[i] = c;
+}
+
+// ---------------------------------------------------------------- forward --
+// A workgroup takes a block of BN rows and a run of vocabulary tiles, and walks
+// the tiles with the rows' running (m, s, e).  With two column blocks a wave, lane
+// group g owns block g's state; with one, both groups hold it.  Bound by the
+// matrix units: beside the logits' product an element costs one exponential and
+// three more operations.
+constexpr int kGroupRows = 8;  // row blocks that walk the vocabulary together (they share W's tiles in an XCD's L2)
+
+template <class C>
+__global__ __launch_bounds__(C::NTHREADS) void head_rows_kernel(
+    const typename C::TIn* __restrict__ H, const typename C::TIn* __restrict__ W, int T, int d, int V,
+    const int* __restrict__ tok, float* __restrict__ ztok, float4* __restrict__ part, int n_vtiles,
+    int tiles_per_split, int n_tblocks, int n_splits, const int* __restrict__ nrows, int row0) {
+  using TileT = typename C::TileT;
+  using L = typename TileT::L;
+  constexpr int MBK = TileT::MBK, NBK = TileT::NBK, BLK = L::BLK, RPB = L::RPB;
+  static_assert(L::GROUPS == 2 && BLK == 32 && (NBK == 1 || NBK == 2), "columns of a wave");
+  __shared__ __attribute__((aligned(16))) char smem[C::LDS_BYTES];
+  const int lane = threadIdx.x & 63;
+  const int wave = wave_id();
+  const int wave_m = wave / C::WAVES_N, wave_n = wave % C::WAVES_N;
+  int tblock, split;
+  grouped_mn(xcd_remap(blockIdx.x, n_tblocks * n_splits), n_tblocks, n_splits, kGroupRows, tblock, split);
+  const int t0 = tblock * C::BN;
+  if (nrows != nullptr && t0 >= *nrows - row0) return;  // packed rows: no kept row here (its results are never read)
+  const int vt0 = split * tiles_per_split;
+  const int vt1 = min(n_vtiles, vt0 + tiles_per_split);
+  const int own_nb = NBK == 1 ? 0 : lane / 32;
+  const int own_row = t0 + wave_n * C::WN + own_nb * BLK + (lane & 31);
+  const int own_tok = own_row < T ? tok[own_row] : -1;
+  float rm = -INFINITY, rs = 0.f, re = 0.f;
+
+  TileT tile;
+  constexpr bool kAhead = PrefetchOK<C>::value;  // the next tile's first slices go out behind a tile's epilogue
+  const typename C::TIn* Ht0 = H + (int64_t)t0 * d;
+  if constexpr (kAhead)
+    if (vt0 < vt1) tile_k64_prologue<C>(W + (int64_t)vt0 * C::BM * d, d, V - vt0 * C::BM, Ht0, d, T - t0, d, smem);
+  for (int vt = vt0; vt < vt1; ++vt) {
+    const int v0 = vt * C::BM;
+    if constexpr (kAhead)
+      run_mma<C, true>(tile, W + (int64_t)v0 * d, d, V - v0, Ht0, d, T - t0, d, smem);
+    else
+      run_mma(tile, W + (int64_t)v0 * d, d, V - v0, Ht0, d, T - t0, d, smem);
+    if constexpr (kAhead)
+      if (vt + 1 < vt1)
+        tile_k64_prologue<C>(W + (int64_t)(v0 + C::BM) * d, d, V - v0 - C::BM, Ht0, d, T - t0, d, smem);
+    const int vbase = v0 + wave_m * C::WM;
+    const bool full = vbase + C::WM <= V;  // every row of the wave's slice is a vocabulary row
+#pragma unroll
+    for (int nb = 0; nb < NBK; ++nb) {
+      const int src = NBK == 1 ? lane : (lane & 31) + nb * 32;  // the owner of this lane's column
+      const bool own = NBK == 1 || own_nb == nb;
+      if (!full) {  // the last tile: columns past the vocabulary count for nothing
+#pragma unroll
+        for (int mb = 0; mb < MBK; ++mb)
+#pragma unroll
+          for (int r = 0; r < RPB; ++r)
+            if (vbase + mb * BLK + L::row_in(r, lane) >= V) tile.acc[mb][nb][r] = -INFINITY;
+      }
+      // the token's logit, by the lane that holds it
+      const int vl = __shfl(own_tok, src) - vbase;
+      if (vl >= 0 && vl < C::WM && L::group_of(vl & 31) == lane / 32) {
+        const int sel = (vl / BLK) * RPB + L::reg_of(vl & 31);
+        float z = 0.f;
+#pragma unroll
+        for (int q = 0; q < MBK * RPB; ++q) z = (q == sel) ? tile.acc[q / RPB][nb][q % RPB] : z;
+        ztok[opaque(t0 + wave_n * C::WN + nb * BLK + (lane & 31))] = z;
+      }
+      float mx = -INFINITY;
+#pragma unroll
+      for (int mb = 0; mb < MBK; ++mb)
+#pragma unroll
+        for (int r = 0; r < RPB; ++r) mx = fmaxf(mx, tile.acc[mb][nb][r]);
+      mx = fmaxf(mx, __shfl_xor(mx, 32)) * kLog2e;
+      const float crm = __shfl(rm, src);
+      const float mn = fmaxf(crm, mx);
+      float ssum = 0.f, esum = 0.f;
+      if (full) {
+#pragma unroll
+        for (int mb = 0; mb < MBK; ++mb)
+#pragma unroll
+          for (int r = 0; r < RPB; ++r) {
+            const float x = tile.acc[mb][nb][r] * kLog2e - mn, u = fast_exp2(x);
+            ssum += u;
+            esum = fmaf(u, x, esum);
+          }
+      } else if (mn > -INFINITY) {
+#pragma unroll
+        for (int mb = 0; mb < MBK; ++mb)
+#pragma unroll
+          for (int r = 0; r < RPB; ++r) {
+            const float x = fmaxf(tile.acc[mb][nb][r] * kLog2e - mn, kExpZero), u = fast_exp2(x);
+            ssum += u;
+            esum = fmaf(u, x, esum);
+          }
+      }
+      ssum += __shfl_xor(ssum, 32);
+      esum += __shfl_xor(esum, 32);
+      if (own && mn > -INFINITY) {
+        const float dm = fmaxf(rm - mn, kExpZero), f = fast_exp2(dm);
+        re = fmaf(f, fmaf(dm, rs, re), esum);
+        rs = fmaf(f, rs, ssum);
+        rm = mn;
+      }
+    }
+  }
+
+  // the waves that share the same rows
+  wait_vmcnt<0>();
+  __syncthreads();
+  float4* red = reinterpret_cast<float4*>(smem);  // [WAVES_M][BN]
+  static_assert(C::WAVES_M * C::BN * 16 <= C::LDS_BYTES, "states");
+  if (NBK == 2 || lane < 32) red[wave_m * C::BN + wave_n * C::WN + lane] = make_float4(rm, rs, re, 0.f);
+  __syncthreads();
+  for (int i = threadIdx.x; i < C::BN; i += C::NTHREADS) {
+    float4 a = red[i];
+#pragma unroll
+    for (int w = 1; w < C::WAVES_M; ++w) {
+      const float4 b = red[w * C::BN + i];
+      ent2_merge(a.x, a.y, a.z, b.x, b.y, b.z);
+    }
+    if (t0 + i < T) part[(int64_t)split * T + t0 + i] = a;
+  }
+}
+
+// Row t of the call: sixteen lanes merge its splits.  rank not NULL: its place
+// among the packed rows, -1 where it is masked (all results zero then).  T rows of
+// the call from row0 on; part and ztok are of this launch's rows, [S][rows].
+__global__ __launch_bounds__(256) void head_finish_kernel(const float4* __restrict__ part, int S, int rows, int row0,
+                                                          const float* __restrict__ ztok, const int* __restrict__ tok,
+                                                          const int* __restrict__ perm, const int* __restrict__ n,
+                                                          float* __restrict__ logprob, float* __restrict__ entropy,
+                                                          float* __restrict__ lse) {
+  const int sub = threadIdx.x & 15;
+  const int i = blockIdx.x * 16 + (threadIdx.x >> 4);
+  const bool live = i < rows && (n == nullptr || row0 + i < *n);
+  float m = -INFINITY, s = 0.f, e = 0.f;
+  if (live)
+    for (int k = sub; k < S; k += 16) {
+      const float4 v = part[(int64_t)k * rows + i];
+      ent2_merge(m, s, e, v.x, v.y, v.z);
+    }
+#pragma unroll
+  for (int o = 1; o < 16; o *= 2) {
+    const float om = __shfl_xor(m, o), os = __shfl_xor(s, o), oe = __shfl_xor(e, o);
+    ent2_merge(m, s, e, om, os, oe);
+  }
+  if (sub != 0 || !live) return;
+  const int t = perm != nullptr ? perm[row0 + i] : row0 + i;
+  const float l2 = fast_log2(s), l = (m + l2) * kLn2;
+  float ent = (l2 - e / s) * kLn2;
+  lse[t] = l;
+  entropy[t] = ent < 0.f ? 0.f : ent;
+  logprob[t] = tok[i] >= 0 ? ztok[i] - l : 0.f;
+}
+
+// Results of masked rows.
+__global__ __launch_bounds__(256) void head_masked_kernel(const int* __restrict__ rank, int T,
+                                                          float* __restrict__ logprob, float* __restrict__ entropy,
+                                                          float* __restrict__ lse) {
+  const int t = blockIdx.x * 256 + threadIdx.x;
+  if (t < T && rank[t] < 0) logprob[t] = entropy[t] = lse[t] = 0.f;
+}
+
+// --------------------------------------------------------------- backward --
+// With q = 2^x, x = z log2 e - lse log2 e, the gradient of a row's logits is
+//   q (c0 + c1 x) + 1[v = token] a,   c0 = -(a + b entropy),   c1 = -b ln 2
+// for its incoming gradients a (log probability) and b (entropy).  Row i:
+// consts[i] = (c0, lse log2 e, c1, a), its token.  Rows past the last one and rows
+// with no gradient get an lse that makes q zero.
+__global__ __launch_bounds__(256) void head_consts_kernel(const void* __restrict__ tokens, int tokens64, int T, int Tp,
+                                                          int V, const int* __restrict__ perm,
+                                                          const int* __restrict__ n, const float* __restrict__ lse,
+                                                          const float* __restrict__ entropy,
+                                                          const float* __restrict__ dlogprob,
+                                                          const float* __restrict__ dentropy,
+                                                          float4* __restrict__ consts, int* __restrict__ tok) {
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= Tp) return;
+  int c = -1;
+  float4 k = make_float4(0.f, 1e30f, 0.f, 0.f);
+  if (i < (n != nullptr ? *n : T)) {
+    const int t = perm != nullptr ? perm[i] : i;
+    const int64_t v = tokens64 ? reinterpret_cast<const int64_t*>(tokens)[t]
+                               : (int64_t)reinterpret_cast<const int32_t*>(tokens)[t];
+    if (v >= 0 && v < V) c = (int)v;
+    const float a = c >= 0 && dlogprob != nullptr ? dlogprob[t] : 0.f;
+    const float b = dentropy != nullptr ? dentropy[t] : 0.f;
+    if (!(a == 0.f && b == 0.f))
+      k = make_float4(b == 0.f ? -a : -(a + b * entropy[t]), lse[t] * kLog2e, -b * kLn2, a);
+  }
+  consts[i] = k;
+  tok[i] = c;
+}
+
+// The G block of rows [tb0, tb0 + BN n_tblocks) and columns [vb0, vb0 + BM
+// n_vtiles): G[t - tb0][v - vb0], and for fp32 also its transpose Gt.  bf16 rounds
+// G once (its contractions read bf16 operands; 2^-9 of each entry, like the
+// operands themselves); rows past T and columns past V get 0.  Tiles leave through
+// the LDS as 512-byte runs of G's rows, behind the issue of the next tile's first
+// slices.
+template <class C>
+__global__ __launch_bounds__(C::NTHREADS) void head_grad_kernel(
+    const typename C::TIn* __restrict__ H, const typename C::TIn* __restrict__ W, int T, int d, int V,
+    const float4* __restrict__ consts, const int* __restrict__ tok, int tb0, int vb0, int n_vtiles,
+    int tiles_per_split, int n_tblocks, int n_splits, typename C::TIn* __restrict__ G, int64_t ldG,
+    typename C::TIn* __restrict__ Gt, int64_t ldGt, const int* __restrict__ nrows) {
+  using TIn = typename C::TIn;
+  constexpr bool kStage = std::is_same<TIn, bf16_t>::value;
+  static_assert(!kStage || (C::BM == 256 && C::BN == 256 && C::WM == 128 && C::LDS_BYTES >= 256 * 256 * 2 &&
+                            PrefetchOK<C>::value), "staged tiles");
+  __shared__ __attribute__((aligned(16))) char smem[C::LDS_BYTES + C::BN * 20];
+  float4* s_row = reinterpret_cast<float4*>(smem + C::LDS_BYTES);
+  int* s_tok = reinterpret_cast<int*>(smem + C::LDS_BYTES + C::BN * 16);
+  uint16_t* stg = reinterpret_cast<uint16_t*>(smem);
+  // 16-byte chunk c of row t sits at c ^ (t / 8): the column reads of eight rows spread over the banks
+  auto stage_chunk = [](int t, int c) { return c ^ ((t >> 3) & 31); };
+  (void)stg;
+  (void)stage_chunk;
+  const int lane = threadIdx.x & 63;
+  const int wave = wave_id();
+  const int wave_m = wave / C::WAVES_N, wave_n = wave % C::WAVES_N;
+  int tblock, split;
+  grouped_mn(xcd_remap(blockIdx.x, n_tblocks * n_splits), n_tblocks, n_splits, kGroupRows, tblock, split);
+  const int t0 = tb0 + tblock * C::BN;
+  if (nrows != nullptr && t0 >= *nrows) return;  // packed rows: the contractions read no G row of this block
+  const int vt0 = split * tiles_per_split;
+  const int vt1 = min(n_vtiles, vt0 + tiles_per_split);
+  for (int i = threadIdx.x; i < C::BN; i += C::NTHREADS) {
+    s_row[i] = consts[t0 + i];
+    s_tok[i] = tok[t0 + i];
+  }
+  __syncthreads();
+  typename C::TileT tile;
+  const TIn* Ht0 = H + (int64_t)t0 * d;
+  if constexpr (kStage)
+    if (vt0 < vt1)
+      tile_k64_prologue<C>(W + (int64_t)(vb0 + vt0 * C::BM) * d, d, V - vb0 - vt0 * C::BM, Ht0, d, T - t0, d, smem);
+  for (int vt = vt0; vt < vt1; ++vt) {
+    const int v0 = vb0 + vt * C::BM;
+    if constexpr (kStage)
+      run_mma<C, true>(tile, W + (int64_t)v0 * d, d, V - v0, Ht0, d, T - t0, d, smem);
+    else
+      run_mma(tile, W + (int64_t)v0 * d, d, V - v0, Ht0, d, T - t0, d, smem);
+    const int vbase = v0 + wave_m * C::WM;
+    const bool full = vbase + C::WM <= V;
+#pragma unroll
+    for (int nb = 0; nb < C::NB; ++nb) {
+      const int tl = opaque(wave_n * C::WN + nb * 32 + (lane & 31));  // (addresses formed here, not held across the loop)
+      const float4 rc = s_row[tl];
+#pragma unroll
+      for (int mb = 0; mb < C::MB; ++mb)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const float x = tile.acc[mb][nb][r] * kLog2e - rc.y;
+          tile.acc[mb][nb][r] = fast_exp2(x) * fmaf(rc.z, x, rc.x);
+        }
+      if (!full) {
+#pragma unroll
+        for (int mb = 0; mb < C::MB; ++mb)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (vbase + mb * 32 + acc_row(r, lane) >= V) tile.acc[mb][nb][r] = 0.f;
+      }
+      const int tk = s_tok[tl], vl = tk - vbase;
+      if (tk >= 0 && vl >= 0 && vl < C::WM && ((vl >> 2) & 1) == lane / 32) {
+        const int sel = (vl >> 5) * 16 + ((vl & 31) >> 3) * 4 + (vl & 3);
+#pragma unroll
+        for (int q = 0; q < C::MB * 16; ++q)
+          if (q == sel) tile.acc[q / 16][nb][q % 16] += rc.w;
+      }
+      if constexpr (kStage) {
+        uint2* row = reinterpret_cast<uint2*>(stg + tl * 256);
+#pragma unroll
+        for (int mb = 0; mb < C::MB; ++mb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            row[stage_chunk(tl, wave_m * 16 + mb * 4 + i) * 2 + (lane >> 5)] =
+                make_uint2(pack_bf16x2(tile.acc[mb][nb][4 * i], tile.acc[mb][nb][4 * i + 1]),
+                           pack_bf16x2(tile.acc[mb][nb][4 * i + 2], tile.acc[mb][nb][4 * i + 3]));
+      } else {
+        const int64_t trow = t0 + tl - tb0;
+#pragma unroll
+        for (int mb = 0; mb < C::MB; ++mb)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int vcol = vbase - vb0 + mb * 32 + acc_row(r, lane);
+            Gt[(int64_t)vcol * ldGt + trow] = tile.acc[mb][nb][r];
+          }
+#pragma unroll
+        for (int mb = 0; mb < C::MB; ++mb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<f32x4*>(G + trow * ldG + (vbase - vb0 + mb * 32 + 8 * i + 4 * (lane >> 5))) =
+                f32x4{tile.acc[mb][nb][4 * i], tile.acc[mb][nb][4 * i + 1], tile.acc[mb][nb][4 * i + 2],
+                      tile.acc[mb][nb][4 * i + 3]};
+      }
+    }
+    if constexpr (kStage) {
+      __syncthreads();
+      const int tid = opaque(threadIdx.x);
+      constexpr int kPasses = 256 / (C::NTHREADS / 32);
+      u32x4 out[kPasses];
+#pragma unroll
+      for (int pass = 0; pass < kPasses; ++pass) {
+        const int tl = pass * (C::NTHREADS / 32) + (tid >> 5), q = tid & 31;
+        out[pass] = reinterpret_cast<const u32x4*>(stg + tl * 256)[stage_chunk(tl, q)];
+      }
+      __syncthreads();
+      if (vt + 1 < vt1)
+        tile_k64_prologue<C>(W + (int64_t)(v0 + C::BM) * d, d, V - v0 - C::BM, Ht0, d, T - t0, d, smem);
+      bf16_t* Gtile = reinterpret_cast<bf16_t*>(G) + (int64_t)(t0 - tb0) * ldG + (v0 - vb0);
+#pragma unroll
+      for (int pass = 0; pass < kPasses; ++pass) {
+        const int tl = pass * (C::NTHREADS / 32) + (tid >> 5), q = tid & 31;
+        __builtin_nontemporal_store(out[pass], reinterpret_cast<u32x4*>(Gtile + (int64_t)tl * ldG + q * 8));
+      }
+    }
+  }
+}
+
+}  // namespace
+
+// -------------------------------------------------------------- launchers --
+#define CKL_LAUNCH_CHECK() \
+  do { hipError_t e_ = hipGetLastError(); if (e_ != hipSuccess) return e_; } while (0)
+
+HeadTile head_tile(int in_bf16, int64_t rows) {
+  (void)rows;
+  if (!in_bf16) return HeadTile{0, CfgF32::BM, CfgF32::BN, 256};
+  return HeadTile{1, CfgWide::BM, CfgWide::BN, 256};
+}
+
+hipError_t launch_head_tokens(const void* tokens, int tokens64, int T, int Tp, int V, const int* perm, const int* n,
+                              int* tok, hipStream_t st) {
+  head_tokens_kernel<<<(Tp + 255) / 256, 256, 0, st>>>(tokens, tokens64, T, Tp, V, perm, n, tok);
+  CKL_LAUNCH_CHECK();
+  return hipSuccess;
+}
+
+hipError_t launch_head_rows(const HeadTile& k, const void* H, const void* W, int T, int d, int V, const int* tok,
+                            float* ztok, float4* part, int n_splits, int tiles_per_split, const int* nrows, int row0,
+                            hipStream_t st) {
+  const int n_vtiles = (V + k.BM - 1) / k.BM, n_tblocks = (T + k.BN - 1) / k.BN;
+  auto go = [&](auto cfg) {
+    using C = decltype(cfg);
+    using TIn = typename C::TIn;
+    head_rows_kernel<C><<<n_tblocks * n_splits, C::NTHREADS, 0, st>>>((const TIn*)H, (const TIn*)W, T, d, V, tok, ztok,
+                                                                      part, n_vtiles, tiles_per_split, n_tblocks,
+                                                                      n_splits, nrows, row0);
+  };
+  switch (k.kind) {
+    case 0: go(CfgF32{}); break;
+    default: go(CfgWide{}); break;
+  }
+  CKL_LAUNCH_CHECK();
+  return hipSuccess;
+}
+
+hipError_t launch_head_finish(const float4* part, int S, int rows, int row0, const float* ztok, const int* tok,
+                              const int* perm, const int* n, float* logprob, float* entropy, float* lse,
+                              hipStream_t st) {
+  head_finish_kernel<<<(rows + 15) / 16, 256, 0, st>>>(part, S, rows, row0, ztok, tok, perm, n, logprob, entropy, lse);
+  CKL_LAUNCH_CHECK();
+  return hipSuccess;
+}
+
+hipError_t launch_head_masked(const int* rank, int T, float* logprob, float* entropy, float* lse, hipStream_t st) {
+  head_masked_kernel<<<(T + 255) / 256, 256, 0, st>>>(rank, T, logprob, entropy, lse);
+  CKL_LAUNCH_CHECK();
+  return hipSuccess;
+}
+
+hipError_t launch_head_consts(const void* tokens, int tokens64, int T, int Tp, int V, const int* perm, const int* n,
+                              const float* lse, const float* entropy, const float* dlogprob, const float* dentropy,
+                              float4* consts, int* tok, hipStream_t st) {
+  head_consts_kernel<<<(Tp + 255) / 256, 256, 0, st>>>(tokens, tokens64, T, Tp, V, perm, n, lse, entropy, dlogprob,
+                                                       dentropy, consts, tok);
+  CKL_LAUNCH_CHECK();
+  return hipSuccess;
+}
+
+hipError_t launch_head_grad(int in_bf16, const void* H, const void* W, int T, int d, int V, const float4* consts,
+                            const int* tok, int tb0, int t_rows, int vb0, int v_rows, int n_splits,
+                            int tiles_per_split, void* G, int64_t ldG, void* Gt, int64_t ldGt, const int* nrows,
+                            hipStream_t st) {
+  auto go = [&](auto cfg) {
+    using C = decltype(cfg);
+    using TIn = typename C::TIn;
+    const int n_vtiles = v_rows / C::BM, n_tblocks = t_rows / C::BN;
+    head_grad_kernel<C><<<n_tblocks * n_splits, C::NTHREADS, 0, st>>>(
+        (const TIn*)H, (const TIn*)W, T, d, V, consts, tok, tb0, vb0, n_vtiles, tiles_per_split, n_tblocks, n_splits,
+        (TIn*)G, ldG, (TIn*)Gt, ldGt, nrows);
+  };
+  in_bf16 ? go(CfgWide{}) : go(CfgF32{});
+  CKL_LAUNCH_CHECK();
+  return hipSuccess;
+}
+
+}  // namespace ckl

@@ -129,5 +129,30 @@ inline ckl_status check_disjoint(std::initializer_list<Span> written, std::initi
   return CKL_OK;
 }
 
+// ------------------------------------------- checks of the operators --
+constexpr int64_t kMaxHidden = 65536;
+
+inline bool dtype_ok(int32_t t) { return t == CKL_F32 || t == CKL_BF16; }
+inline size_t esize(int32_t t) { return t == CKL_BF16 ? 2 : 4; }
+
+inline ckl_status check_rows(int64_t T) {
+  if (T < 0) return fail(CKL_ERR_INVALID_ARG, "T=%lld must be >= 0", (long long)T);
+  if (T > kMaxRows)
+    return fail(CKL_ERR_UNSUPPORTED, "T=%lld: at most %lld rows", (long long)T, (long long)kMaxRows);
+  return CKL_OK;
+}
+inline ckl_status check_hidden(int64_t d) {
+  if (d < 8 || d % 8 != 0) return fail(CKL_ERR_INVALID_ARG, "d=%lld must be a positive multiple of 8", (long long)d);
+  if (d > kMaxHidden) return fail(CKL_ERR_UNSUPPORTED, "d=%lld exceeds %lld", (long long)d, (long long)kMaxHidden);
+  return CKL_OK;
+}
+inline ckl_status check_vocab(int64_t V) {
+  if (V < 1) return fail(CKL_ERR_INVALID_ARG, "V=%lld must be >= 1", (long long)V);
+  if (V > kMaxRows)
+    return fail(CKL_ERR_UNSUPPORTED, "V=%lld: at most %lld rows", (long long)V, (long long)kMaxRows);
+  return CKL_OK;
+}
+inline size_t exp_cols(int64_t d) { return (size_t)ceil_div(d, CKL_ACT_BLOCK); }
+
 }  // namespace host
 }  // namespace ckl

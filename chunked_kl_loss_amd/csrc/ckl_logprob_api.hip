@@ -1,0 +1,461 @@
+// Host side of the log probabilities of given tokens, from logits and from hidden
+// states and the output head: argument checks, workspaces and launch sequences
+// behind the C ABI declared in include/ckl.h.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "../../include/ckl.h"
+#include "ckl_head.hpp"
+#include "ckl_host.hpp"
+#include "ckl_kernels.hpp"
+#include "ckl_ops.hpp"
+
+using namespace ckl::host;
+
+namespace {
+
+ckl_status check_logprob(int64_t T, int64_t V, int64_t top) {
+  ckl_status s = check_rows(T);
+  if (s == CKL_OK) s = check_vocab(V);
+  if (s != CKL_OK) return s;
+  if (top < 0 || top > V) return fail(CKL_ERR_INVALID_ARG, "top=%lld must satisfy 0 <= top <= V", (long long)top);
+  if (top > kMaxK) return fail(CKL_ERR_UNSUPPORTED, "top=%lld exceeds %lld", (long long)top, (long long)kMaxK);
+  if (T * top >= ((int64_t)1 << 31)) return fail(CKL_ERR_UNSUPPORTED, "T*top must stay below 2^31");
+  if (T * ceil_div(V + 7, 8192) >= ((int64_t)1 << 31)) return fail(CKL_ERR_UNSUPPORTED, "T*V is too large");
+  return CKL_OK;
+}
+ckl_status check_tokens(const void* tokens, int32_t token_bytes) {
+  if (token_bytes != 4 && token_bytes != 8) return fail(CKL_ERR_INVALID_ARG, "token_bytes must be 4 or 8");
+  if ((uintptr_t)tokens & (uintptr_t)(token_bytes - 1))
+    return fail(CKL_ERR_INVALID_ARG, "tokens must be aligned to their size");
+  return CKL_OK;
+}
+bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
+
+// Words and sums of the row segments.
+struct LogprobWs {
+  size_t cand, state, state_e, total;
+};
+LogprobWs logprob_layout(int64_t T, int64_t V, int64_t top) {
+  LogprobWs w{};
+  int segments = 1;
+  int64_t cols = 0;
+  if (T > 0 && top > 0) ckl::topk_plan(T, V, &segments, &cols);
+  if (segments > 1) {
+    const size_t n = (size_t)T * segments;
+    w.state = align256(n * ckl::topk_segment_words(top) * 8);
+    w.state_e = w.state + align256(n * 8);
+    w.total = w.state_e + align256(n * 4);
+  }
+  return w;
+}
+
+// ---------------------------------------------------------- states and head --
+// Row padding (elements) of the matrices whose leading dimension is chosen here:
+// 256 bytes keep the rows of a load on different memory channels.
+constexpr int64_t kLdPad = 128;
+constexpr int64_t kGradSlots = 256;  // workgroups of head_grad at once: one to a compute unit
+
+// Vocabulary splits of a launch over row blocks: the count that finishes in the
+// fewest rounds of tiles, and among equals the fewest splits.
+void pick_splits(int64_t row_blocks, int64_t vtiles, int64_t slots, int64_t* splits, int64_t* tps) {
+  int64_t best = -1;
+  for (int64_t s = 1; s <= vtiles; ++s) {
+    const int64_t t = ceil_div(vtiles, s), sp = ceil_div(vtiles, t);
+    if (sp != s) continue;  // the same as fewer
+    const int64_t cost = ceil_div(row_blocks * sp, slots) * t;
+    if (best < 0 || cost < best) {
+      best = cost;
+      *splits = sp;
+      *tps = t;
+    }
+  }
+}
+
+struct HeadPlan {
+  int bf16;
+  size_t esz;
+  int64_t T, d, V;
+  // forward: chunks of Cs rows
+  ckl::HeadTile tile;
+  int64_t Cs, nS, splits, tps;
+  // backward: G blocks of Tc rows x Vc columns
+  int64_t BM, BN, Tp, Vp, Tc, Vc, nT, nV;
+};
+ckl_status head_plan(int64_t T, int64_t d, int64_t V, int64_t chunk, int32_t in_dtype, int32_t dh_dtype,
+                     int32_t dw_dtype, HeadPlan* q) {
+  if (T < 0) return fail(CKL_ERR_INVALID_ARG, "T=%lld must be >= 0", (long long)T);
+  chunk = std::min(chunk, kMaxRows);
+  ckl_problem p{};
+  p.T = std::max<int64_t>(T, 1);
+  p.d = d;
+  p.V = V;
+  p.K = 1;
+  p.chunk = chunk;
+  p.in_dtype = in_dtype;
+  p.dh_dtype = dh_dtype;
+  p.dw_dtype = dw_dtype;
+  int64_t blocks[5];
+  ckl_status s = ckl_backward_plan(&p, blocks);  // (checks the sizes)
+  if (s != CKL_OK) return s;
+  q->bf16 = in_dtype == CKL_BF16;
+  q->esz = esize(in_dtype);
+  q->T = T;
+  q->d = d;
+  q->V = V;
+  q->BM = ckl::tile_rows_m(q->bf16);
+  q->BN = ckl::tile_rows_n(q->bf16);
+  q->Tp = round_up(p.T, q->BN);
+  q->Vp = round_up(V, q->BM);
+  q->Tc = blocks[0];
+  q->Vc = blocks[1];
+  q->nT = blocks[2];
+  q->nV = blocks[3];
+  q->Cs = std::min(round_up(chunk, 256), round_up(p.T, 256));
+  q->nS = ceil_div(p.T, q->Cs);
+  const int64_t rows = std::min(q->Cs, p.T);
+  q->tile = ckl::head_tile(q->bf16, rows);
+  pick_splits(ceil_div(rows, q->tile.BN), ceil_div(V, q->tile.BM), q->tile.slots, &q->splits, &q->tps);
+  return CKL_OK;
+}
+
+struct Layout {
+  size_t o = 0;
+  size_t take(size_t bytes) {
+    const size_t at = o;
+    o += align256(bytes);
+    return at;
+  }
+};
+// Packed rows of a mask: kept positions, ranks, their number, their states.
+struct PackWs {
+  size_t perm, rank, N, H;
+};
+PackWs pack_layout(const HeadPlan& q, Layout* l) {
+  PackWs w{};
+  w.perm = l->take(q.T * 4);
+  w.rank = l->take(q.T * 4);
+  w.N = l->take(4);
+  w.H = l->take((size_t)q.T * q.d * q.esz);
+  return w;
+}
+struct HeadFwdWs {
+  size_t tok, ztok, part, total;
+  PackWs pk;
+};
+HeadFwdWs head_fwd_layout(const HeadPlan& q, bool masked) {
+  HeadFwdWs w{};
+  Layout l;
+  w.tok = l.take(q.Tp * 4);
+  w.ztok = l.take(q.Tp * 4);
+  w.part = l.take((size_t)q.splits * q.Cs * 16);
+  if (masked) w.pk = pack_layout(q, &l);
+  w.total = l.o;
+  return w;
+}
+struct HeadBwdWs {
+  size_t consts, tok, Ht, Wt, G, Gt, dH, dW, total;
+  PackWs pk;
+};
+HeadBwdWs head_bwd_layout(const HeadPlan& q, bool masked, int32_t dh_dtype, int32_t dw_dtype) {
+  HeadBwdWs w{};
+  Layout l;
+  w.consts = l.take(q.Tp * 16);
+  w.tok = l.take(q.Tp * 4);
+  w.Ht = l.take((size_t)q.d * (q.Tp + kLdPad) * q.esz);
+  w.Wt = l.take((size_t)q.d * (q.Vc + kLdPad) * q.esz);
+  w.G = l.take((size_t)q.Tc * (q.Vc + kLdPad) * q.esz);
+  w.Gt = q.bf16 ? 0 : l.take((size_t)q.Vc * (q.Tc + kLdPad) * q.esz);
+  w.dH = dh_dtype == CKL_BF16 || masked ? l.take((size_t)q.T * q.d * 4) : 0;
+  w.dW = dw_dtype == CKL_BF16 ? l.take((size_t)q.V * q.d * 4) : 0;
+  if (masked) w.pk = pack_layout(q, &l);
+  w.total = l.o;
+  return w;
+}
+
+// The rows that a call works on: all of H, or the packed copy of the kept ones.
+struct Rows {
+  const void* H;
+  const int* perm = nullptr;
+  int* rank = nullptr;
+  const int* n = nullptr;
+};
+hipError_t head_pack(const HeadPlan& q, char* b, const PackWs& w, const uint8_t* mask, const void* H, hipStream_t st,
+                     Rows* r) {
+  int* perm = (int*)(b + w.perm);
+  int* n = (int*)(b + w.N);
+  r->rank = (int*)(b + w.rank);
+  hipError_t e = timed(CKL_KERNEL_OTHER, st,
+                       [&] { return ckl::launch_compact_rows(mask, (int)q.T, perm, r->rank, n, st); });
+  if (e != hipSuccess) return e;
+  r->H = b + w.H;
+  r->perm = perm;
+  r->n = n;
+  return timed(CKL_KERNEL_OTHER, st,
+               [&] { return ckl::launch_gather_rows(H, (int)q.T, q.d * (int64_t)q.esz, perm, n, b + w.H, st); });
+}
+
+}  // namespace
+
+extern "C" {
+
+ckl_status ckl_logprob_workspace_size(int64_t T, int64_t V, int64_t top, size_t* bytes) {
+  ckl_status s = check_logprob(T, V, top);
+  if (s != CKL_OK) return s;
+  if (!bytes) return fail(CKL_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = logprob_layout(T, V, top).total;
+  return CKL_OK;
+}
+
+ckl_status ckl_token_logprobs(const void* logits, int32_t dtype, int64_t T, int64_t V, const void* tokens,
+                              int32_t token_bytes, int64_t top, const uint8_t* mask, float* logprob, float* entropy,
+                              float* lse, int32_t* top_idx, float* top_logprob, void* ws, size_t ws_bytes,
+                              void* stream) {
+  ckl_status s = check_logprob(T, V, top);
+  if (s == CKL_OK) s = check_tokens(tokens, token_bytes);
+  if (s != CKL_OK) return s;
+  if (!dtype_ok(dtype)) return fail(CKL_ERR_INVALID_ARG, "dtype must be CKL_F32 (0) or CKL_BF16 (1)");
+  if (T == 0) return CKL_OK;
+  if (!logits || !tokens || !logprob || !entropy || !lse || (top > 0 && (!top_idx || !top_logprob)))
+    return fail(CKL_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned16(logits) || !aligned16(ws)) return fail(CKL_ERR_INVALID_ARG, "logits and ws must be 16-byte aligned");
+  if (!aligned4(logprob) || !aligned4(entropy) || !aligned4(lse) || !aligned4(top_idx) || !aligned4(top_logprob))
+    return fail(CKL_ERR_INVALID_ARG, "the outputs must be 4-byte aligned");
+  const LogprobWs w = logprob_layout(T, V, top);
+  if (w.total && (!ws || ws_bytes < w.total))
+    return fail(CKL_ERR_WORKSPACE, "the workspace needs %zu bytes, got %zu", w.total, ws ? ws_bytes : (size_t)0);
+  const size_t row = (size_t)T * 4, tops = (size_t)T * top * 4;
+  s = check_disjoint({{logprob, row, "logprob"}, {entropy, row, "entropy"}, {lse, row, "lse"},
+                      {top_idx, tops, "top_idx"}, {top_logprob, tops, "top_logprob"}, {ws, w.total, "ws"}},
+                     {{logits, (size_t)T * V * esize(dtype), "logits"}, {tokens, (size_t)T * token_bytes, "tokens"},
+                      {mask, (size_t)T, "mask"}});
+  if (s != CKL_OK) return s;
+  hipStream_t st = (hipStream_t)stream;
+  char* b = (char*)ws;
+  const ckl::TokenRows t{tokens, token_bytes == 8, mask, logprob, entropy};
+  HIP_TRY(timed(CKL_KERNEL_TOPK, st,
+                [&] {
+                  return ckl::launch_token_logprobs(logits, dtype == CKL_BF16, T, V, (int)top, t, lse, top_idx,
+                                                    top_logprob, (uint64_t*)(b + w.cand), (float2*)(b + w.state),
+                                                    (float*)(b + w.state_e), st);
+                }),
+          "token_logprobs");
+  return CKL_OK;
+}
+
+ckl_status ckl_token_logprobs_backward(const void* logits, int32_t dtype, int64_t T, int64_t V, const void* tokens,
+                                       int32_t token_bytes, const uint8_t* mask, const float* lse,
+                                       const float* entropy, const float* dlogprob, const float* dentropy,
+                                       void* dlogits, void* stream) {
+  ckl_status s = check_logprob(T, V, 0);
+  if (s == CKL_OK) s = check_tokens(tokens, token_bytes);
+  if (s != CKL_OK) return s;
+  if (!dtype_ok(dtype)) return fail(CKL_ERR_INVALID_ARG, "dtype must be CKL_F32 (0) or CKL_BF16 (1)");
+  if (T == 0) return CKL_OK;
+  if (!logits || !tokens || !lse || !entropy || !dlogits)
+    return fail(CKL_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned16(logits) || !aligned16(dlogits))
+    return fail(CKL_ERR_INVALID_ARG, "logits and dlogits must be 16-byte aligned");
+  if (!aligned4(lse) || !aligned4(entropy) || !aligned4(dlogprob) || !aligned4(dentropy))
+    return fail(CKL_ERR_INVALID_ARG, "lse, entropy, dlogprob and dentropy must be 4-byte aligned");
+  const size_t row = (size_t)T * 4, all = (size_t)T * V * esize(dtype);
+  s = check_disjoint({{dlogits, all, "dlogits"}},
+                     {{logits, all, "logits"}, {tokens, (size_t)T * token_bytes, "tokens"}, {mask, (size_t)T, "mask"},
+                      {lse, row, "lse"}, {entropy, row, "entropy"}, {dlogprob, row, "dlogprob"},
+                      {dentropy, row, "dentropy"}});
+  if (s != CKL_OK) return s;
+  hipStream_t st = (hipStream_t)stream;
+  const ckl::TokenRows t{tokens, token_bytes == 8, mask, nullptr, const_cast<float*>(entropy)};
+  HIP_TRY(timed(CKL_KERNEL_TOPK, st,
+                [&] {
+                  return ckl::launch_token_logprobs_backward(logits, dtype == CKL_BF16, T, V, t, lse, dlogprob,
+                                                             dentropy, dlogits, st);
+                }),
+          "token_logprobs_backward");
+  return CKL_OK;
+}
+
+ckl_status ckl_head_workspace_size(int64_t T, int64_t d, int64_t V, int64_t chunk, int32_t in_dtype, int32_t dh_dtype,
+                                   int32_t dw_dtype, int32_t masked, int which, size_t* bytes) {
+  HeadPlan q;
+  ckl_status s = head_plan(T, d, V, chunk, in_dtype, dh_dtype, dw_dtype, &q);
+  if (s != CKL_OK) return s;
+  if (!bytes) return fail(CKL_ERR_INVALID_ARG, "bytes is NULL");
+  if (masked != 0 && masked != 1) return fail(CKL_ERR_INVALID_ARG, "masked must be 0 or 1");
+  if (which != 0 && which != 1) return fail(CKL_ERR_INVALID_ARG, "which must be 0 (forward) or 1 (backward)");
+  *bytes = T == 0 ? 0 : which == 0 ? head_fwd_layout(q, masked).total
+                                   : head_bwd_layout(q, masked, dh_dtype, dw_dtype).total;
+  return CKL_OK;
+}
+
+ckl_status ckl_head_logprobs(const void* H, const void* W, int32_t in_dtype, int64_t T, int64_t d, int64_t V,
+                             const void* tokens, int32_t token_bytes, const uint8_t* mask, int64_t chunk,
+                             float* logprob, float* entropy, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  HeadPlan q;
+  ckl_status s = head_plan(T, d, V, chunk, in_dtype, in_dtype, CKL_F32, &q);
+  if (s == CKL_OK) s = check_tokens(tokens, token_bytes);
+  if (s != CKL_OK) return s;
+  if (T == 0) return CKL_OK;
+  if (!H || !W || !tokens || !logprob || !entropy || !lse)
+    return fail(CKL_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned16(H) || !aligned16(W) || !aligned16(ws))
+    return fail(CKL_ERR_INVALID_ARG, "H, W and ws must be 16-byte aligned");
+  if (!aligned4(logprob) || !aligned4(entropy) || !aligned4(lse))
+    return fail(CKL_ERR_INVALID_ARG, "logprob, entropy and lse must be 4-byte aligned");
+  const HeadFwdWs w = head_fwd_layout(q, mask != nullptr);
+  if (!ws || ws_bytes < w.total)
+    return fail(CKL_ERR_WORKSPACE, "the workspace needs %zu bytes, got %zu", w.total, ws ? ws_bytes : (size_t)0);
+  const size_t row = (size_t)T * 4;
+  s = check_disjoint({{logprob, row, "logprob"}, {entropy, row, "entropy"}, {lse, row, "lse"}, {ws, w.total, "ws"}},
+                     {{H, (size_t)T * d * q.esz, "H"}, {W, (size_t)V * d * q.esz, "W"},
+                      {tokens, (size_t)T * token_bytes, "tokens"}, {mask, (size_t)T, "mask"}});
+  if (s != CKL_OK) return s;
+  hipStream_t st = (hipStream_t)stream;
+  char* b = (char*)ws;
+  int* tok = (int*)(b + w.tok);
+  float* ztok = (float*)(b + w.ztok);
+  float4* part = (float4*)(b + w.part);
+  Rows r{H};
+  if (mask) HIP_TRY(head_pack(q, b, w.pk, mask, H, st, &r), "packing kept rows");
+  HIP_TRY(timed(CKL_KERNEL_OTHER, st,
+                [&] {
+                  return ckl::launch_head_tokens(tokens, token_bytes == 8, (int)T, (int)q.Tp, (int)V, r.perm, r.n, tok,
+                                                 st);
+                }),
+          "head_tokens");
+  for (int64_t c = 0; c < q.nS; ++c) {
+    const int64_t r0 = c * q.Cs;
+    const int rows = (int)std::min(q.Cs, T - r0);
+    HIP_TRY(timed(CKL_KERNEL_FWD_LSE, st,
+                  [&] {
+                    return ckl::launch_head_rows(q.tile, (const char*)r.H + r0 * d * q.esz, W, rows, (int)d, (int)V,
+                                                 tok + r0, ztok + r0, part, (int)q.splits, (int)q.tps, r.n, (int)r0,
+                                                 st);
+                  }),
+            "head_rows");
+    HIP_TRY(timed(CKL_KERNEL_FWD_FINALIZE, st,
+                  [&] {
+                    return ckl::launch_head_finish(part, (int)q.splits, rows, (int)r0, ztok + r0, tok + r0, r.perm, r.n,
+                                                   logprob, entropy, lse, st);
+                  }),
+            "head_finish");
+  }
+  if (mask)
+    HIP_TRY(timed(CKL_KERNEL_OTHER, st,
+                  [&] { return ckl::launch_head_masked(r.rank, (int)T, logprob, entropy, lse, st); }),
+            "head_masked");
+  return CKL_OK;
+}
+
+ckl_status ckl_head_logprobs_backward(const void* H, const void* W, int32_t in_dtype, int64_t T, int64_t d, int64_t V,
+                                      const void* tokens, int32_t token_bytes, const uint8_t* mask, int64_t chunk,
+                                      const float* lse, const float* entropy, const float* dlogprob,
+                                      const float* dentropy, void* dH, int32_t dh_dtype, void* dW, int32_t dw_dtype,
+                                      void* ws, size_t ws_bytes, void* stream) {
+  HeadPlan q;
+  ckl_status s = head_plan(T, d, V, chunk, in_dtype, dh_dtype, dw_dtype, &q);
+  if (s == CKL_OK) s = check_tokens(tokens, token_bytes);
+  if (s != CKL_OK) return s;
+  if (!W || (T > 0 && (!H || !tokens || !lse || !entropy)))
+    return fail(CKL_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!dW && (T > 0 && !dH)) return fail(CKL_ERR_INVALID_ARG, "dH and dW are both NULL");
+  if (!aligned16(H) || !aligned16(W) || !aligned16(dH) || !aligned16(dW) || !aligned16(ws))
+    return fail(CKL_ERR_INVALID_ARG, "H, W, dH, dW and ws must be 16-byte aligned");
+  if (!aligned4(lse) || !aligned4(entropy) || !aligned4(dlogprob) || !aligned4(dentropy))
+    return fail(CKL_ERR_INVALID_ARG, "lse, entropy, dlogprob and dentropy must be 4-byte aligned");
+  const size_t dw_bytes = (size_t)V * d * esize(dw_dtype);
+  hipStream_t st = (hipStream_t)stream;
+  if (T == 0) {
+    if (dW)
+      HIP_TRY(timed(CKL_KERNEL_OTHER, st,
+                    [&] { return ckl::launch_fill_f32((float*)dW, (int64_t)(dw_bytes / 4), 0.f, st); }),
+              "zero dW");
+    return CKL_OK;
+  }
+  const HeadBwdWs w = head_bwd_layout(q, mask != nullptr, dh_dtype, dw_dtype);
+  if (!ws || ws_bytes < w.total)
+    return fail(CKL_ERR_WORKSPACE, "the workspace needs %zu bytes, got %zu", w.total, ws ? ws_bytes : (size_t)0);
+  const size_t row = (size_t)T * 4;
+  s = check_disjoint({{dH, (size_t)T * d * esize(dh_dtype), "dH"}, {dW, dw_bytes, "dW"}, {ws, w.total, "ws"}},
+                     {{H, (size_t)T * d * q.esz, "H"}, {W, (size_t)V * d * q.esz, "W"},
+                      {tokens, (size_t)T * token_bytes, "tokens"}, {mask, (size_t)T, "mask"}, {lse, row, "lse"},
+                      {entropy, row, "entropy"}, {dlogprob, row, "dlogprob"}, {dentropy, row, "dentropy"}});
+  if (s != CKL_OK) return s;
+  char* b = (char*)ws;
+  float4* consts = (float4*)(b + w.consts);
+  int* tok = (int*)(b + w.tok);
+  char* Ht = b + w.Ht;
+  void* Wt = b + w.Wt;
+  void* G = b + w.G;
+  void* Gt = q.bf16 ? nullptr : b + w.Gt;
+  Rows r{H};
+  if (mask) HIP_TRY(head_pack(q, b, w.pk, mask, H, st, &r), "packing kept rows");
+  // fp32 sums in the outputs themselves, or in the workspace where the output is bf16 or its rows are packed
+  float* dHacc = dh_dtype == CKL_BF16 || mask ? (float*)(b + w.dH) : (float*)dH;
+  float* dWacc = dw_dtype == CKL_BF16 ? (float*)(b + w.dW) : (float*)dW;
+  HIP_TRY(timed(CKL_KERNEL_OTHER, st,
+                [&] {
+                  return ckl::launch_head_consts(tokens, token_bytes == 8, (int)T, (int)q.Tp, (int)V, r.perm, r.n, lse,
+                                                 entropy, dlogprob, dentropy, consts, tok, st);
+                }),
+          "head_consts");
+  if (dW)
+    HIP_TRY(timed(CKL_KERNEL_TRANSPOSE, st,
+                  [&] {
+                    return ckl::launch_transpose_pad(q.bf16, r.H, (int)T, (int)d, (int)q.Tp, Ht, q.Tp + kLdPad, st);
+                  }),
+            "transpose H");
+  const int64_t ldWt = q.Vc + kLdPad;
+  for (int64_t vb = 0; vb < q.nV; ++vb) {
+    const int64_t vb0 = vb * q.Vc, vrows = std::min(q.Vc, q.Vp - vb0);
+    if (dH)
+      HIP_TRY(timed(CKL_KERNEL_TRANSPOSE, st,
+                    [&] {
+                      return ckl::launch_transpose_pad(q.bf16, (const char*)W + vb0 * d * q.esz,
+                                                       (int)std::min(q.Vc, V - vb0), (int)d, (int)vrows, Wt, ldWt, st);
+                    }),
+              "transpose W block");
+    for (int64_t tb = 0; tb < q.nT; ++tb) {
+      const int64_t tb0 = tb * q.Tc, trows = std::min(q.Tc, q.Tp - tb0);
+      int64_t splits, tps;
+      pick_splits(trows / q.BN, vrows / q.BM, kGradSlots, &splits, &tps);
+      HIP_TRY(timed(CKL_KERNEL_BWD_GRAD, st,
+                    [&] {
+                      return ckl::launch_head_grad(q.bf16, r.H, W, (int)T, (int)d, (int)V, consts, tok, (int)tb0,
+                                                   (int)trows, (int)vb0, (int)vrows, (int)splits, (int)tps, G,
+                                                   vrows + kLdPad, Gt, trows + kLdPad, r.n, st);
+                    }),
+              "head_grad");
+      // dW[vb0 ..) (+)= G^T H[tb0 ..) (bf16: G read k-major),  dH[tb0 ..) (+)= G W[vb0 ..)
+      ckl::GemmArgs gdw{q.bf16 ? G : Gt, q.bf16 ? vrows + kLdPad : trows + kLdPad, Ht + tb0 * q.esz, q.Tp + kLdPad,
+                        dW ? dWacc + vb0 * d : nullptr, d, dW ? (int)std::min(vrows, V - vb0) : 0, (int)d, (int)trows,
+                        tb > 0};
+      gdw.xt = q.bf16;
+      ckl::GemmArgs gdh{G, vrows + kLdPad, Wt, ldWt, dH ? dHacc + tb0 * d : nullptr, d,
+                        dH ? (int)std::min(trows, T - tb0) : 0, (int)d, (int)vrows, vb > 0};
+      if (r.n) {
+        gdw.lim = gdh.lim = r.n;
+        gdw.lim_base = gdh.lim_base = (int)tb0;
+        gdw.lim_kind = 2;
+        gdw.lim_round = (int)q.BN;
+        gdh.lim_kind = 1;
+      }
+      HIP_TRY(timed(CKL_KERNEL_GEMM_DHDW, st, [&] { return ckl::launch_gemm_pair(q.bf16, gdw, gdh, st); }),
+              "gemm dW + dH");
+    }
+  }
+  if (dH && mask)
+    HIP_TRY(timed(CKL_KERNEL_OTHER, st,
+                  [&] {
+                    return ckl::launch_scatter_rows(dHacc, r.rank, (int)T, (int)d, dH, dh_dtype == CKL_BF16, st);
+                  }),
+            "scatter dH");
+  else if (dH && dh_dtype == CKL_BF16)
+    HIP_TRY(timed(CKL_KERNEL_OTHER, st, [&] { return ckl::launch_cast_f32_bf16(dHacc, dH, T * d, st); }), "cast dH");
+  if (dW && dw_dtype == CKL_BF16)
+    HIP_TRY(timed(CKL_KERNEL_OTHER, st, [&] { return ckl::launch_cast_f32_bf16(dWacc, dW, V * d, st); }), "cast dW");
+  return CKL_OK;
+}
+
+}  // extern "C"

@@ -646,11 +646,11 @@ hipError_t launch_teacher_topk(const void* logits, int bf16, int64_t rows, int64
     using E = std::remove_const_t<std::remove_pointer_t<decltype(p)>>;
     constexpr int CAP = decltype(cap)::value;
     topk_rows_kernel<E, CAP><<<blocks, kTopkThreads, 0, st>>>(p, rows, (int)V, K, segments, (int)seg_cols, logprob,
-                                                              mask, idx, val, lse, cand, state);
+                                                              mask, idx, val, lse, cand, state, RowOut{});
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || segments == 1) return e;
-    topk_merge_kernel<CAP><<<(unsigned)rows, kTopkThreads, 0, st>>>(cand, state, K, segments, logprob, mask, idx, val,
-                                                                   lse);
+    topk_merge_kernel<E, CAP><<<(unsigned)rows, kTopkThreads, 0, st>>>(cand, state, K, segments, logprob, mask, idx,
+                                                                      val, lse, p, (int)V, RowOut{});
     return hipGetLastError();
   };
   // room for what a cut may leave and 2048 more words, and for the final sort
@@ -884,6 +884,15 @@ int64_t norm_backward_groups(int64_t T, int64_t d) {
   return std::min<int64_t>(T, 256 * std::max(1, 1024 / threads));
 }
 
+hipError_t launch_norm_dweight(const float* part, int groups, int d, int weight_bf16, void* dweight, hipStream_t st) {
+  const unsigned blocks = (unsigned)cdiv(d, 64);
+  if (weight_bf16)
+    norm_dweight_kernel<<<blocks, 1024, 0, st>>>(part, groups, d, (bf16_t*)dweight);
+  else
+    norm_dweight_kernel<<<blocks, 1024, 0, st>>>(part, groups, d, (float*)dweight);
+  return hipGetLastError();
+}
+
 hipError_t launch_norm_backward(const void* dy, int bf16, int64_t T, int d, const int8_t* codes, const uint8_t* exps,
                                 const float* rstd, const void* weight, int weight_bf16, void* dx, void* dweight,
                                 float* part, hipStream_t st) {
@@ -907,12 +916,7 @@ hipError_t launch_norm_backward(const void* dy, int bf16, int64_t T, int d, cons
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  const unsigned blocks = (unsigned)cdiv(d, 64);
-  if (weight_bf16)
-    norm_dweight_kernel<<<blocks, 1024, 0, st>>>(part, (int)groups, d, (bf16_t*)dweight);
-  else
-    norm_dweight_kernel<<<blocks, 1024, 0, st>>>(part, (int)groups, d, (float*)dweight);
-  return hipGetLastError();
+  return launch_norm_dweight(part, (int)groups, d, weight_bf16, dweight, st);
 }
 
 }  // namespace ckl

@@ -19,6 +19,24 @@ hipError_t launch_teacher_topk(const void* logits, int bf16, int64_t rows, int64
                                const uint8_t* mask, int* idx, float* val, float* lse, uint64_t* cand, float2* state,
                                hipStream_t st);
 
+// ------------------------------------------------ log probabilities of tokens --
+struct TokenRows {
+  const void* tokens;
+  int tokens64;
+  const uint8_t* mask;
+  float* logprob;
+  float* entropy;  // (the backward pass reads it)
+};
+// top = 0: no alternatives (idx, val, cand, state and state_e unused); else as
+// launch_teacher_topk with K = top, and state_e [rows][segments].
+hipError_t launch_token_logprobs(const void* logits, int bf16, int64_t rows, int64_t V, int top, const TokenRows& t,
+                                 float* lse, int* idx, float* val, uint64_t* cand, float2* state, float* state_e,
+                                 hipStream_t st);
+// dlogprob or dentropy may be NULL (zero).
+hipError_t launch_token_logprobs_backward(const void* logits, int bf16, int64_t rows, int64_t V, const TokenRows& t,
+                                          const float* lse, const float* dlogprob, const float* dentropy,
+                                          void* dlogits, hipStream_t st);
+
 // ---------------------------------------------------------------- embedding --
 hipError_t launch_embedding_forward(const void* W, int bf16, int64_t V, int d, int64_t v_offset, const void* tokens,
                                     int tokens64, int64_t T, float scale, void* out, hipStream_t st);
@@ -46,5 +64,30 @@ int64_t norm_backward_groups(int64_t T, int64_t d);
 hipError_t launch_norm_backward(const void* dy, int bf16, int64_t T, int d, const int8_t* codes, const uint8_t* exps,
                                 const float* rstd, const void* weight, int weight_bf16, void* dx, void* dweight,
                                 float* part, hipStream_t st);
+// dweight = the sum of `groups` fp32 rows of d, in their order by slices.
+hipError_t launch_norm_dweight(const float* part, int groups, int d, int weight_bf16, void* dweight, hipStream_t st);
+
+// -------------------------------------- dropout, norm behind a residual's sum --
+// threshold of 65536: the share dropped (0: none).  state not NULL: {seed, offset}
+// in device memory instead of seed, its offset added to the call's.
+struct DropArgs {
+  uint32_t threshold;
+  float scale;
+  uint64_t seed, offset;
+  const int64_t* state;
+};
+hipError_t launch_dropout(const void* x, int bf16, int64_t n, const DropArgs& a, void* out, hipStream_t st);
+// form 0: y in x's type, with dropout; 1: int8 and block exponents, 2: e4m3 and
+// row scales, without.
+hipError_t launch_add_norm(const void* x, int x_bf16, const void* residual, int r_bf16, int64_t T, int d,
+                           const void* weight, int weight_bf16, float eps, const DropArgs& a, void* h, int form,
+                           void* y, void* scales, float* rstd, hipStream_t st);
+// Workgroups of the backward pass; each leaves one fp32 row of d in `part`.
+int64_t add_norm_backward_groups(int64_t T, int64_t d);
+// dx NULL: it is dres (no dropout, one type).
+hipError_t launch_add_norm_backward(const void* dy, int x_bf16, const void* dh, int r_bf16, int64_t T, int d,
+                                    const void* h, const float* rstd, const void* weight, int weight_bf16,
+                                    const DropArgs& a, void* dx, void* dres, void* dweight, float* part,
+                                    hipStream_t st);
 
 }  // namespace ckl

@@ -13,29 +13,6 @@ using namespace ckl::host;
 
 namespace {
 
-constexpr int64_t kMaxHidden = 65536;
-
-bool dtype_ok(int32_t t) { return t == CKL_F32 || t == CKL_BF16; }
-size_t esize(int32_t t) { return t == CKL_BF16 ? 2 : 4; }
-
-ckl_status check_rows(int64_t T) {
-  if (T < 0) return fail(CKL_ERR_INVALID_ARG, "T=%lld must be >= 0", (long long)T);
-  if (T > kMaxRows)
-    return fail(CKL_ERR_UNSUPPORTED, "T=%lld: at most %lld rows", (long long)T, (long long)kMaxRows);
-  return CKL_OK;
-}
-ckl_status check_hidden(int64_t d) {
-  if (d < 8 || d % 8 != 0) return fail(CKL_ERR_INVALID_ARG, "d=%lld must be a positive multiple of 8", (long long)d);
-  if (d > kMaxHidden) return fail(CKL_ERR_UNSUPPORTED, "d=%lld exceeds %lld", (long long)d, (long long)kMaxHidden);
-  return CKL_OK;
-}
-ckl_status check_vocab(int64_t V) {
-  if (V < 1) return fail(CKL_ERR_INVALID_ARG, "V=%lld must be >= 1", (long long)V);
-  if (V > kMaxRows)
-    return fail(CKL_ERR_UNSUPPORTED, "V=%lld: at most %lld rows", (long long)V, (long long)kMaxRows);
-  return CKL_OK;
-}
-
 ckl_status check_topk(int64_t T, int64_t V, int64_t K) {
   ckl_status s = check_rows(T);
   if (s == CKL_OK) s = check_vocab(V);
@@ -71,8 +48,6 @@ ckl_status check_embedding(int64_t T, int64_t d, int64_t V, int64_t v_offset) {
     return fail(CKL_ERR_INVALID_ARG, "v_offset must be >= 0 and v_offset + V at most 2^63 - 1");
   return CKL_OK;
 }
-
-size_t exp_cols(int64_t d) { return (size_t)ceil_div(d, CKL_ACT_BLOCK); }
 
 }  // namespace
 

@@ -65,7 +65,7 @@ struct TopkShared {
   uint32_t wave_n[4];
   uint32_t range[2][4];
   uint32_t pending[2][4];
-  float wave_m[4], wave_s[4];
+  float wave_m[4], wave_s[4], wave_e[4];
   uint32_t count, sel, need, bin;
   uint32_t start[BINS + 1];
 };
@@ -360,10 +360,10 @@ __device__ __forceinline__ void topk_reduce_state(float& m, float& s, S& sh) {
 // results.  The words are put into bins over the range of their keys, and in its
 // bin a word's place is the number of larger words there.  Where a bin that
 // matters holds more than 256 words (keys that are mostly equal, or a far
-// outlier) a bitonic sort does it.  (2048 rows of 100000 bf16, K = 2048: 352 us
+// outlier) a bitonic sort does it.  Returns the log sum exp.  (2048 rows of 100000 bf16, K = 2048: 352 us
 // a call with this, 580 with the bitonic sort.)
 template <int CAP, typename S>
-__device__ __forceinline__ void topk_finish(uint64_t* buf, int n, int K, float m, float s, int logprob, int* idx,
+__device__ __forceinline__ float topk_finish(uint64_t* buf, int n, int K, float m, float s, int logprob, int* idx,
                                             float* val, float* lse, S& sh) {
   constexpr int W = CAP <= 4096 ? 10 : 24, limit = W * kTopkThreads;  // words that go into the bins
   constexpr int per = S::bins / kTopkThreads;
@@ -425,7 +425,7 @@ __device__ __forceinline__ void topk_finish(uint64_t* buf, int n, int K, float m
     else if constexpr (CAP > 4096)
       topk_sort_bitonic<CAP / kTopkThreads>(buf, n);
     for (int k = tid; k < K; k += kTopkThreads) put(k, buf[k]);
-    return;
+    return l;
   }
 #pragma unroll
   for (int w = 0; w < W; ++w)
@@ -446,6 +446,7 @@ __device__ __forceinline__ void topk_finish(uint64_t* buf, int n, int K, float m
     }
     if (p < K) put(p, word);
   }
+  return l;
 }
 
 __device__ __forceinline__ void topk_masked_row(int K, int* idx, float* val, float* lse) {
@@ -454,6 +455,117 @@ __device__ __forceinline__ void topk_masked_row(int K, int* idx, float* val, flo
     val[k] = 0.f;
   }
   if (threadIdx.x == 0) *lse = 0.f;
+}
+
+// ------------------------------------------- a row's sums for its entropy --
+// (m, s, e): a reference m, s = sum of 2^a and e = sum of a 2^a with a = (x - m)
+// log2 e, of which log sum exp x = m + ln s and the entropy = ln s - ln 2 e / s.
+// A shift of the reference by D (base 2) makes e' = 2^D (e + D s).
+constexpr float kExpZero = -1e4f;  // 2^a is zero from here on, and its product with a too
+__device__ __forceinline__ void ent_merge(float& m, float& s, float& e, float m2, float s2, float e2) {
+  const float mn = fmaxf(m, m2);
+  const float d1 = m == mn ? 0.f : fmaxf((m - mn) * kLog2e, kExpZero);  // (equal infinities have no difference)
+  const float d2 = m2 == mn ? 0.f : fmaxf((m2 - mn) * kLog2e, kExpZero);
+  const float f1 = fast_exp2(d1), f2 = fast_exp2(d2);
+  e = f1 * (e + d1 * s) + f2 * (e2 + d2 * s2);
+  s = f1 * s + f2 * s2;
+  m = mn;
+}
+// What a thread gathers.  The reference moves only when it falls behind by 4 (a
+// few times a row): the terms of e are then at most 6 times those of s, which
+// costs the entropy at most 6 roundings of 2^-24.  Exponentials are taken with
+// neg = -m log2 e rounded, as above.
+struct RowAcc {
+  float m = -INFINITY, neg = 0.f, s = 0.f, e = 0.f;
+  // divides out the rounding of neg
+  __device__ __forceinline__ void settle() {
+    if (fabsf(neg) < kTopkNegLimit && m > -INFINITY) {
+      const float off = fmaf(m, kLog2e, neg), f = fast_exp2(-off);
+      e = f * (e - off * s);
+      s *= f;
+    }
+  }
+  // eight elements of maximum vm; returns the sum of their exponentials
+  template <typename R>
+  __device__ __forceinline__ float add(const R& raw, float vm) {
+    if (vm > m + 4.f) {
+      if (m > -INFINITY) {
+        settle();
+        const float d = fmaxf((m - vm) * kLog2e, kExpZero), f = fast_exp2(d);
+        e = f * (e + d * s);
+        s *= f;
+      }
+      m = vm;
+      neg = -vm * kLog2e;
+    }
+    float sum = 0.f, es = 0.f;
+    if (fabsf(neg) < kTopkNegLimit) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float a = fmaf(raw.get(i), kLog2e, neg), u = fast_exp2(a);
+        sum += u;
+        es = fmaf(u, fmaxf(a, kExpZero), es);
+      }
+    } else {  // masks of a large or the lowest value, infinities
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float x = raw.get(i), a = x == m ? 0.f : (x - m) * kLog2e, u = fast_exp2(a);
+        sum += u;
+        es = fmaf(u, fmaxf(a, kExpZero), es);
+      }
+    }
+    s += sum;
+    e += es;
+    return sum;
+  }
+};
+// The sums of the whole workgroup, in every thread.
+__device__ __forceinline__ void ent_reduce(float& m, float& s, float& e, float* wm, float* ws, float* we) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    const float m2 = __shfl_xor(m, o), s2 = __shfl_xor(s, o), e2 = __shfl_xor(e, o);
+    ent_merge(m, s, e, m2, s2, e2);
+  }
+  const int wave = threadIdx.x >> 6;
+  if ((threadIdx.x & 63) == 0) {
+    wm[wave] = m;
+    ws[wave] = s;
+    we[wave] = e;
+  }
+  __syncthreads();
+  m = wm[0];
+  s = ws[0];
+  e = we[0];
+  for (int w = 1; w < (int)(blockDim.x >> 6); ++w) ent_merge(m, s, e, wm[w], ws[w], we[w]);
+}
+// What a row of logits leaves besides its alternatives, by one thread: the log
+// probability of its token (0 where the token is no column) and its entropy.  l:
+// the row's log sum exp.
+struct RowOut {
+  const void* tokens;
+  int tokens64;
+  float* logprob;
+  float* entropy;
+  float* state_e;  // of row segments
+};
+__device__ __forceinline__ int64_t token_at(const void* tokens, int tokens64, int64_t i) {
+  return tokens64 ? reinterpret_cast<const int64_t*>(tokens)[i] : (int64_t)reinterpret_cast<const int32_t*>(tokens)[i];
+}
+template <typename T>
+__device__ __forceinline__ void row_outputs(const RowOut& o, const T* logits, int64_t row, int V, float l, float s,
+                                            float e) {
+  const int64_t tok = token_at(o.tokens, o.tokens64, row);
+  float lp = 0.f;
+  if (tok >= 0 && tok < V) {
+    const float z = (float)logits[row * (int64_t)V + tok];
+    lp = z == -INFINITY && l == l ? z : z - l;  // (a logit of -inf has log probability -inf in every row)
+  }
+  float ent = logf(s) - kLn2 * (e / s);
+  ent = ent < 0.f ? 0.f : ent;
+  if (l == -INFINITY) ent = 0.f;             // no column is left
+  if (!(l < INFINITY)) ent = __uint_as_float(0x7fc00000u);
+  o.logprob[row] = lp;
+  o.entropy[row] = ent;
 }
 
 // Eight columns as they are in memory.
@@ -500,11 +612,12 @@ struct Raw8<float> {
 // What a segment of a row leaves for the merge: up to `slots` words.
 __host__ __device__ inline int topk_slots(int K) { return K + K / 8 + 32; }
 
-template <typename T, int CAP>
+// ENT: the rows' entropies and the log probabilities of given tokens besides.
+template <typename T, int CAP, bool ENT = false>
 __global__ __launch_bounds__(kTopkThreads, CAP <= 4096 ? 4 : 2) void topk_rows_kernel(
     const T* __restrict__ logits, int64_t rows, int V, int K, int segments, int seg_cols, int logprob,
     const uint8_t* __restrict__ mask, int* __restrict__ idx, float* __restrict__ val, float* __restrict__ lse,
-    uint64_t* __restrict__ cand, float2* __restrict__ state) {
+    uint64_t* __restrict__ cand, float2* __restrict__ state, RowOut out) {
   __shared__ __attribute__((aligned(16))) uint64_t buf[CAP];
   __shared__ TopkShared<CAP <= 4096 ? 256 : 1024> sh;
   __shared__ uint32_t lists[kTopkThreads / 64][kTopkList];
@@ -512,7 +625,10 @@ __global__ __launch_bounds__(kTopkThreads, CAP <= 4096 ? 4 : 2) void topk_rows_k
   const int64_t row = blockIdx.x / segments;
   const int seg = (int)(blockIdx.x - row * segments);
   if (mask != nullptr && mask[row] == 0) {
-    if (segments == 1) topk_masked_row(K, idx + row * K, val + row * K, lse + row);
+    if (segments == 1) {
+      topk_masked_row(K, idx + row * K, val + row * K, lse + row);
+      if (ENT && tid == 0) out.logprob[row] = out.entropy[row] = 0.f;
+    }
     return;
   }
   // Columns shifted so that shifted column 0 lies on a 16-byte boundary (rows
@@ -574,6 +690,7 @@ __global__ __launch_bounds__(kTopkThreads, CAP <= 4096 ? 4 : 2) void topk_rows_k
   Raw8<T> raw[kTopkVecs], next[kTopkVecs];
   // sum of 2^(x log2 e + neg), neg = -m log2 e rounded, for a reference m
   float m = -INFINITY, neg = 0.f, s = 0.f;
+  RowAcc acc;  // (ENT: instead of them)
   int n = 0, listed = 0, side = 0;
   uint32_t after = 0;  // what is wanted at least once all lists are read
   for (int t0 = lo - kTopkTile; t0 < hi; t0 += kTopkTile) {
@@ -588,23 +705,27 @@ __global__ __launch_bounds__(kTopkThreads, CAP <= 4096 ? 4 : 2) void topk_rows_k
         float vm = raw[u].get(0), sum = 0.f;
 #pragma unroll
         for (int i = 1; i < 8; ++i) vm = fmaxf(vm, raw[u].get(i));
-        // The reference moves only when it falls behind by 40: terms up to e^40
-        // are as precise and cannot overflow.
-        if (vm > m + 40.f) {
-          const float to = -vm * kLog2e;
-          s *= fast_exp2((m - vm) * kLog2e);
-          if (fabsf(neg) < kTopkNegLimit && m > -INFINITY) s *= fast_exp2(-fmaf(m, kLog2e, neg));  // the old neg's rounding
-          m = vm;
-          neg = to;
-        }
-        if (fabsf(neg) < kTopkNegLimit) {
+        if constexpr (ENT) {
+          sum = acc.add(raw[u], vm);
+        } else {
+          // The reference moves only when it falls behind by 40: terms up to e^40
+          // are as precise and cannot overflow.
+          if (vm > m + 40.f) {
+            const float to = -vm * kLog2e;
+            s *= fast_exp2((m - vm) * kLog2e);
+            if (fabsf(neg) < kTopkNegLimit && m > -INFINITY) s *= fast_exp2(-fmaf(m, kLog2e, neg));  // the old neg's rounding
+            m = vm;
+            neg = to;
+          }
+          if (fabsf(neg) < kTopkNegLimit) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) sum += fast_exp2(fmaf(raw[u].get(i), kLog2e, neg));
-        } else {  // masks of a large or the lowest value, infinities
+            for (int i = 0; i < 8; ++i) sum += fast_exp2(fmaf(raw[u].get(i), kLog2e, neg));
+          } else {  // masks of a large or the lowest value, infinities
 #pragma unroll
-          for (int i = 0; i < 8; ++i) sum += fast_exp2((raw[u].get(i) - m) * kLog2e);
+            for (int i = 0; i < 8; ++i) sum += fast_exp2((raw[u].get(i) - m) * kLog2e);
+          }
+          s += sum;
         }
-        s += sum;
         // (NaN: fmaxf passes it over, the sum does not)
         const bool hot = !(vm < need_value) || sum != sum;
         const uint64_t who = __ballot(hot);
@@ -712,10 +833,20 @@ __global__ __launch_bounds__(kTopkThreads, CAP <= 4096 ? 4 : 2) void topk_rows_k
       __syncthreads();
     }
   }
-  if (fabsf(neg) < kTopkNegLimit && m > -INFINITY) s *= fast_exp2(-fmaf(m, kLog2e, neg));  // the rounding of neg
-  topk_reduce_state(m, s, sh);
+  float e = 0.f;
+  if constexpr (ENT) {
+    acc.settle();
+    m = acc.m;
+    s = acc.s;
+    e = acc.e;
+    ent_reduce(m, s, e, sh.wave_m, sh.wave_s, sh.wave_e);
+  } else {
+    if (fabsf(neg) < kTopkNegLimit && m > -INFINITY) s *= fast_exp2(-fmaf(m, kLog2e, neg));  // the rounding of neg
+    topk_reduce_state(m, s, sh);
+  }
   if (segments == 1) {
-    topk_finish<CAP>(buf, n, K, m, s, logprob, idx + row * K, val + row * K, lse + row, sh);
+    const float l = topk_finish<CAP>(buf, n, K, m, s, logprob, idx + row * K, val + row * K, lse + row, sh);
+    if (ENT && tid == 0) row_outputs(out, logits, row, V, l, s, e);
   } else {
     const int slots = topk_slots(K);
     if (n > slots) {
@@ -726,20 +857,23 @@ __global__ __launch_bounds__(kTopkThreads, CAP <= 4096 ? 4 : 2) void topk_rows_k
     uint64_t* c = cand + (int64_t)blockIdx.x * slots;
     for (int k = tid; k < slots; k += kTopkThreads) c[k] = k < n ? buf[k] : 0;
     if (tid == 0) state[blockIdx.x] = make_float2(m, s);
+    if (ENT && tid == 0) out.state_e[blockIdx.x] = e;
   }
 }
 
 // The segments' words of a row, cut and sorted in the same way.
-template <int CAP>
+template <typename T, int CAP, bool ENT = false>
 __global__ __launch_bounds__(kTopkThreads, CAP <= 4096 ? 4 : 2) void topk_merge_kernel(
     const uint64_t* __restrict__ cand, const float2* __restrict__ state, int K, int segments, int logprob,
-    const uint8_t* __restrict__ mask, int* __restrict__ idx, float* __restrict__ val, float* __restrict__ lse) {
+    const uint8_t* __restrict__ mask, int* __restrict__ idx, float* __restrict__ val, float* __restrict__ lse,
+    const T* __restrict__ logits, int V, RowOut out) {
   __shared__ __attribute__((aligned(16))) uint64_t buf[CAP];
   __shared__ TopkShared<CAP <= 4096 ? 256 : 1024> sh;
   const int tid = threadIdx.x;
   const int64_t row = blockIdx.x;
   if (mask != nullptr && mask[row] == 0) {
     topk_masked_row(K, idx + row * K, val + row * K, lse + row);
+    if (ENT && tid == 0) out.logprob[row] = out.entropy[row] = 0.f;
     return;
   }
   const int total = segments * topk_slots(K);
@@ -770,13 +904,20 @@ __global__ __launch_bounds__(kTopkThreads, CAP <= 4096 ? 4 : 2) void topk_merge_
     n = (int)sh.count;
     __syncthreads();
   }
-  float m = -INFINITY, s = 0.f;
+  float m = -INFINITY, s = 0.f, e = 0.f;
   for (int i = tid; i < segments; i += kTopkThreads) {
     const float2 st = state[row * segments + i];
-    exp_merge(m, s, st.x, st.y);
+    if constexpr (ENT)
+      ent_merge(m, s, e, st.x, st.y, out.state_e[row * segments + i]);
+    else
+      exp_merge(m, s, st.x, st.y);
   }
-  topk_reduce_state(m, s, sh);
-  topk_finish<CAP>(buf, n, K, m, s, logprob, idx + row * K, val + row * K, lse + row, sh);
+  if constexpr (ENT)
+    ent_reduce(m, s, e, sh.wave_m, sh.wave_s, sh.wave_e);
+  else
+    topk_reduce_state(m, s, sh);
+  const float l = topk_finish<CAP>(buf, n, K, m, s, logprob, idx + row * K, val + row * K, lse + row, sh);
+  if (ENT && tid == 0) row_outputs(out, logits, row, V, l, s, e);
 }
 
 }  // namespace

@@ -1,5 +1,7 @@
-"""Operators around the loss: the top-K teacher cache, the embedding table and
-its gradient, activations in 8 bits and the RMS norm that saves its input so.
+"""Operators around the loss: the top-K teacher cache, log probabilities of given
+tokens (from logits, and from states and head), the embedding table and its
+gradient, activations in 8 bits and the RMS norm that saves its input so,
+dropout, and the RMS norm with the residual's addition.
 
 Argument marshalling over include/ckl.h, as in _binding.  Leading dimensions
 are rows; tensors are contiguous and on one GPU.  The library takes arrays from
@@ -14,7 +16,8 @@ import functools
 import torch
 
 from . import _binding
-from ._binding import CKL_BF16, CKL_F32, CKL_TEACHER_LOGITS, check, load_library
+from ._binding import (CKL_BF16, CKL_F32, CKL_QUANT_E4M3, CKL_QUANT_INT8, CKL_TEACHER_LOGITS, check,
+                       load_library)
 
 ACT_BLOCK = 32  # columns that share an exponent (CKL_ACT_BLOCK)
 
@@ -55,7 +58,7 @@ def _aligned(t):
 def _new(shape, dtype, device):
     t = torch.empty(shape, dtype=dtype, device=device)
     if _binding.FILL_BYTE is not None and t.numel() > 0:
-        t.view(torch.uint8).fill_(int(_binding.FILL_BYTE))
+        t.view(-1).view(torch.uint8).fill_(int(_binding.FILL_BYTE))
     return t
 
 
@@ -121,6 +124,124 @@ def teacher_topk(logits, K: int, mask=None, teacher_form: int = CKL_TEACHER_LOGI
     _call(dev, load_library().ckl_teacher_topk, logits.data_ptr(), code, T, V, K, teacher_form, mask_ptr,
           idx.data_ptr(), values.data_ptr(), lse.data_ptr(), ws_ptr, ws_bytes)
     return idx, values, lse
+
+
+# ----------------------------------------------- log probabilities of tokens --
+def _check_rows_args(tokens, mask, lead, what):
+    """Checks of per-row arguments; the mask's address."""
+    if tokens.shape != lead:
+        raise ValueError(f"tokens must have the leading shape of {what}")
+    if mask is None:
+        return None
+    if mask.shape != lead or mask.dtype not in (torch.uint8, torch.bool):
+        raise ValueError(f"mask must be a uint8/bool tensor of the leading shape of {what}")
+    return mask.data_ptr()
+
+
+def _check_row_floats(lead, **rows):
+    for name, t in rows.items():
+        if t is not None and (t.shape != lead or t.dtype != torch.float32):
+            raise ValueError(f"{name} must be a float32 tensor of the rows' shape")
+
+
+def _given(**tensors):
+    """Names and tensors of those that are not None, for _check."""
+    there = {name: t for name, t in tensors.items() if t is not None}
+    return tuple(there), *there.values()
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def token_logprobs_forward(logits, tokens, top: int = 0, mask=None):
+    """From logits [..., V] (bf16 or fp32): (logprob, entropy, lse: float32 [...], top_idx int32 and top_logprob
+    float32 [..., top]).  logprob is that of tokens [...] (int32 / int64; 0 for a token outside [0, V)), entropy
+    that of the row's softmax, top_idx the most likely columns in descending order (equal ones by index).  Rows
+    whose mask (uint8 / bool [...]) is 0 are not read and get 0 (top_idx 0 .. top-1)."""
+    if logits.dim() < 1:
+        raise ValueError("logits must be [..., V]")
+    top = int(top)
+    lead, V = logits.shape[:-1], logits.shape[-1]
+    dev = _check(*_given(logits=logits, tokens=tokens, mask=mask))
+    mask_ptr = _check_rows_args(tokens, mask, lead, "logits")
+    T, code, nb = tokens.numel(), _code(logits.dtype), _token_bytes(tokens)
+    logits = _aligned(logits)
+    ws, ws_ptr, ws_bytes = _workspace(dev, "ckl_logprob_workspace_size", T, V, top)
+    logprob, entropy, lse = (_new(lead, torch.float32, dev) for _ in range(3))
+    top_idx = _new((*lead, top), torch.int32, dev)
+    top_logprob = _new((*lead, top), torch.float32, dev)
+    _call(dev, load_library().ckl_token_logprobs, logits.data_ptr(), code, T, V, tokens.data_ptr(), nb, top, mask_ptr,
+          logprob.data_ptr(), entropy.data_ptr(), lse.data_ptr(), top_idx.data_ptr(), top_logprob.data_ptr(), ws_ptr,
+          ws_bytes)
+    return logprob, entropy, lse, top_idx, top_logprob
+
+
+def token_logprobs_backward(dlogprob, dentropy, logits, tokens, lse, entropy, mask=None):
+    """Gradient of the logits, in their type, from those of logprob and entropy (float32 [...]; either may be None)
+    and what token_logprobs_forward returned.  Rows that are masked or have no gradient get zeros."""
+    lead, V = logits.shape[:-1], logits.shape[-1]
+    dev = _check(*_given(logits=logits, tokens=tokens, lse=lse, entropy=entropy, mask=mask, dlogprob=dlogprob,
+                         dentropy=dentropy))
+    mask_ptr = _check_rows_args(tokens, mask, lead, "logits")
+    _check_row_floats(lead, lse=lse, entropy=entropy, dlogprob=dlogprob, dentropy=dentropy)
+    T, code, nb = tokens.numel(), _code(logits.dtype), _token_bytes(tokens)
+    logits = _aligned(logits)
+    dlogits = _new(logits.shape, logits.dtype, dev)
+    _call(dev, load_library().ckl_token_logprobs_backward, logits.data_ptr(), code, T, V, tokens.data_ptr(), nb,
+          mask_ptr, lse.data_ptr(), entropy.data_ptr(), _ptr(dlogprob), _ptr(dentropy), dlogits.data_ptr())
+    return dlogits
+
+
+def _check_head(H, W):
+    if H.dim() < 1 or W.dim() != 2 or H.shape[-1] != W.shape[1] or H.dtype != W.dtype:
+        raise ValueError("H [..., d] and W [V, d] must share d and dtype")
+
+
+def head_logprobs_forward(H, W, tokens, mask=None, chunk: int = 2048):
+    """(logprob, entropy, lse: float32 [...]) of the logits H W^T, which are never stored: H [..., d] and W [V, d]
+    (bf16 or fp32), tokens and mask [...] as for token_logprobs_forward.  Masked rows are not computed."""
+    _check_head(H, W)
+    lead = H.shape[:-1]
+    dev = _check(*_given(H=H, W=W, tokens=tokens, mask=mask))
+    mask_ptr = _check_rows_args(tokens, mask, lead, "H")
+    T, code, nb = tokens.numel(), _code(H.dtype), _token_bytes(tokens)
+    V, d = W.shape
+    H, W = _aligned(H), _aligned(W)
+    ws, ws_ptr, ws_bytes = _workspace(dev, "ckl_head_workspace_size", T, d, V, chunk, code, code, CKL_F32,
+                                      int(mask is not None), 0)
+    logprob, entropy, lse = (_new(lead, torch.float32, dev) for _ in range(3))
+    _call(dev, load_library().ckl_head_logprobs, H.data_ptr(), W.data_ptr(), code, T, d, V, tokens.data_ptr(), nb,
+          mask_ptr, chunk, logprob.data_ptr(), entropy.data_ptr(), lse.data_ptr(), ws_ptr, ws_bytes)
+    return logprob, entropy, lse
+
+
+def head_logprobs_backward(dlogprob, dentropy, H, W, tokens, lse, entropy, mask=None, chunk: int = 2048, dh_dtype=None,
+                           dw_dtype=None, need_dh: bool = True, need_dw: bool = True):
+    """Gradients (dH in dh_dtype, default H's; dW in dw_dtype, default float32) from those of logprob and entropy
+    (float32 [...]; either may be None) and what head_logprobs_forward returned.  The logits are multiplied again.
+    need_dh / need_dw False: that gradient is not computed and None."""
+    _check_head(H, W)
+    if not (need_dh or need_dw):
+        return None, None
+    lead = H.shape[:-1]
+    dev = _check(*_given(H=H, W=W, tokens=tokens, lse=lse, entropy=entropy, mask=mask, dlogprob=dlogprob,
+                         dentropy=dentropy))
+    mask_ptr = _check_rows_args(tokens, mask, lead, "H")
+    _check_row_floats(lead, lse=lse, entropy=entropy, dlogprob=dlogprob, dentropy=dentropy)
+    T, code, nb = tokens.numel(), _code(H.dtype), _token_bytes(tokens)
+    V, d = W.shape
+    dh_dtype = H.dtype if dh_dtype is None else dh_dtype
+    dw_dtype = torch.float32 if dw_dtype is None else dw_dtype
+    H, W = _aligned(H), _aligned(W)
+    ws, ws_ptr, ws_bytes = _workspace(dev, "ckl_head_workspace_size", T, d, V, chunk, code, _code(dh_dtype),
+                                      _code(dw_dtype), int(mask is not None), 1)
+    dH = _new(H.shape, dh_dtype, dev) if need_dh else None
+    dW = _new(W.shape, dw_dtype, dev) if need_dw else None
+    _call(dev, load_library().ckl_head_logprobs_backward, H.data_ptr(), W.data_ptr(), code, T, d, V,
+          tokens.data_ptr(), nb, mask_ptr, chunk, lse.data_ptr(), entropy.data_ptr(), _ptr(dlogprob), _ptr(dentropy),
+          _ptr(dH), _code(dh_dtype), _ptr(dW), _code(dw_dtype), ws_ptr, ws_bytes)
+    return dH, dW
 
 
 # --------------------------------------------------------------- embedding --
@@ -310,3 +431,101 @@ def norm_backward_saved(dy, saved, weight):
     _call(dev, load_library().ckl_norm_backward, dy.data_ptr(), _CODES[dy.dtype], T, d, at + codes, at + exps, at,
           weight.data_ptr(), _CODES[weight.dtype], dx.data_ptr(), dweight.data_ptr(), ws_ptr, ws_bytes)
     return dx, dweight
+
+
+# ---------------------------------------- dropout, norm behind a residual's sum --
+def _drop_args(p, seed, offset, device):
+    """p, seed, offset and the state's address for the library."""
+    p = float(p)
+    if not 0.0 <= p <= 1.0:
+        raise ValueError("p must be from 0 to 1")
+    offset = int(offset)
+    if not 0 <= offset < 2 ** 64:
+        raise ValueError("offset must be from 0 to 2^64 - 1")
+    if isinstance(seed, torch.Tensor):
+        if seed.shape != (2,) or seed.dtype != torch.int64 or not seed.is_contiguous() or seed.device != device:
+            raise ValueError("seed must be an integer or an int64 tensor [2], (seed, offset), on the inputs' GPU")
+        return p, 0, offset, seed.data_ptr()
+    seed = int(seed)
+    if not 0 <= seed < 2 ** 64:
+        raise ValueError("seed must be from 0 to 2^64 - 1")
+    return p, seed, offset, None
+
+
+def dropout_forward(x, p: float, seed=0, offset: int = 0):
+    """x * 1 / (1 - p) where kept, 0 elsewhere, with a mask that is a function of (seed, offset, element): p is taken
+    to the nearest multiple of 2^-16.  The gradient is the same call on the incoming one.  seed: an integer, or an
+    int64 tensor (seed, offset) on the GPU that is read when the kernel runs, its offset added to this one: a
+    captured call then draws anew when the tensor changes."""
+    dev, code = _check(("x",), x), _code(x.dtype)
+    args = _drop_args(p, seed, offset, dev)
+    x = _aligned(x)
+    out = _new(x.shape, x.dtype, dev)
+    _call(dev, load_library().ckl_dropout, x.data_ptr(), code, x.numel(), *args, out.data_ptr())
+    return out
+
+
+def _check_branch(x, residual, weight):
+    if x.dim() < 1 or residual.shape != x.shape:
+        raise ValueError("x and residual must be [..., d] of one shape")
+    dev = _check(("x", "residual", "weight"), x, residual, weight)
+    return dev, _code(x.dtype), _code(residual.dtype), _weight_code(weight, x.shape[-1])
+
+
+def add_norm_forward(x, residual, weight, eps: float = 1e-6, p: float = 0.0, seed=0, offset: int = 0,
+                     save: bool = True):
+    """(y, h, rstd): h = residual + dropout(x) in the residual's type (x's, or float32 with x in bf16), y = h * rstd *
+    weight in x's, rstd float32 [...] of h for add_norm_backward (None with save=False).  p, seed, offset as for
+    dropout_forward."""
+    dev, code, r_code, w_code = _check_branch(x, residual, weight)
+    args = _drop_args(p, seed, offset, dev)
+    x, residual, weight = _aligned(x), _aligned(residual), _aligned(weight)
+    y, h = _new(x.shape, x.dtype, dev), _new(x.shape, residual.dtype, dev)
+    rstd = _new(x.shape[:-1], torch.float32, dev) if save else None
+    _call(dev, load_library().ckl_add_norm_forward, x.data_ptr(), code, residual.data_ptr(), r_code, _rows(x),
+          x.shape[-1], weight.data_ptr(), w_code, eps, *args, h.data_ptr(), y.data_ptr(), _ptr(rstd))
+    return y, h, rstd
+
+
+def add_norm_backward(dy, dh, h, rstd, weight, p: float = 0.0, seed=0, offset: int = 0):
+    """Gradients (dx in dy's type, dresidual in h's, dweight in weight's) from those of y and h (dh may be None), h and
+    rstd.  Without dropout and with one type, dx is dresidual itself."""
+    if dy.shape != h.shape or (dh is not None and (dh.shape != h.shape or dh.dtype != h.dtype)):
+        raise ValueError("dy and dh must have h's shape, and dh its type")
+    dev = _check(*_given(dy=dy, h=h, rstd=rstd, weight=weight, dh=dh))
+    _check_rstd(rstd, h.shape[:-1])
+    d, T, code, r_code = h.shape[-1], _rows(h), _code(dy.dtype), _code(h.dtype)
+    w_code = _weight_code(weight, d)
+    args = _drop_args(p, seed, offset, dev)
+    dy, h, weight = _aligned(dy), _aligned(h), _aligned(weight)
+    dh = None if dh is None else _aligned(dh)
+    ws, ws_ptr, ws_bytes = _workspace(dev, "ckl_add_norm_workspace_size", T, d)
+    dresidual = _new(h.shape, h.dtype, dev)
+    dx = _new(h.shape, dy.dtype, dev) if args[0] > 0.0 or code != r_code else None
+    dweight = _new(weight.shape, weight.dtype, dev)
+    _call(dev, load_library().ckl_add_norm_backward, dy.data_ptr(), code, _ptr(dh), r_code, T, d, h.data_ptr(),
+          rstd.data_ptr(), weight.data_ptr(), w_code, *args, _ptr(dx), dresidual.data_ptr(), dweight.data_ptr(),
+          ws_ptr, ws_bytes)
+    return (dresidual if dx is None else dx), dresidual, dweight
+
+
+_FORMS = {"int8": CKL_QUANT_INT8, "e4m3": CKL_QUANT_E4M3}
+
+
+def add_norm_quant(x, residual, weight, eps: float = 1e-6, form: str = "int8"):
+    """The norm behind a residual's addition with its output in 8 bits (no gradient): (codes, scales, h).  form "int8":
+    codes int8 [..., d] and scales uint8 [..., ceil(d / 32)] as act_encode writes them, for act_decode; "e4m3":
+    codes float8_e4m3fn [..., d] that stand for code * scale, scales float32 [...]."""
+    if form not in _FORMS:
+        raise ValueError("form must be 'int8' or 'e4m3'")
+    dev, code, r_code, w_code = _check_branch(x, residual, weight)
+    x, residual, weight = _aligned(x), _aligned(residual), _aligned(weight)
+    d, lead = x.shape[-1], x.shape[:-1]
+    h = _new(x.shape, residual.dtype, dev)
+    if form == "int8":
+        codes, scales = _new(x.shape, torch.int8, dev), _new((*lead, -(-d // ACT_BLOCK)), torch.uint8, dev)
+    else:
+        codes, scales = _new(x.shape, torch.float8_e4m3fn, dev), _new(lead, torch.float32, dev)
+    _call(dev, load_library().ckl_add_norm_quant, x.data_ptr(), code, residual.data_ptr(), r_code, _rows(x), d,
+          weight.data_ptr(), w_code, eps, _FORMS[form], h.data_ptr(), codes.data_ptr(), scales.data_ptr())
+    return codes, scales, h

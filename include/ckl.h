@@ -381,6 +381,122 @@ ckl_status ckl_norm_backward(const void* dy, int32_t dtype, int64_t T, int64_t d
                              const uint8_t* exps, const float* rstd, const void* weight, int32_t weight_dtype,
                              void* dx, void* dweight, void* ws, size_t ws_bytes, void* stream);
 
+/* ---- Between a model's last block and its training signal -----------------
+ * Rules as for the operators above (T may be 0; d a multiple of 8 up to 65536; T
+ * and V at most 4,000,000). */
+
+/* Log probabilities of given tokens, the rows' entropies and the `top` most likely
+ * alternatives, from logits in one pass.
+ *   logits: [T, V] dtype.  tokens: [T] int32 or int64 (token_bytes 4 or 8),
+ *   aligned to their size.  mask: [T] uint8 (nonzero = keep) or NULL.
+ *   logprob: [T] float32, logit of the token - lse; 0 where the token is outside
+ *   [0, V) (padding).
+ *   entropy: [T] float32, lse - sum_v q_v z_v = -sum_v q_v log q_v, q = softmax(z).
+ *   lse:     [T] float32, as ckl_teacher_topk's.
+ *   top_idx [T, top] int32, top_logprob [T, top] float32: as ckl_teacher_topk with
+ *   K = top and CKL_TEACHER_LOGPROBS.  top may be 0 (both may then be NULL).
+ * A logit of -inf (a forbidden token) has log probability -inf and adds nothing to
+ * the entropy; a row of nothing but -inf has lse -inf and entropy 0.  A row that
+ * holds a NaN gives NaN; one that holds +inf has lse +inf and entropy NaN.  Rows
+ * with mask 0 are not read and give 0 (top_idx 0 .. top-1).
+ * 0 <= top <= min(V, 4096), T*top < 2^31.  ws: ckl_logprob_workspace_size bytes
+ * (0 for many rows or top = 0). */
+ckl_status ckl_logprob_workspace_size(int64_t T, int64_t V, int64_t top, size_t* bytes);
+ckl_status ckl_token_logprobs(const void* logits, int32_t dtype, int64_t T, int64_t V, const void* tokens,
+                              int32_t token_bytes, int64_t top, const uint8_t* mask, float* logprob, float* entropy,
+                              float* lse, int32_t* top_idx, float* top_logprob, void* ws, size_t ws_bytes,
+                              void* stream);
+
+/* Gradient of the first two: with a = dlogprob[t] (0 for a token outside) and b =
+ * dentropy[t] (NULL: zero),
+ *   dlogits[t, v] = a (1[v = token] - q_v) - b q_v (log q_v + entropy[t]),
+ * in fp32, rounded once to dtype.  lse and entropy: from ckl_token_logprobs.  Rows
+ * with mask 0, with a = b = 0 or with lse -inf get zeros and are not read. */
+ckl_status ckl_token_logprobs_backward(const void* logits, int32_t dtype, int64_t T, int64_t V, const void* tokens,
+                                       int32_t token_bytes, const uint8_t* mask, const float* lse,
+                                       const float* entropy, const float* dlogprob, const float* dentropy,
+                                       void* dlogits, void* stream);
+
+/* The same log probabilities and entropies of z = H W^T, whose T x V logits are
+ * never stored.  H [T, d], W [V, d] in_dtype; tokens, mask, logprob, entropy and
+ * lse as above, chunk as in ckl_problem.  Masked rows are not computed and may
+ * hold anything; their results are 0.  fp32 products and sums (bf16: exact
+ * products, fp32 sums).
+ *   ws: ckl_head_workspace_size(T, d, V, chunk, in_dtype, dh_dtype, dw_dtype,
+ *   masked, which) bytes; which 0: forward (the output dtypes do not matter), 1:
+ *   backward; masked: 1 where a mask is given. */
+ckl_status ckl_head_workspace_size(int64_t T, int64_t d, int64_t V, int64_t chunk, int32_t in_dtype, int32_t dh_dtype,
+                                   int32_t dw_dtype, int32_t masked, int which, size_t* bytes);
+ckl_status ckl_head_logprobs(const void* H, const void* W, int32_t in_dtype, int64_t T, int64_t d, int64_t V,
+                             const void* tokens, int32_t token_bytes, const uint8_t* mask, int64_t chunk,
+                             float* logprob, float* entropy, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* Its gradients dH = G W and dW = G^T H with G[t, v] as dlogits above (dlogprob or
+ * dentropy NULL: zero).  The logits are multiplied again, and G is kept in blocks of
+ * about chunk x V entries of in_dtype (bf16 rounds it once).  dH [T, d] dh_dtype,
+ * dW [V, d] dw_dtype, overwritten; one of them may be NULL and is then not
+ * computed.  lse and entropy: from ckl_head_logprobs on the same inputs.  T = 0:
+ * dW is zero. */
+ckl_status ckl_head_logprobs_backward(const void* H, const void* W, int32_t in_dtype, int64_t T, int64_t d, int64_t V,
+                                      const void* tokens, int32_t token_bytes, const uint8_t* mask, int64_t chunk,
+                                      const float* lse, const float* entropy, const float* dlogprob,
+                                      const float* dentropy, void* dH, int32_t dh_dtype, void* dW, int32_t dw_dtype,
+                                      void* ws, size_t ws_bytes, void* stream);
+
+/* Dropout whose mask is a function of (seed, offset, element) and never stored:
+ * out[i] = x[i] * 65536 / (65536 - t) where element i is kept, 0 elsewhere, with t =
+ * 65536 p rounded to the nearest integer (ties to even; the share dropped is t /
+ * 65536).  Element i is kept where its sixteen random bits are >= t: half i % 2
+ * (0: the low one) of word (i % 8) / 2 of Philox4x32-10 with key (low, high word of
+ * seed) and counter (low, high word of i / 8, low, high word of offset).  The
+ * gradient is the same call on the incoming one.
+ *   x, out: [n] dtype, n up to 2^40.  0 <= p <= 1 (1: all zeros).
+ *   state:  NULL, or 2 int64 in device memory, {seed, offset}, read when the kernel
+ *           runs: the seed is then state[0] and state[1] is added to `offset`, so
+ *           that a captured call draws anew when the memory changes. */
+ckl_status ckl_dropout(const void* x, int32_t dtype, int64_t n, double p, uint64_t seed, uint64_t offset,
+                       const int64_t* state, void* out, void* stream);
+
+/* RMS norm behind a branch: h = residual + dropout(x) (element t d + i of the mask
+ * above; p = 0: no dropout) rounded once to the residual's type, and
+ *   y[t] = h[t] * rstd[t] * weight,   rstd[t] = 1 / sqrt(mean_i h[t, i]^2 + eps)
+ * of the rounded h, in fp32, rounded once.  The sum of squares is an fp32 sum (taken
+ * again of h 2^-96 where it is past that type; eps should keep rows of values below
+ * 1e-19 from vanishing in it); a row that holds an infinity or a NaN gives NaN there.
+ *   x, y: [T, d] x_dtype.  residual, h: [T, d] r_dtype, which is x_dtype, or fp32
+ *   with x in bf16.  weight: [d].  rstd: [T] float32 or NULL (no backward pass). */
+ckl_status ckl_add_norm_forward(const void* x, int32_t x_dtype, const void* residual, int32_t r_dtype, int64_t T,
+                                int64_t d, const void* weight, int32_t weight_dtype, float eps, double p,
+                                uint64_t seed, uint64_t offset, const int64_t* state, void* h, void* y, float* rstd,
+                                void* stream);
+
+/* Its gradients, with n = h * rstd and dh the gradient that reaches h from elsewhere
+ * (the residual stream; NULL: none):
+ *   dresidual = dh + rstd * (dy * weight - n * mean_i(dy * weight * n)),
+ *   dx = dropout(dresidual, unrounded),   dweight = sum_t dy * n,
+ * in fp32, each rounded once.  p, seed, offset, state: the forward's, with the same
+ * values in state.
+ *   dy, dx: [T, d] x_dtype.  dh, dresidual: [T, d] r_dtype.  dx may be NULL where it
+ *   is dresidual (no dropout and one type).  dweight: [d] weight_dtype (zero for T =
+ *   0).  ws: ckl_add_norm_workspace_size(T, d) bytes. */
+ckl_status ckl_add_norm_workspace_size(int64_t T, int64_t d, size_t* bytes);
+ckl_status ckl_add_norm_backward(const void* dy, int32_t x_dtype, const void* dh, int32_t r_dtype, int64_t T,
+                                 int64_t d, const void* h, const float* rstd, const void* weight,
+                                 int32_t weight_dtype, double p, uint64_t seed, uint64_t offset, const int64_t* state,
+                                 void* dx, void* dresidual, void* dweight, void* ws, size_t ws_bytes, void* stream);
+
+/* The norm's output in 8 bits, for a product that reads them: h as above without
+ * dropout, and y (not rounded in between) as
+ *   CKL_QUANT_INT8: codes int8 [T, d] and scales uint8 [T, ceil(d / CKL_ACT_BLOCK)], the
+ *     form of ckl_act_encode, which ckl_act_decode restores;
+ *   CKL_QUANT_E4M3: codes e4m3 (OCP, no infinities) [T, d] and scales float32 [T]: a
+ *     code is y / scale rounded to nearest even, scale = max |y| / 448 of the row (at
+ *     least 2^-126); NaN, with codes of zero, for a row that holds an infinity or a NaN. */
+typedef enum { CKL_QUANT_INT8 = 1, CKL_QUANT_E4M3 = 2 } ckl_quant_form;
+ckl_status ckl_add_norm_quant(const void* x, int32_t x_dtype, const void* residual, int32_t r_dtype, int64_t T,
+                              int64_t d, const void* weight, int32_t weight_dtype, float eps, int32_t form, void* h,
+                              void* codes, void* scales, void* stream);
+
 /* Kernel classes for the timing records below. */
 typedef enum {
   CKL_KERNEL_TEACHER_PREP = 0, /* teacher softmax + sort                      */
@@ -391,9 +507,10 @@ typedef enum {
   CKL_KERNEL_G_PASS = 5,       /* fused call: u -> G (fp32 also G^T)        */
   CKL_KERNEL_TRANSPOSE = 6,    /* H^T and W^T staging                         */
   CKL_KERNEL_OTHER = 7,        /* counts, scales, fills, casts               */
-  CKL_KERNEL_TOPK = 8,         /* ckl_teacher_topk                            */
+  CKL_KERNEL_TOPK = 8,         /* ckl_teacher_topk, ckl_token_logprobs*       */
   CKL_KERNEL_EMBEDDING = 9,    /* ckl_embedding_forward / _backward           */
-  CKL_KERNEL_ACTIVATION = 10,  /* ckl_act_encode / _decode, ckl_norm_*        */
+  CKL_KERNEL_ACTIVATION = 10,  /* ckl_act_*, ckl_norm_*, ckl_dropout,         */
+                               /* ckl_add_norm_*                              */
   CKL_KERNEL_CLASSES = 11
 } ckl_kernel_class;
 
