@@ -1,7 +1,6 @@
 // gfx950 kernels of the log probabilities of given tokens, and of the rows'
 // entropies, straight from hidden states and the output head: the logits never
 // leave the MFMA accumulators.
-//   head_tokens   the rows' tokens as columns, in the order of the (packed) rows
 //   head_rows     z^T = W H^T by tiles; a row's log sum exp and sum of p log p
 //                 behind a running maximum, the token's logit where it falls
 //   head_finish   splits merged; log probability, entropy, log sum exp
@@ -19,8 +18,15 @@ namespace ckl {
 
 namespace {
 
+// Tiles (vocabulary x token rows, and a wave's share of them).  Few rows: W is read once whatever the tile, and a
+// narrow one leaves room for several workgroups on a compute unit, whose loads hide one another's latency.
 using CfgWide = Dma64Cfg<256, 256, 128, 64>;
+using CfgMiddle = Dma64Cfg<256, 128, 64, 64>;
+using CfgNarrow = Dma64Cfg<128, 64, 32, 32>;
+using CfgSlim = Dma64Cfg<128, 32, 32, 32>;
 using CfgF32 = TileCfg<float, 128, 128, 64, 64>;
+using CfgF32Small = TileCfg<float, 64, 128, 32, 64>;
+using CfgF32Slim = TileCfg<float, 128, 32, 32, 32>;
 
 constexpr float kExpZero = -1e4f;  // 2^x is zero from here on, and its product with x too
 
@@ -35,21 +41,12 @@ __device__ __forceinline__ void ent2_merge(float& m, float& s, float& e, float m
   m = mn;
 }
 
-// tok[i] = the column of row i's token, -1 where it is none (or row i is past the
-// rows).  perm not NULL: row i is row perm[i] of the call, for i < *n.
-__global__ __launch_bounds__(256) void head_tokens_kernel(const void* __restrict__ tokens, int tokens64, int T, int Tp,
-                                                          int V, const int* __restrict__ perm,
-                                                          const int* __restrict__ n, int* __restrict__ tok) {
-  const int i = blockIdx.x * 256 + threadIdx.x;
-  if (i >= Tp) return;
-  int c = -1;
-  if (i < (n != nullptr ? *n : T)) {
-    const int t = perm != nullptr ? perm[i] : i;
-    const int64_t v = tokens64 ? reinterpret_cast<const int64_t*>(tokens)[t]
-                               : (int64_t)reinterpret_cast<const int32_t*>(tokens)[t];
-    if (v >= 0 && v < V) c = (int)v;
-  }
-  tok[i] = c;
+// The column of packed row i's token, -1 where it is none.
+__device__ __forceinline__ int token_column(const HeadRows& r, int i, int V) {
+  const int t = r.perm != nullptr ? r.perm[i] : i;
+  const int64_t v = r.tokens64 ? reinterpret_cast<const int64_t*>(r.tokens)[t]
+                               : (int64_t)reinterpret_cast<const int32_t*>(r.tokens)[t];
+  return v >= 0 && v < V ? (int)v : -1;
 }
 
 // ---------------------------------------------------------------- forward --
@@ -63,8 +60,8 @@ constexpr int kGroupRows = 8;  // row blocks that walk the vocabulary together (
 template <class C>
 __global__ __launch_bounds__(C::NTHREADS) void head_rows_kernel(
     const typename C::TIn* __restrict__ H, const typename C::TIn* __restrict__ W, int T, int d, int V,
-    const int* __restrict__ tok, float* __restrict__ ztok, float4* __restrict__ part, int n_vtiles,
-    int tiles_per_split, int n_tblocks, int n_splits, const int* __restrict__ nrows, int row0) {
+    HeadRows rows, int row0, float* __restrict__ ztok, float4* __restrict__ part, int n_vtiles, int tiles_per_split,
+    int n_tblocks, int n_splits) {
   using TileT = typename C::TileT;
   using L = typename TileT::L;
   constexpr int MBK = TileT::MBK, NBK = TileT::NBK, BLK = L::BLK, RPB = L::RPB;
@@ -76,12 +73,14 @@ __global__ __launch_bounds__(C::NTHREADS) void head_rows_kernel(
   int tblock, split;
   grouped_mn(xcd_remap(blockIdx.x, n_tblocks * n_splits), n_tblocks, n_splits, kGroupRows, tblock, split);
   const int t0 = tblock * C::BN;
-  if (nrows != nullptr && t0 >= *nrows - row0) return;  // packed rows: no kept row here (its results are never read)
+  // packed rows: those past the last kept one are never read
+  const int kept = rows.n != nullptr ? *rows.n - row0 : T;
+  if (t0 >= kept) return;
   const int vt0 = split * tiles_per_split;
   const int vt1 = min(n_vtiles, vt0 + tiles_per_split);
   const int own_nb = NBK == 1 ? 0 : lane / 32;
   const int own_row = t0 + wave_n * C::WN + own_nb * BLK + (lane & 31);
-  const int own_tok = own_row < T ? tok[own_row] : -1;
+  const int own_tok = own_row < min(T, kept) ? token_column(rows, row0 + own_row, V) : -1;
   float rm = -INFINITY, rs = 0.f, re = 0.f;
 
   TileT tile;
@@ -177,21 +176,20 @@ __global__ __launch_bounds__(C::NTHREADS) void head_rows_kernel(
   }
 }
 
-// Row t of the call: sixteen lanes merge its splits.  rank not NULL: its place
-// among the packed rows, -1 where it is masked (all results zero then).  T rows of
-// the call from row0 on; part and ztok are of this launch's rows, [S][rows].
-__global__ __launch_bounds__(256) void head_finish_kernel(const float4* __restrict__ part, int S, int rows, int row0,
-                                                          const float* __restrict__ ztok, const int* __restrict__ tok,
-                                                          const int* __restrict__ perm, const int* __restrict__ n,
+// Packed row row0 + i: sixteen lanes merge its splits ([S][count], with ztok from
+// row0 on) into its row of the call; and row row0 + i of the call, where it is
+// masked, gets zeros.
+__global__ __launch_bounds__(256) void head_finish_kernel(const float4* __restrict__ part, int S, int count, int V,
+                                                          HeadRows rows, int row0, const float* __restrict__ ztok,
                                                           float* __restrict__ logprob, float* __restrict__ entropy,
                                                           float* __restrict__ lse) {
   const int sub = threadIdx.x & 15;
-  const int i = blockIdx.x * 16 + (threadIdx.x >> 4);
-  const bool live = i < rows && (n == nullptr || row0 + i < *n);
+  const int i = blockIdx.x * 16 + (threadIdx.x >> 4), p = row0 + i;
+  const bool live = i < count && (rows.n == nullptr || p < *rows.n);
   float m = -INFINITY, s = 0.f, e = 0.f;
   if (live)
     for (int k = sub; k < S; k += 16) {
-      const float4 v = part[(int64_t)k * rows + i];
+      const float4 v = part[(int64_t)k * count + i];
       ent2_merge(m, s, e, v.x, v.y, v.z);
     }
 #pragma unroll
@@ -199,21 +197,14 @@ __global__ __launch_bounds__(256) void head_finish_kernel(const float4* __restri
     const float om = __shfl_xor(m, o), os = __shfl_xor(s, o), oe = __shfl_xor(e, o);
     ent2_merge(m, s, e, om, os, oe);
   }
+  if (sub == 1 && i < count && rows.rank != nullptr && rows.rank[p] < 0) logprob[p] = entropy[p] = lse[p] = 0.f;
   if (sub != 0 || !live) return;
-  const int t = perm != nullptr ? perm[row0 + i] : row0 + i;
+  const int t = rows.perm != nullptr ? rows.perm[p] : p;
   const float l2 = fast_log2(s), l = (m + l2) * kLn2;
-  float ent = (l2 - e / s) * kLn2;
+  const float ent = (l2 - e / s) * kLn2;
   lse[t] = l;
   entropy[t] = ent < 0.f ? 0.f : ent;
-  logprob[t] = tok[i] >= 0 ? ztok[i] - l : 0.f;
-}
-
-// Results of masked rows.
-__global__ __launch_bounds__(256) void head_masked_kernel(const int* __restrict__ rank, int T,
-                                                          float* __restrict__ logprob, float* __restrict__ entropy,
-                                                          float* __restrict__ lse) {
-  const int t = blockIdx.x * 256 + threadIdx.x;
-  if (t < T && rank[t] < 0) logprob[t] = entropy[t] = lse[t] = 0.f;
+  logprob[t] = token_column(rows, p, V) >= 0 ? ztok[i] - l : 0.f;
 }
 
 // --------------------------------------------------------------- backward --
@@ -222,9 +213,8 @@ __global__ __launch_bounds__(256) void head_masked_kernel(const int* __restrict_
 // for its incoming gradients a (log probability) and b (entropy).  Row i:
 // consts[i] = (c0, lse log2 e, c1, a), its token.  Rows past the last one and rows
 // with no gradient get an lse that makes q zero.
-__global__ __launch_bounds__(256) void head_consts_kernel(const void* __restrict__ tokens, int tokens64, int T, int Tp,
-                                                          int V, const int* __restrict__ perm,
-                                                          const int* __restrict__ n, const float* __restrict__ lse,
+__global__ __launch_bounds__(256) void head_consts_kernel(HeadRows rows, int T, int Tp, int V,
+                                                          const float* __restrict__ lse,
                                                           const float* __restrict__ entropy,
                                                           const float* __restrict__ dlogprob,
                                                           const float* __restrict__ dentropy,
@@ -233,11 +223,9 @@ __global__ __launch_bounds__(256) void head_consts_kernel(const void* __restrict
   if (i >= Tp) return;
   int c = -1;
   float4 k = make_float4(0.f, 1e30f, 0.f, 0.f);
-  if (i < (n != nullptr ? *n : T)) {
-    const int t = perm != nullptr ? perm[i] : i;
-    const int64_t v = tokens64 ? reinterpret_cast<const int64_t*>(tokens)[t]
-                               : (int64_t)reinterpret_cast<const int32_t*>(tokens)[t];
-    if (v >= 0 && v < V) c = (int)v;
+  if (i < (rows.n != nullptr ? *rows.n : T)) {
+    const int t = rows.perm != nullptr ? rows.perm[i] : i;
+    c = token_column(rows, i, V);
     const float a = c >= 0 && dlogprob != nullptr ? dlogprob[t] : 0.f;
     const float b = dentropy != nullptr ? dentropy[t] : 0.f;
     if (!(a == 0.f && b == 0.f))
@@ -379,74 +367,83 @@ __global__ __launch_bounds__(C::NTHREADS) void head_grad_kernel(
 #define CKL_LAUNCH_CHECK() \
   do { hipError_t e_ = hipGetLastError(); if (e_ != hipSuccess) return e_; } while (0)
 
-HeadTile head_tile(int in_bf16, int64_t rows) {
-  (void)rows;
-  if (!in_bf16) return HeadTile{0, CfgF32::BM, CfgF32::BN, 256};
-  return HeadTile{1, CfgWide::BM, CfgWide::BN, 256};
+enum { kF32, kF32Small, kF32Slim, kWide, kMiddle, kNarrow, kSlim };
+template <typename F>
+void by_tile(int kind, F&& f) {
+  switch (kind) {
+    case kF32: f(CfgF32{}); break;
+    case kF32Small: f(CfgF32Small{}); break;
+    case kF32Slim: f(CfgF32Slim{}); break;
+    case kWide: f(CfgWide{}); break;
+    case kMiddle: f(CfgMiddle{}); break;
+    case kNarrow: f(CfgNarrow{}); break;
+    default: f(CfgSlim{}); break;
+  }
 }
 
-hipError_t launch_head_tokens(const void* tokens, int tokens64, int T, int Tp, int V, const int* perm, const int* n,
-                              int* tok, hipStream_t st) {
-  head_tokens_kernel<<<(Tp + 255) / 256, 256, 0, st>>>(tokens, tokens64, T, Tp, V, perm, n, tok);
-  CKL_LAUNCH_CHECK();
-  return hipSuccess;
+HeadTile head_tile(int in_bf16, int64_t rows, int64_t V) {
+  int kind;
+  if (in_bf16)
+    kind = rows <= 32 ? kSlim : rows <= 64 ? kNarrow : rows <= 128 ? kMiddle : kWide;
+  else
+    kind = rows <= 32 ? kF32Slim : (rows + 127) / 128 * ((V + 127) / 128) < 256 ? kF32Small : kF32;
+  HeadTile t{kind, 0, 0, 0};
+  by_tile(kind, [&](auto cfg) {
+    using C = decltype(cfg);
+    t.BM = C::BM;
+    t.BN = C::BN;
+    t.slots = 256 * (163840 / C::LDS_BYTES > 4 ? 4 : 163840 / C::LDS_BYTES);
+  });
+  return t;
 }
 
-hipError_t launch_head_rows(const HeadTile& k, const void* H, const void* W, int T, int d, int V, const int* tok,
-                            float* ztok, float4* part, int n_splits, int tiles_per_split, const int* nrows, int row0,
-                            hipStream_t st) {
+hipError_t launch_head_rows(const HeadTile& k, const void* H, const void* W, int T, int d, int V, const HeadRows& rows,
+                            int row0, float* ztok, float4* part, int n_splits, int tiles_per_split, hipStream_t st) {
   const int n_vtiles = (V + k.BM - 1) / k.BM, n_tblocks = (T + k.BN - 1) / k.BN;
   auto go = [&](auto cfg) {
     using C = decltype(cfg);
     using TIn = typename C::TIn;
-    head_rows_kernel<C><<<n_tblocks * n_splits, C::NTHREADS, 0, st>>>((const TIn*)H, (const TIn*)W, T, d, V, tok, ztok,
-                                                                      part, n_vtiles, tiles_per_split, n_tblocks,
-                                                                      n_splits, nrows, row0);
+    head_rows_kernel<C><<<n_tblocks * n_splits, C::NTHREADS, 0, st>>>((const TIn*)H, (const TIn*)W, T, d, V, rows, row0,
+                                                                      ztok, part, n_vtiles, tiles_per_split, n_tblocks,
+                                                                      n_splits);
   };
-  switch (k.kind) {
-    case 0: go(CfgF32{}); break;
-    default: go(CfgWide{}); break;
-  }
+  by_tile(k.kind, go);
   CKL_LAUNCH_CHECK();
   return hipSuccess;
 }
 
-hipError_t launch_head_finish(const float4* part, int S, int rows, int row0, const float* ztok, const int* tok,
-                              const int* perm, const int* n, float* logprob, float* entropy, float* lse,
-                              hipStream_t st) {
-  head_finish_kernel<<<(rows + 15) / 16, 256, 0, st>>>(part, S, rows, row0, ztok, tok, perm, n, logprob, entropy, lse);
+hipError_t launch_head_finish(const float4* part, int S, int count, int V, const HeadRows& rows, int row0,
+                              const float* ztok, float* logprob, float* entropy, float* lse, hipStream_t st) {
+  head_finish_kernel<<<(count + 15) / 16, 256, 0, st>>>(part, S, count, V, rows, row0, ztok, logprob, entropy, lse);
   CKL_LAUNCH_CHECK();
   return hipSuccess;
 }
 
-hipError_t launch_head_masked(const int* rank, int T, float* logprob, float* entropy, float* lse, hipStream_t st) {
-  head_masked_kernel<<<(T + 255) / 256, 256, 0, st>>>(rank, T, logprob, entropy, lse);
-  CKL_LAUNCH_CHECK();
-  return hipSuccess;
-}
-
-hipError_t launch_head_consts(const void* tokens, int tokens64, int T, int Tp, int V, const int* perm, const int* n,
-                              const float* lse, const float* entropy, const float* dlogprob, const float* dentropy,
-                              float4* consts, int* tok, hipStream_t st) {
-  head_consts_kernel<<<(Tp + 255) / 256, 256, 0, st>>>(tokens, tokens64, T, Tp, V, perm, n, lse, entropy, dlogprob,
-                                                       dentropy, consts, tok);
+hipError_t launch_head_consts(const HeadRows& rows, int T, int Tp, int V, const float* lse, const float* entropy,
+                              const float* dlogprob, const float* dentropy, float4* consts, int* tok, hipStream_t st) {
+  head_consts_kernel<<<(Tp + 255) / 256, 256, 0, st>>>(rows, T, Tp, V, lse, entropy, dlogprob, dentropy, consts, tok);
   CKL_LAUNCH_CHECK();
   return hipSuccess;
 }
 
 hipError_t launch_head_grad(int in_bf16, const void* H, const void* W, int T, int d, int V, const float4* consts,
-                            const int* tok, int tb0, int t_rows, int vb0, int v_rows, int n_splits,
-                            int tiles_per_split, void* G, int64_t ldG, void* Gt, int64_t ldGt, const int* nrows,
-                            hipStream_t st) {
-  auto go = [&](auto cfg) {
+                            const int* tok, int tb0, int t_rows, int vb0, int v_rows, int tiles_per_split, void* G,
+                            int64_t ldG, void* Gt, int64_t ldGt, const int* nrows, hipStream_t st) {
+  auto go = [&](auto cfg, int tps) {
     using C = decltype(cfg);
     using TIn = typename C::TIn;
-    const int n_vtiles = v_rows / C::BM, n_tblocks = t_rows / C::BN;
-    head_grad_kernel<C><<<n_tblocks * n_splits, C::NTHREADS, 0, st>>>(
-        (const TIn*)H, (const TIn*)W, T, d, V, consts, tok, tb0, vb0, n_vtiles, tiles_per_split, n_tblocks, n_splits,
-        (TIn*)G, ldG, (TIn*)Gt, ldGt, nrows);
+    const int n_vtiles = v_rows / C::BM, n_tblocks = t_rows / C::BN, splits = (n_vtiles + tps - 1) / tps;
+    head_grad_kernel<C><<<n_tblocks * splits, C::NTHREADS, 0, st>>>(
+        (const TIn*)H, (const TIn*)W, T, d, V, consts, tok, tb0, vb0, n_vtiles, tps, n_tblocks, splits, (TIn*)G, ldG,
+        (TIn*)Gt, ldGt, nrows);
   };
-  in_bf16 ? go(CfgWide{}) : go(CfgF32{});
+  // (fp32 tiles that would not fill the compute units: halves of them)
+  if (in_bf16)
+    go(CfgWide{}, tiles_per_split);
+  else if ((int64_t)(t_rows / CfgF32::BN) * (v_rows / CfgF32::BM) < 256)
+    go(CfgF32Small{}, 1);
+  else
+    go(CfgF32{}, tiles_per_split);
   CKL_LAUNCH_CHECK();
   return hipSuccess;
 }

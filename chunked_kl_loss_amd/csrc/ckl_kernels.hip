@@ -1303,6 +1303,7 @@ struct GemmProblem {
   // (kdim rounded up to lim_round, the rows of whole G tiles)
   const int* lim;
   int lim_base, lim_kind, lim_round;
+  bf16_t* out16;  // (B16) not NULL: the sum rounded to bf16 goes here, with out's stride; out is read only
 };
 
 constexpr int kGroupM = 2;
@@ -1313,7 +1314,8 @@ constexpr bool kXtOK = false;
 template <int BM, int BN, int WM, int WN>
 constexpr bool kXtOK<Dma64Cfg<BM, BN, WM, WN>> = BM % 128 == 0;
 
-template <class C>
+// B16: results may leave in bf16 (GemmProblem::out16).
+template <class C, bool B16 = false>
 __global__ __launch_bounds__(C::NTHREADS) void gemm_store_kernel(GemmProblem<typename C::TIn> p0,
                                                                  GemmProblem<typename C::TIn> p1) {
   // bf16 configurations stage the fp32 output through LDS one wave row block
@@ -1376,7 +1378,10 @@ __global__ __launch_bounds__(C::NTHREADS) void gemm_store_kernel(GemmProblem<typ
         const int rnd = second ? p1.lim_round : p0.lim_round;
         const int kl = n_lim <= 0 ? 0 : (n_lim + rnd - 1) / rnd * rnd;
         kdim = min(kdim, kl);
-        if (kdim <= 0 && beta) return;
+        if (kdim <= 0 && beta) {
+          if constexpr (!B16) return;
+          if ((second ? p1.out16 : p0.out16) == nullptr) return;  // (else the old sums still have to be rounded)
+        }
       }
     }
   }
@@ -1450,6 +1455,15 @@ __global__ __launch_bounds__(C::NTHREADS) void gemm_store_kernel(GemmProblem<typ
             const int m = r0 + ml, n = n0 + c4;
             if (m >= M_eff || n >= N) continue;
             const f32x4 a = *reinterpret_cast<const f32x4*>(st + ml * C::BN + (c4 ^ stage_swz(ml)));
+            if constexpr (B16) {
+              bf16_t* o16 = second ? p1.out16 : p0.out16;
+              if (o16 != nullptr) {  // (N and ldo are multiples of 4)
+                const f32x4 r = beta ? a + *reinterpret_cast<const f32x4*>(oldb + i * 4) : a;
+                *reinterpret_cast<u32x2*>(o16 + (int64_t)m * ldo + n) =
+                    u32x2{pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3])};
+                continue;
+              }
+            }
             float* o = out + (int64_t)m * ldo + n;
             if (n + 4 <= N) {
               *reinterpret_cast<f32x4*>(o) = beta ? a + *reinterpret_cast<const f32x4*>(oldb + i * 4) : a;
@@ -1791,6 +1805,11 @@ static hipError_t gemm_pair_t(const GemmArgs& a0, const GemmArgs& a1, hipStream_
     p[i].lim_base = a[i]->lim_base;
     p[i].lim_kind = a[i]->lim ? a[i]->lim_kind : 0;
     p[i].lim_round = a[i]->lim_round > 0 ? a[i]->lim_round : 1;
+    p[i].out16 = (bf16_t*)a[i]->out16;
+    // (the path that writes it: 16-byte rows of sums, whole vectors)
+    if (a[i]->out16 && (sizeof(TIn) != 2 || a[i]->batches > 1 || a[i]->N % 4 || a[i]->ldo % 4 ||
+                        ((uintptr_t)a[i]->out & 15) || ((uintptr_t)a[i]->out16 & 7)))
+      return hipErrorInvalidValue;
     if (a[i]->lim && (a[i]->lim_kind < 1 || a[i]->lim_kind > 2 || (a[i]->lim_kind == 2 && a[i]->lim_round % 8)))
       return hipErrorInvalidValue;
     // k-major X: every tile reads BM whole columns of each k row
@@ -1801,6 +1820,13 @@ static hipError_t gemm_pair_t(const GemmArgs& a0, const GemmArgs& a1, hipStream_
   }
   if (p[0].tiles + p[1].tiles == 0) return hipSuccess;
   const int n = (p[0].tiles + kNumXcd - 1) / kNumXcd * kNumXcd + p[1].tiles;
+  if constexpr (sizeof(TIn) == 2) {
+    if (p[0].out16 || p[1].out16) {
+      hipLaunchKernelGGL((gemm_store_kernel<C, true>), dim3(n), dim3(C::NTHREADS), 0, st, p[0], p[1]);
+      CKL_LAUNCH_CHECK();
+      return hipSuccess;
+    }
+  }
   hipLaunchKernelGGL(gemm_store_kernel<C>, dim3(n), dim3(C::NTHREADS), 0, st, p[0], p[1]);
   CKL_LAUNCH_CHECK();
   return hipSuccess;

@@ -108,6 +108,8 @@ struct GemmArgs {
   // skipped), 2 bounds kdim by it rounded up to lim_round (a multiple of 8)
   const int* lim = nullptr;
   int lim_base = 0, lim_kind = 0, lim_round = 1;
+  // bf16 inputs, no batches: the result in bf16 goes here, with out's stride (beta adds out, which is only read)
+  void* out16 = nullptr;
 };
 // Two independent products in one launch (problem 0's tiles are scheduled first).
 hipError_t launch_gemm_pair(int in_bf16, const GemmArgs& a0, const GemmArgs& a1, hipStream_t st);

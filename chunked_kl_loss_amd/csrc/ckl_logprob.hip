@@ -146,10 +146,16 @@ hipError_t launch_token_logprobs(const void* logits, int bf16, int64_t rows, int
   if (top == 0) {
     auto go = [&](auto* p) {
       using E = std::remove_const_t<std::remove_pointer_t<decltype(p)>>;
-      if (rows < 2048)
-        row_stats_kernel<E, 1024><<<(unsigned)rows, 1024, 0, st>>>(p, rows, (int)V, t.mask, out, lse);
+      auto run = [&](auto threads) {
+        constexpr int N = decltype(threads)::value;
+        row_stats_kernel<E, N><<<(unsigned)rows, N, 0, st>>>(p, rows, (int)V, t.mask, out, lse);
+      };
+      if (V <= 2048)
+        run(std::integral_constant<int, 64>{});
+      else if (V <= 65536)
+        run(std::integral_constant<int, 256>{});
       else
-        row_stats_kernel<E, 256><<<(unsigned)rows, 256, 0, st>>>(p, rows, (int)V, t.mask, out, lse);
+        run(std::integral_constant<int, 512>{});
     };
     bf16 ? go((const bf16_t*)logits) : go((const float*)logits);
     return hipGetLastError();

@@ -80,8 +80,8 @@ struct HeadPlan {
   // forward: chunks of Cs rows
   ckl::HeadTile tile;
   int64_t Cs, nS, splits, tps;
-  // backward: G blocks of Tc rows x Vc columns
-  int64_t BM, BN, Tp, Vp, Tc, Vc, nT, nV;
+  // backward: G blocks of Tc rows x Vc columns; dH as Sh sums over Vs columns of a block each
+  int64_t BM, BN, Tp, Vp, Tc, Vc, nT, nV, Sh, Vs;
 };
 ckl_status head_plan(int64_t T, int64_t d, int64_t V, int64_t chunk, int32_t in_dtype, int32_t dh_dtype,
                      int32_t dw_dtype, HeadPlan* q) {
@@ -92,7 +92,9 @@ ckl_status head_plan(int64_t T, int64_t d, int64_t V, int64_t chunk, int32_t in_
   p.d = d;
   p.V = V;
   p.K = 1;
-  p.chunk = chunk;
+  // (the plan keeps half its budget of chunk x V entries for bf16: all of it here.  2048 x 2880 over 201088 words,
+  // forward and backward, in 2 / 3 blocks: see head_grad)
+  p.chunk = chunk * (in_dtype == CKL_BF16 ? 2 : 1);
   p.in_dtype = in_dtype;
   p.dh_dtype = dh_dtype;
   p.dw_dtype = dw_dtype;
@@ -112,10 +114,17 @@ ckl_status head_plan(int64_t T, int64_t d, int64_t V, int64_t chunk, int32_t in_
   q->Vc = blocks[1];
   q->nT = blocks[2];
   q->nV = blocks[3];
+  // dH has few tiles of a long sum, dW many of a short one: dH is cut into parts of about a quarter of a compute
+  // unit's share of both (but not below the 512 columns that cost as much as storing a part's tile)
+  const int64_t gm = ckl::gemm_tile_m(q->bf16), gn = ckl::gemm_tile_n(q->bf16);
+  const int64_t dh_tiles = ceil_div(q->Tc, gm) * ceil_div(d, gn), dw_tiles = ceil_div(q->Vc, gm) * ceil_div(d, gn);
+  const int64_t share = (dh_tiles * q->Vc + dw_tiles * q->Tc) / (kGradSlots * 4);
+  q->Vs = std::min(round_up(std::max<int64_t>(share, 512), 64), q->Vc);
+  q->Sh = ceil_div(q->Vc, q->Vs);
   q->Cs = std::min(round_up(chunk, 256), round_up(p.T, 256));
   q->nS = ceil_div(p.T, q->Cs);
   const int64_t rows = std::min(q->Cs, p.T);
-  q->tile = ckl::head_tile(q->bf16, rows);
+  q->tile = ckl::head_tile(q->bf16, rows, V);
   pick_splits(ceil_div(rows, q->tile.BN), ceil_div(V, q->tile.BM), q->tile.slots, &q->splits, &q->tps);
   return CKL_OK;
 }
@@ -141,14 +150,13 @@ PackWs pack_layout(const HeadPlan& q, Layout* l) {
   return w;
 }
 struct HeadFwdWs {
-  size_t tok, ztok, part, total;
+  size_t ztok, part, total;
   PackWs pk;
 };
 HeadFwdWs head_fwd_layout(const HeadPlan& q, bool masked) {
   HeadFwdWs w{};
   Layout l;
-  w.tok = l.take(q.Tp * 4);
-  w.ztok = l.take(q.Tp * 4);
+  w.ztok = l.take(q.Cs * 4);
   w.part = l.take((size_t)q.splits * q.Cs * 16);
   if (masked) w.pk = pack_layout(q, &l);
   w.total = l.o;
@@ -167,33 +175,28 @@ HeadBwdWs head_bwd_layout(const HeadPlan& q, bool masked, int32_t dh_dtype, int3
   w.Wt = l.take((size_t)q.d * (q.Vc + kLdPad) * q.esz);
   w.G = l.take((size_t)q.Tc * (q.Vc + kLdPad) * q.esz);
   w.Gt = q.bf16 ? 0 : l.take((size_t)q.Vc * (q.Tc + kLdPad) * q.esz);
-  w.dH = dh_dtype == CKL_BF16 || masked ? l.take((size_t)q.T * q.d * 4) : 0;
-  w.dW = dw_dtype == CKL_BF16 ? l.take((size_t)q.V * q.d * 4) : 0;
+  w.dH = dh_dtype == CKL_BF16 || masked || q.Sh > 1 ? l.take((size_t)q.Sh * q.T * q.d * 4) : 0;
+  // fp32 sums of a bf16 dW (bf16 inputs: needed only between blocks of rows)
+  w.dW = dw_dtype == CKL_BF16 && (!q.bf16 || q.nT > 1) ? l.take((size_t)q.V * q.d * 4) : 0;
   if (masked) w.pk = pack_layout(q, &l);
   w.total = l.o;
   return w;
 }
 
-// The rows that a call works on: all of H, or the packed copy of the kept ones.
-struct Rows {
-  const void* H;
-  const int* perm = nullptr;
-  int* rank = nullptr;
-  const int* n = nullptr;
-};
-hipError_t head_pack(const HeadPlan& q, char* b, const PackWs& w, const uint8_t* mask, const void* H, hipStream_t st,
-                     Rows* r) {
-  int* perm = (int*)(b + w.perm);
-  int* n = (int*)(b + w.N);
-  r->rank = (int*)(b + w.rank);
-  hipError_t e = timed(CKL_KERNEL_OTHER, st,
-                       [&] { return ckl::launch_compact_rows(mask, (int)q.T, perm, r->rank, n, st); });
+// Packs the kept rows of a mask: *H and *rows become theirs.
+hipError_t head_pack(const HeadPlan& q, char* b, const PackWs& w, const uint8_t* mask, const void** H,
+                     ckl::HeadRows* rows, hipStream_t st) {
+  int *perm = (int*)(b + w.perm), *rank = (int*)(b + w.rank), *n = (int*)(b + w.N);
+  hipError_t e =
+      timed(CKL_KERNEL_OTHER, st, [&] { return ckl::launch_compact_rows(mask, (int)q.T, perm, rank, n, st); });
   if (e != hipSuccess) return e;
-  r->H = b + w.H;
-  r->perm = perm;
-  r->n = n;
+  rows->perm = perm;
+  rows->rank = rank;
+  rows->n = n;
+  const void* from = *H;
+  *H = b + w.H;
   return timed(CKL_KERNEL_OTHER, st,
-               [&] { return ckl::launch_gather_rows(H, (int)q.T, q.d * (int64_t)q.esz, perm, n, b + w.H, st); });
+               [&] { return ckl::launch_gather_rows(from, (int)q.T, q.d * (int64_t)q.esz, perm, n, b + w.H, st); });
 }
 
 }  // namespace
@@ -313,38 +316,27 @@ ckl_status ckl_head_logprobs(const void* H, const void* W, int32_t in_dtype, int
   if (s != CKL_OK) return s;
   hipStream_t st = (hipStream_t)stream;
   char* b = (char*)ws;
-  int* tok = (int*)(b + w.tok);
   float* ztok = (float*)(b + w.ztok);
   float4* part = (float4*)(b + w.part);
-  Rows r{H};
-  if (mask) HIP_TRY(head_pack(q, b, w.pk, mask, H, st, &r), "packing kept rows");
-  HIP_TRY(timed(CKL_KERNEL_OTHER, st,
-                [&] {
-                  return ckl::launch_head_tokens(tokens, token_bytes == 8, (int)T, (int)q.Tp, (int)V, r.perm, r.n, tok,
-                                                 st);
-                }),
-          "head_tokens");
+  ckl::HeadRows r{tokens, token_bytes == 8, nullptr, nullptr, nullptr};
+  const void* Hs = H;
+  if (mask) HIP_TRY(head_pack(q, b, w.pk, mask, &Hs, &r, st), "packing kept rows");
   for (int64_t c = 0; c < q.nS; ++c) {
     const int64_t r0 = c * q.Cs;
     const int rows = (int)std::min(q.Cs, T - r0);
     HIP_TRY(timed(CKL_KERNEL_FWD_LSE, st,
                   [&] {
-                    return ckl::launch_head_rows(q.tile, (const char*)r.H + r0 * d * q.esz, W, rows, (int)d, (int)V,
-                                                 tok + r0, ztok + r0, part, (int)q.splits, (int)q.tps, r.n, (int)r0,
-                                                 st);
+                    return ckl::launch_head_rows(q.tile, (const char*)Hs + r0 * d * q.esz, W, rows, (int)d, (int)V, r,
+                                                 (int)r0, ztok, part, (int)q.splits, (int)q.tps, st);
                   }),
             "head_rows");
     HIP_TRY(timed(CKL_KERNEL_FWD_FINALIZE, st,
                   [&] {
-                    return ckl::launch_head_finish(part, (int)q.splits, rows, (int)r0, ztok + r0, tok + r0, r.perm, r.n,
-                                                   logprob, entropy, lse, st);
+                    return ckl::launch_head_finish(part, (int)q.splits, rows, (int)V, r, (int)r0, ztok, logprob,
+                                                   entropy, lse, st);
                   }),
             "head_finish");
   }
-  if (mask)
-    HIP_TRY(timed(CKL_KERNEL_OTHER, st,
-                  [&] { return ckl::launch_head_masked(r.rank, (int)T, logprob, entropy, lse, st); }),
-            "head_masked");
   return CKL_OK;
 }
 
@@ -389,21 +381,26 @@ ckl_status ckl_head_logprobs_backward(const void* H, const void* W, int32_t in_d
   void* Wt = b + w.Wt;
   void* G = b + w.G;
   void* Gt = q.bf16 ? nullptr : b + w.Gt;
-  Rows r{H};
-  if (mask) HIP_TRY(head_pack(q, b, w.pk, mask, H, st, &r), "packing kept rows");
+  ckl::HeadRows r{tokens, token_bytes == 8, nullptr, nullptr, nullptr};
+  const void* Hs = H;
+  if (mask) HIP_TRY(head_pack(q, b, w.pk, mask, &Hs, &r, st), "packing kept rows");
   // fp32 sums in the outputs themselves, or in the workspace where the output is bf16 or its rows are packed
-  float* dHacc = dh_dtype == CKL_BF16 || mask ? (float*)(b + w.dH) : (float*)dH;
-  float* dWacc = dw_dtype == CKL_BF16 ? (float*)(b + w.dW) : (float*)dW;
+  const bool dh_parts = dh_dtype == CKL_BF16 || mask || q.Sh > 1;
+  float* dHacc = dh_parts ? (float*)(b + w.dH) : (float*)dH;
+  const int64_t dh_stride = T * d;
+  // bf16 inputs and dW: the last block of rows writes the rounded sums
+  const bool dw16 = q.bf16 && dw_dtype == CKL_BF16;
+  float* dWacc = dw_dtype != CKL_BF16 ? (float*)dW : w.dW ? (float*)(b + w.dW) : nullptr;
   HIP_TRY(timed(CKL_KERNEL_OTHER, st,
                 [&] {
-                  return ckl::launch_head_consts(tokens, token_bytes == 8, (int)T, (int)q.Tp, (int)V, r.perm, r.n, lse,
-                                                 entropy, dlogprob, dentropy, consts, tok, st);
+                  return ckl::launch_head_consts(r, (int)T, (int)q.Tp, (int)V, lse, entropy, dlogprob, dentropy, consts,
+                                                 tok, st);
                 }),
           "head_consts");
   if (dW)
     HIP_TRY(timed(CKL_KERNEL_TRANSPOSE, st,
                   [&] {
-                    return ckl::launch_transpose_pad(q.bf16, r.H, (int)T, (int)d, (int)q.Tp, Ht, q.Tp + kLdPad, st);
+                    return ckl::launch_transpose_pad(q.bf16, Hs, (int)T, (int)d, (int)q.Tp, Ht, q.Tp + kLdPad, st);
                   }),
             "transpose H");
   const int64_t ldWt = q.Vc + kLdPad;
@@ -422,18 +419,24 @@ ckl_status ckl_head_logprobs_backward(const void* H, const void* W, int32_t in_d
       pick_splits(trows / q.BN, vrows / q.BM, kGradSlots, &splits, &tps);
       HIP_TRY(timed(CKL_KERNEL_BWD_GRAD, st,
                     [&] {
-                      return ckl::launch_head_grad(q.bf16, r.H, W, (int)T, (int)d, (int)V, consts, tok, (int)tb0,
-                                                   (int)trows, (int)vb0, (int)vrows, (int)splits, (int)tps, G,
+                      return ckl::launch_head_grad(q.bf16, Hs, W, (int)T, (int)d, (int)V, consts, tok, (int)tb0,
+                                                   (int)trows, (int)vb0, (int)vrows, (int)tps, G,
                                                    vrows + kLdPad, Gt, trows + kLdPad, r.n, st);
                     }),
               "head_grad");
-      // dW[vb0 ..) (+)= G^T H[tb0 ..) (bf16: G read k-major),  dH[tb0 ..) (+)= G W[vb0 ..)
-      ckl::GemmArgs gdw{q.bf16 ? G : Gt, q.bf16 ? vrows + kLdPad : trows + kLdPad, Ht + tb0 * q.esz, q.Tp + kLdPad,
-                        dW ? dWacc + vb0 * d : nullptr, d, dW ? (int)std::min(vrows, V - vb0) : 0, (int)d, (int)trows,
-                        tb > 0};
-      gdw.xt = q.bf16;
+      // dH[tb0 ..) (+)= G W[vb0 ..) by parts of the vocabulary block (the longer sums: scheduled first),
+      // dW[vb0 ..) (+)= G^T H[tb0 ..) (bf16: G read k-major)
       ckl::GemmArgs gdh{G, vrows + kLdPad, Wt, ldWt, dH ? dHacc + tb0 * d : nullptr, d,
-                        dH ? (int)std::min(trows, T - tb0) : 0, (int)d, (int)vrows, vb > 0};
+                        dH ? (int)std::min(trows, T - tb0) : 0, (int)d, (int)std::min(q.Vs, vrows), vb > 0};
+      gdh.batches = (int)ceil_div(vrows, q.Vs);
+      gdh.kdim_last = (int)(vrows - (gdh.batches - 1) * q.Vs);
+      gdh.xb = gdh.yb = q.Vs;
+      gdh.ob = dh_stride;
+      ckl::GemmArgs gdw{q.bf16 ? G : Gt, q.bf16 ? vrows + kLdPad : trows + kLdPad, Ht + tb0 * q.esz, q.Tp + kLdPad,
+                        dWacc ? dWacc + vb0 * d : nullptr, d, dW ? (int)std::min(vrows, V - vb0) : 0, (int)d,
+                        (int)trows, tb > 0};
+      gdw.xt = q.bf16;
+      if (dW && dw16 && tb == q.nT - 1) gdw.out16 = (char*)dW + vb0 * d * 2;
       if (r.n) {
         gdw.lim = gdh.lim = r.n;
         gdw.lim_base = gdh.lim_base = (int)tb0;
@@ -441,19 +444,24 @@ ckl_status ckl_head_logprobs_backward(const void* H, const void* W, int32_t in_d
         gdw.lim_round = (int)q.BN;
         gdh.lim_kind = 1;
       }
-      HIP_TRY(timed(CKL_KERNEL_GEMM_DHDW, st, [&] { return ckl::launch_gemm_pair(q.bf16, gdw, gdh, st); }),
-              "gemm dW + dH");
+      HIP_TRY(timed(CKL_KERNEL_GEMM_DHDW, st, [&] { return ckl::launch_gemm_pair(q.bf16, gdh, gdw, st); }),
+              "gemm dH + dW");
     }
   }
   if (dH && mask)
     HIP_TRY(timed(CKL_KERNEL_OTHER, st,
                   [&] {
-                    return ckl::launch_scatter_rows(dHacc, r.rank, (int)T, (int)d, dH, dh_dtype == CKL_BF16, st);
+                    return ckl::launch_zero_masked_rows(r.rank, (int)T, d * (int64_t)esize(dh_dtype), dH, st);
                   }),
-            "scatter dH");
-  else if (dH && dh_dtype == CKL_BF16)
-    HIP_TRY(timed(CKL_KERNEL_OTHER, st, [&] { return ckl::launch_cast_f32_bf16(dHacc, dH, T * d, st); }), "cast dH");
-  if (dW && dw_dtype == CKL_BF16)
+            "zero masked dH");
+  if (dH && dh_parts)
+    HIP_TRY(timed(CKL_KERNEL_OTHER, st,
+                  [&] {
+                    return ckl::launch_splitk_sum(dHacc, dh_stride, (int)q.Sh, T * d, dH, dh_dtype == CKL_BF16, r.perm,
+                                                  r.n, 0, (int)d, st);
+                  }),
+            "sum dH");
+  if (dW && dw_dtype == CKL_BF16 && !dw16)
     HIP_TRY(timed(CKL_KERNEL_OTHER, st, [&] { return ckl::launch_cast_f32_bf16(dWacc, dW, V * d, st); }), "cast dW");
   return CKL_OK;
 }

@@ -61,7 +61,7 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 template <int BINS>
 struct TopkShared {
   static constexpr int bins = BINS;  // of the final order; 256 serve everything else
-  uint32_t hist[BINS];
+  __attribute__((aligned(16))) uint32_t hist[BINS];
   uint32_t wave_n[4];
   uint32_t range[2][4];
   uint32_t pending[2][4];
@@ -504,7 +504,15 @@ struct RowAcc {
       for (int i = 0; i < 8; ++i) {
         const float a = fmaf(raw.get(i), kLog2e, neg), u = fast_exp2(a);
         sum += u;
-        es = fmaf(u, fmaxf(a, kExpZero), es);
+        es = fmaf(u, a, es);
+      }
+      if (es != es) {  // (0 times an infinite a: -inf and masks of the lowest value; or a NaN)
+        es = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float a = fmaf(raw.get(i), kLog2e, neg);
+          es = fmaf(fast_exp2(a), fmaxf(a, kExpZero), es);
+        }
       }
     } else {  // masks of a large or the lowest value, infinities
 #pragma unroll

@@ -88,10 +88,13 @@ def test_workspaces(lib):  # noqa: F811
     # the forward keeps per-row arrays; a mask adds a copy of the states
     plain, masked = (size(hw, 32768, 2880, 201088, 2048, 1, 1, 0, m, 0) for m in (0, 1))
     assert plain < 4 << 20 and 32768 * 2880 * 2 <= masked - plain < 32768 * 2880 * 2 + (1 << 20)
-    # the backward holds about half of chunk x V gradients; dW in bf16 adds an fp32 one
+    # the backward holds about chunk x V gradients, W^T of a block of them, and dH and H^T besides; an fp32 dW only
+    # where there are several blocks of rows, or the inputs are fp32 and dW is bf16
     small, large = (size(hw, 32768, 2880, 201088, c, 1, 1, 0, 0, 1) for c in (512, 4096))
-    assert small < large < 32768 * 2880 * 8 + 4096 * 201088 * 2
-    assert size(hw, 2048, 2880, 201088, 2048, 1, 1, 1, 0, 1) - size(hw, 2048, 2880, 201088, 2048, 1, 1, 0, 0, 1) == 201088 * 2880 * 4
+    assert small < large < 1.1 * (32768 * 2880 * 6 + 4096 * 201088 * 2 + 201088 * 2880 * 2)
+    add = [size(hw, T, 2880, 201088, 2048, t, 1, 1, 0, 1) - size(hw, T, 2880, 201088, 2048, t, 1, 0, 0, 1)
+           for T, t in ((2048, 1), (32768, 1), (2048, 0))]
+    assert add == [0, 201088 * 2880 * 4, 201088 * 2880 * 4]
     for bad in ((4, 64, 1000, 64, 1, 1, 0, 2, 0), (4, 64, 1000, 64, 1, 1, 0, 0, 2), (4, 64, 1000, 0, 1, 1, 0, 0, 0),
                 (4, 60, 1000, 64, 1, 1, 0, 0, 0), (4, 64, 1000, 64, 3, 1, 0, 0, 0)):
         assert hw(*bad, ctypes.byref(ctypes.c_size_t())) == INV
