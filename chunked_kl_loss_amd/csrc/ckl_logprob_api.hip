@@ -41,7 +41,7 @@ LogprobWs logprob_layout(int64_t T, int64_t V, int64_t top) {
   LogprobWs w{};
   int segments = 1;
   int64_t cols = 0;
-  if (T > 0 && top > 0) ckl::topk_plan(T, V, &segments, &cols);
+  if (T > 0 && top > 0 && !ckl::logprob_in_registers(V, top)) ckl::topk_plan(T, V, &segments, &cols);
   if (segments > 1) {
     const size_t n = (size_t)T * segments;
     w.state = align256(n * ckl::topk_segment_words(top) * 8);
@@ -92,9 +92,10 @@ ckl_status head_plan(int64_t T, int64_t d, int64_t V, int64_t chunk, int32_t in_
   p.d = d;
   p.V = V;
   p.K = 1;
-  // (the plan keeps half its budget of chunk x V entries for bf16: all of it here.  2048 x 2880 over 201088 words,
-  // forward and backward, in 2 / 3 blocks: see head_grad)
-  p.chunk = chunk * (in_dtype == CKL_BF16 ? 2 : 1);
+  // (the plan takes half its budget for bf16, which keeps no transpose: all of it here, and the vocabulary's padding
+  // to whole tiles, so that a chunk of rows is one block.)
+  const int64_t bm = ckl::tile_rows_m(1);
+  p.chunk = in_dtype == CKL_BF16 && V > 0 ? ceil_div(2 * chunk * round_up(V, bm), V) : chunk;
   p.in_dtype = in_dtype;
   p.dh_dtype = dh_dtype;
   p.dw_dtype = dw_dtype;

@@ -27,8 +27,14 @@ struct TokenRows {
   float* logprob;
   float* entropy;  // (the backward pass reads it)
 };
-// top = 0: no alternatives (idx, val, cand, state and state_e unused); else as
-// launch_teacher_topk with K = top, and state_e [rows][segments].
+// Whether a row's alternatives are kept in the waves' registers (row_top_kernel); if
+// not, rows are cut as launch_teacher_topk cuts them, with cand and state as there
+// and state_e [rows][segments].  A word that comes costs a wave of the former about
+// 0.15 us, a row of the latter about 8 us.  (us, registers / buffer: 60000 x 1500 bf16,
+// top 5 / 20 / 64: 97 / 164 / 333 against 690 to 760; 8192 x 12000 bf16, top 5 / 20 / 64:
+// 81 / 99 / 154 against 122 / 122 / 127, fp32 99 / 134 / 196 against 134 to 137; 2000 x 32000
+// bf16, top 5 / 20: 40 / 57 against 46 / 50; 2048 x 201088, top 10 / 20: 179 / 199 against 170.)
+inline bool logprob_in_registers(int64_t V, int64_t top) { return V <= 2048 ? top <= 64 : V <= 16384 && top <= 24; }
 hipError_t launch_token_logprobs(const void* logits, int bf16, int64_t rows, int64_t V, int top, const TokenRows& t,
                                  float* lse, int* idx, float* val, uint64_t* cand, float2* state, float* state_e,
                                  hipStream_t st);

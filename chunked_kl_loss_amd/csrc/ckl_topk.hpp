@@ -590,6 +590,13 @@ struct Raw8<bf16_t> {
   __device__ __forceinline__ float get(int i) const {
     return (i & 1) ? __uint_as_float(a[i >> 1] & 0xffff0000u) : __uint_as_float(a[i >> 1] << 16);
   }
+  // one lane's, in all of them
+  __device__ __forceinline__ Raw8 of_lane(int lane) const {
+    Raw8 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.a[i] = (uint32_t)__builtin_amdgcn_readlane((int)a[i], lane);
+    return r;
+  }
   // (i not known at compile time)
   __device__ __forceinline__ float pick(int i) const {
     const uint32_t lo = (i & 2) ? a[1] : a[0], hi = (i & 2) ? a[3] : a[2];
@@ -610,10 +617,18 @@ struct Raw8<float> {
     a[1] = f32x4{f[4], f[5], f[6], f[7]};
   }
   __device__ __forceinline__ float get(int i) const { return a[i >> 2][i & 3]; }
+  __device__ __forceinline__ Raw8 of_lane(int lane) const {
+    Raw8 r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      r.a[i >> 2][i & 3] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(a[i >> 2][i & 3]), lane));
+    return r;
+  }
   __device__ __forceinline__ float pick(int i) const {
-    const f32x4 w = (i & 4) ? a[1] : a[0];
-    const float lo = (i & 1) ? w[1] : w[0], hi = (i & 1) ? w[3] : w[2];
-    return (i & 2) ? hi : lo;
+    const bool up = i & 4, odd = i & 1;
+    const float p = up ? a[1][0] : a[0][0], q = up ? a[1][1] : a[0][1];
+    const float r = up ? a[1][2] : a[0][2], t = up ? a[1][3] : a[0][3];
+    return (i & 2) ? (odd ? t : r) : (odd ? q : p);
   }
 };
 

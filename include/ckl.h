@@ -400,7 +400,7 @@ ckl_status ckl_norm_backward(const void* dy, int32_t dtype, int64_t T, int64_t d
  * holds a NaN gives NaN; one that holds +inf has lse +inf and entropy NaN.  Rows
  * with mask 0 are not read and give 0 (top_idx 0 .. top-1).
  * 0 <= top <= min(V, 4096), T*top < 2^31.  ws: ckl_logprob_workspace_size bytes
- * (0 for many rows or top = 0). */
+ * (0 for many rows, short rows or top = 0). */
 ckl_status ckl_logprob_workspace_size(int64_t T, int64_t V, int64_t top, size_t* bytes);
 ckl_status ckl_token_logprobs(const void* logits, int32_t dtype, int64_t T, int64_t V, const void* tokens,
                               int32_t token_bytes, int64_t top, const uint8_t* mask, float* logprob, float* entropy,

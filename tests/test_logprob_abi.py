@@ -37,9 +37,9 @@ TOKENS = [(dict(nb=2), INV), (dict(tok=P[11] + 4), INV), (dict(nb=4, tok=P[11] +
 @pytest.mark.parametrize("kw,status", TOKENS + [
     (dict(top=-1), INV), (dict(top=1001), INV), (dict(V=9000, top=4097), UNS), (dict(T=2000000, V=5000, top=4096), UNS),
     (dict(z=None), INV), (dict(lp=None), INV), (dict(lse=None), INV), (dict(idx=None), INV), (dict(val=None), INV),
-    (dict(z=P[0] + 2), INV), (dict(ws=P[8] + 8), INV), (dict(idx=P[6] + 2), INV), (dict(V=201088, ws=None), WSP),
-    (dict(V=201088, ws_bytes=16), WSP), (dict(lp=P[4]), INV), (dict(lse=P[0]), INV), (dict(idx=P[1]), INV),
-    (dict(val=P[2]), INV), (dict(V=201088, ws=P[3]), INV)])
+    (dict(z=P[0] + 2), INV), (dict(ws=P[8] + 8), INV), (dict(idx=P[6] + 2), INV), (dict(V=201088, top=100, ws=None), WSP),
+    (dict(V=201088, top=100, ws_bytes=16), WSP), (dict(lp=P[4]), INV), (dict(lse=P[0]), INV), (dict(idx=P[1]), INV),
+    (dict(val=P[2]), INV), (dict(V=201088, top=100, ws=P[3]), INV)])
 def test_token_logprobs_refusals(lib, kw, status):  # noqa: F811
     assert rows(lib, **kw) == status
     assert lib.ckl_last_error()
@@ -82,7 +82,7 @@ def test_nothing_to_do(lib):  # noqa: F811
 
 def test_workspaces(lib):  # noqa: F811
     ws = lib.ckl_logprob_workspace_size
-    assert size(ws, 1, 201088, 0) == 0 and size(ws, 4096, 201088, 20) == 0 and 0 < size(ws, 1, 201088, 20) < 1 << 20
+    assert size(ws, 1, 201088, 0) == 0 and size(ws, 1, 2048, 64) == 0 and size(ws, 4096, 201088, 100) == 0 and 0 < size(ws, 1, 201088, 100) < 1 << 20
     assert ws(1, 10, 11, ctypes.byref(ctypes.c_size_t())) == INV and ws(1, 10, 1, None) == INV
     hw = lib.ckl_head_workspace_size
     # the forward keeps per-row arrays; a mask adds a copy of the states

@@ -130,7 +130,8 @@ def some_tokens(T, V, seed, kind=torch.int64):
 @pytest.mark.parametrize("T,V,top", [(1, 1, 1), (1, 1, 0), (2, 2, 1), (1, 7, 7), (3, 9, 0), (3, 33, 5), (5, 2041, 0),
                                      (5, 2048, 1), (5, 2049, 20), (2, 8185, 0), (2, 8193, 3), (7, 4099, 1),
                                      (2, 50021, 1000), (1, 201088, 20), (3, 201088, 0), (1, 120001, 4096),
-                                     (1100, 301, 17), (2100, 303, 0), (1030, 9000, 1025), (600, 5003, 0)])
+                                     (1100, 301, 17), (2100, 303, 0), (1030, 9000, 1025), (600, 5003, 0),
+                                     (3, 64, 64), (9, 5003, 64), (9, 5003, 65), (9, 2047, 64), (9, 16385, 7), (2, 201088, 64), (2, 201088, 200)])
 def test_sizes(T, V, top, dtype):
     z = normal((T, V), DT[dtype], 7 * T + V, 3.0)
     tok = some_tokens(T, V, V, torch.int32 if T % 2 else torch.int64)
@@ -227,6 +228,27 @@ def test_order_of_the_columns(rising):
     z = torch.linspace(0, 90, V)[None].repeat(3, 1)
     z = z if rising else z.flip(1)
     check(z.contiguous(), torch.tensor([0, V // 2, V - 1]), 7)
+
+
+@pytest.mark.parametrize("top", [1, 12, 13, 64, 70])
+@pytest.mark.parametrize("T", [2, 1100])
+@pytest.mark.parametrize("kind", ["equal", "few", "rising", "falling", "zeros", "comb"])
+def test_ties_and_orders(kind, T, top):
+    V = 5001
+    if kind == "equal":
+        z = torch.full((T, V), 1.25)
+    elif kind == "few":
+        z = torch.randint(0, 4, (T, V), generator=gen(5)).float()
+    elif kind == "zeros":  # -0 and +0 are one value
+        z = torch.where(torch.rand(T, V, generator=gen(6)) < 0.5, -0.0, 0.0)
+        z[:, 4000] = 1.0
+    elif kind == "comb":  # a few lanes hold all that is wanted
+        z = torch.zeros(T, V)
+        z[:, ::512] = 3.0 + torch.arange(len(range(0, V, 512))) / 8
+    else:
+        z = torch.arange(V, dtype=torch.float32).expand(T, V) / 64
+        z = z if kind == "rising" else z.flip(1)
+    check(z.contiguous(), some_tokens(T, V, 1), top, train=False)
 
 
 def test_sure_and_diffuse_rows():
@@ -397,7 +419,7 @@ def test_neighbours_stay_untouched():
 
     from chunked_kl_loss_amd import _binding as B
     lib = B.load_library()
-    for T, V, top, dt in ((3, 20001, 5, torch.float32), (9, 333, 5, torch.bfloat16), (5, 1001, 0, torch.float32)):
+    for T, V, top, dt in ((3, 20001, 5, torch.float32), (3, 20001, 70, torch.float32), (9, 333, 5, torch.bfloat16), (5, 1001, 0, torch.float32)):
         z, tok = normal((T, V), dt, 1).cuda(), some_tokens(T, V, 2).cuda()
         code = int(dt == torch.bfloat16)
         rows = [torch.full((T + 64,), -7.0, device="cuda") for _ in range(3)]
