@@ -13,6 +13,7 @@
 #include <type_traits>
 
 #include "ckl_tile.hpp"
+#include "ckl_vec.hpp"
 
 namespace ckl {
 
@@ -240,16 +241,107 @@ __global__ __launch_bounds__(256) void head_consts_kernel(HeadRows rows, int T, 
   tok[i] = c;
 }
 
+// The rows by the 64 words that hold their token, in their order: a workgroup lists
+// four such groups, behind the number of rows whose token lies below them (2048 rows
+// are 8 KB, read by every workgroup from the caches).
+__global__ __launch_bounds__(256) void head_buckets_kernel(const int* __restrict__ tok, int T,
+                                                           const int* __restrict__ n, int* __restrict__ order,
+                                                           int* __restrict__ start) {
+  __shared__ int counts[5][4], mine[2][4][4];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int v0 = blockIdx.x * 256;
+  if (n != nullptr) T = min(T, *n);
+  int sum[5] = {};  // rows below the four groups, in the first, ..
+  for (int i = threadIdx.x; i < T; i += 256) {
+    const int c = tok[i], g = (c - v0) >> 6;
+    sum[0] += c >= 0 && c < v0 ? 1 : 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) sum[k + 1] += c >= v0 && g == k ? 1 : 0;
+  }
+#pragma unroll
+  for (int k = 0; k < 5; ++k) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) sum[k] += __shfl_xor(sum[k], o);
+    if (lane == 0) counts[k][wave] = sum[k];
+  }
+  __syncthreads();
+  int at[4], all = 0;
+#pragma unroll
+  for (int k = 0; k < 5; ++k) {
+    all += counts[k][0] + counts[k][1] + counts[k][2] + counts[k][3];
+    if (k < 4) at[k] = all;
+  }
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) start[blockIdx.x * 4 + k] = at[k];
+    if (blockIdx.x == gridDim.x - 1) start[gridDim.x * 4] = all;
+  }
+  if (all == at[0]) return;  // no row's token is here
+  int side = 0;
+  for (int i0 = 0; i0 < T; i0 += 256) {
+    const int i = i0 + threadIdx.x;
+    const int c = i < T ? tok[i] : -1;
+    const int g = c >= v0 && c < v0 + 256 ? (c - v0) >> 6 : -1;
+    uint64_t who[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      who[k] = __ballot(g == k);
+      if (lane == 0) mine[side][k][wave] = __popcll(who[k]);
+    }
+    __syncthreads();  // (the other side is written only after everyone has passed the next barrier)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      int p = at[k] + __popcll(who[k] & ((1ull << lane) - 1));
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        p += w < wave ? mine[side][k][w] : 0;
+        at[k] += mine[side][k][w];
+      }
+      if (g == k) order[p] = i;
+    }
+    side ^= 1;
+  }
+}
+
+// dH from its parts and the tokens' entries, eight columns a thread.
+template <typename TOut>
+__global__ __launch_bounds__(256) void head_dh_kernel(const float* __restrict__ part, int64_t stride, int S, int T,
+                                                      int nv, const int* __restrict__ tok,
+                                                      const float* __restrict__ gtok, const bf16_t* __restrict__ W,
+                                                      HeadRows rows, TOut* __restrict__ dH) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int r = (int)(i / nv), c = (int)(i - (int64_t)r * nv);
+  if (r >= (rows.n != nullptr ? min(T, *rows.n) : T)) return;
+  const int t = rows.perm != nullptr ? rows.perm[r] : r, k = tok[r];
+  float a[8], b[8];
+  load8(part + i * 8, a);
+#pragma unroll 4
+  for (int s = 1; s < S; ++s) {
+    load8(part + s * stride + i * 8, b);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a[j] += b[j];
+  }
+  if (k >= 0) {
+    const float g = gtok[r];
+    load8(W + ((int64_t)k * nv + c) * 8, b);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a[j] = fmaf(g, b[j], a[j]);
+  }
+  store8(dH + ((int64_t)t * nv + c) * 8, a);
+}
+
 // The G block of rows [tb0, tb0 + BN n_tblocks) and columns [vb0, vb0 + BM
 // n_vtiles): G[t - tb0][v - vb0], and for fp32 also its transpose Gt.  bf16 rounds
-// G once (its contractions read bf16 operands; 2^-9 of each entry, like the
-// operands themselves); rows past T and columns past V get 0.  Tiles leave through
+// G once, to what the contractions read, but for each row's largest entry as a rule,
+// its token's: that one stays in fp32 (gtok[t], 0 in G) and is added to dH and dW as
+// gtok W[token] and gtok H[t], so that its rounding, which a whole row of dH would
+// share, does not come on top of theirs.  Rows past T and columns past V get 0.  Tiles leave through
 // the LDS as 512-byte runs of G's rows, behind the issue of the next tile's first
 // slices.
 template <class C>
 __global__ __launch_bounds__(C::NTHREADS) void head_grad_kernel(
     const typename C::TIn* __restrict__ H, const typename C::TIn* __restrict__ W, int T, int d, int V,
-    const float4* __restrict__ consts, const int* __restrict__ tok, int tb0, int vb0, int n_vtiles,
+    const float4* __restrict__ consts, const int* __restrict__ tok, float* __restrict__ gtok, int tb0, int vb0, int n_vtiles,
     int tiles_per_split, int n_tblocks, int n_splits, typename C::TIn* __restrict__ G, int64_t ldG,
     typename C::TIn* __restrict__ Gt, int64_t ldGt, const int* __restrict__ nrows) {
   using TIn = typename C::TIn;
@@ -314,7 +406,11 @@ __global__ __launch_bounds__(C::NTHREADS) void head_grad_kernel(
         const int sel = (vl >> 5) * 16 + ((vl & 31) >> 3) * 4 + (vl & 3);
 #pragma unroll
         for (int q = 0; q < C::MB * 16; ++q)
-          if (q == sel) tile.acc[q / 16][nb][q % 16] += rc.w;
+          if (q == sel) {
+            const float g = tile.acc[q / 16][nb][q % 16] + rc.w;
+            tile.acc[q / 16][nb][q % 16] = kStage ? 0.f : g;
+            if (kStage) gtok[t0 + tl] = g;
+          }
       }
       if constexpr (kStage) {
         uint2* row = reinterpret_cast<uint2*>(stg + tl * 256);
@@ -435,15 +531,32 @@ hipError_t launch_head_consts(const HeadRows& rows, int T, int Tp, int V, const 
   return hipSuccess;
 }
 
+hipError_t launch_head_buckets(const int* tok, int T, const int* n, int tiles, int* order, int* start, hipStream_t st) {
+  head_buckets_kernel<<<tiles, 256, 0, st>>>(tok, T, n, order, start);
+  CKL_LAUNCH_CHECK();
+  return hipSuccess;
+}
+
+hipError_t launch_head_dh(const float* part, int64_t stride, int S, int T, int d, const int* tok, const float* gtok,
+                          const void* W, const HeadRows& rows, void* dH, int dh_bf16, hipStream_t st) {
+  const unsigned blocks = (unsigned)(((int64_t)T * (d / 8) + 255) / 256);
+  if (dh_bf16)
+    head_dh_kernel<<<blocks, 256, 0, st>>>(part, stride, S, T, d / 8, tok, gtok, (const bf16_t*)W, rows, (bf16_t*)dH);
+  else
+    head_dh_kernel<<<blocks, 256, 0, st>>>(part, stride, S, T, d / 8, tok, gtok, (const bf16_t*)W, rows, (float*)dH);
+  CKL_LAUNCH_CHECK();
+  return hipSuccess;
+}
+
 hipError_t launch_head_grad(int in_bf16, const void* H, const void* W, int T, int d, int V, const float4* consts,
-                            const int* tok, int tb0, int t_rows, int vb0, int v_rows, int tiles_per_split, void* G,
+                            const int* tok, float* gtok, int tb0, int t_rows, int vb0, int v_rows, int tiles_per_split, void* G,
                             int64_t ldG, void* Gt, int64_t ldGt, const int* nrows, hipStream_t st) {
   auto go = [&](auto cfg, int tps) {
     using C = decltype(cfg);
     using TIn = typename C::TIn;
     const int n_vtiles = v_rows / C::BM, n_tblocks = t_rows / C::BN, splits = (n_vtiles + tps - 1) / tps;
     head_grad_kernel<C><<<n_tblocks * splits, C::NTHREADS, 0, st>>>(
-        (const TIn*)H, (const TIn*)W, T, d, V, consts, tok, tb0, vb0, n_vtiles, tps, n_tblocks, splits, (TIn*)G, ldG,
+        (const TIn*)H, (const TIn*)W, T, d, V, consts, tok, gtok, tb0, vb0, n_vtiles, tps, n_tblocks, splits, (TIn*)G, ldG,
         (TIn*)Gt, ldGt, nrows);
   };
   // (fp32 tiles that would not fill the compute units: halves of them)

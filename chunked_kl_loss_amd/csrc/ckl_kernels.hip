@@ -1303,7 +1303,8 @@ struct GemmProblem {
   // (kdim rounded up to lim_round, the rows of whole G tiles)
   const int* lim;
   int lim_base, lim_kind, lim_round;
-  bf16_t* out16;  // (B16) not NULL: the sum rounded to bf16 goes here, with out's stride; out is read only
+  bf16_t* out16;  // (MORE) not NULL: the sum rounded to bf16 goes here, with out's stride; out is read only
+  GemmRows rows;  // (MORE) rows added to the second problem's sums
 };
 
 constexpr int kGroupM = 2;
@@ -1314,8 +1315,9 @@ constexpr bool kXtOK = false;
 template <int BM, int BN, int WM, int WN>
 constexpr bool kXtOK<Dma64Cfg<BM, BN, WM, WN>> = BM % 128 == 0;
 
-// B16: results may leave in bf16 (GemmProblem::out16).
-template <class C, bool B16 = false>
+// MORE: results may leave in bf16 (GemmProblem::out16), and rows be added to them
+// (GemmProblem::rows).
+template <class C, bool MORE = false>
 __global__ __launch_bounds__(C::NTHREADS) void gemm_store_kernel(GemmProblem<typename C::TIn> p0,
                                                                  GemmProblem<typename C::TIn> p1) {
   // bf16 configurations stage the fp32 output through LDS one wave row block
@@ -1379,10 +1381,17 @@ __global__ __launch_bounds__(C::NTHREADS) void gemm_store_kernel(GemmProblem<typ
         const int kl = n_lim <= 0 ? 0 : (n_lim + rnd - 1) / rnd * rnd;
         kdim = min(kdim, kl);
         if (kdim <= 0 && beta) {
-          if constexpr (!B16) return;
+          if constexpr (!MORE) return;
           if ((second ? p1.out16 : p0.out16) == nullptr) return;  // (else the old sums still have to be rounded)
         }
       }
+    }
+  }
+  int row_start[MORE ? C::WAVES_M + 1 : 1] = {};  // (fetched under the main loop)
+  if constexpr (MORE) {
+    if (second && p1.rows.order != nullptr) {
+#pragma unroll
+      for (int i = 0; i <= C::WAVES_M; ++i) row_start[i] = p1.rows.start[(p1.rows.col0 + m0) / 64 + i];
     }
   }
   using TileT = typename C::TileT;
@@ -1450,12 +1459,41 @@ __global__ __launch_bounds__(C::NTHREADS) void gemm_store_kernel(GemmProblem<typ
           }
           wait_vmcnt<0>();
           __syncthreads();
+          if constexpr (MORE) {
+            if (second && p1.rows.order != nullptr) {
+              // a thread takes one column of every row that falls in this part, in the list's order
+              const GemmRows& q = p1.rows;
+              const int v0 = q.col0 + m0 + part * PART, e1 = row_start[part + 1];
+              const int c = threadIdx.x;
+              bool any = false;
+              for (int e0 = row_start[part]; e0 < e1; e0 += 8) {
+                int to[8];
+                float x[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {  // (eight rows' loads under way together)
+                  const int i = e0 + j < e1 ? q.order[e0 + j] : -1;
+                  const int ml = i >= 0 ? q.col[i] - v0 : -1;
+                  const bool here = i >= q.lo && i < q.hi;
+                  to[j] = here ? ml : -1;
+                  x[j] = here && c < C::BN && n0 + c < N
+                             ? q.scale[i] * (float)reinterpret_cast<const bf16_t*>(q.rows)[(int64_t)i * N + n0 + c]
+                             : 0.f;
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                  any |= to[j] >= 0;
+                  if (to[j] >= 0 && c < C::BN) st[to[j] * C::BN + (c ^ stage_swz(to[j]))] += x[j];
+                }
+              }
+              if (any) __syncthreads();
+            }
+          }
           for (int i = threadIdx.x; i < PART * CPR; i += C::NTHREADS) {
             const int ml = i / CPR, c4 = (i % CPR) * 4;
             const int m = r0 + ml, n = n0 + c4;
             if (m >= M_eff || n >= N) continue;
             const f32x4 a = *reinterpret_cast<const f32x4*>(st + ml * C::BN + (c4 ^ stage_swz(ml)));
-            if constexpr (B16) {
+            if constexpr (MORE) {
               bf16_t* o16 = second ? p1.out16 : p0.out16;
               if (o16 != nullptr) {  // (N and ldo are multiples of 4)
                 const f32x4 r = beta ? a + *reinterpret_cast<const f32x4*>(oldb + i * 4) : a;
@@ -1806,9 +1844,14 @@ static hipError_t gemm_pair_t(const GemmArgs& a0, const GemmArgs& a1, hipStream_
     p[i].lim_kind = a[i]->lim ? a[i]->lim_kind : 0;
     p[i].lim_round = a[i]->lim_round > 0 ? a[i]->lim_round : 1;
     p[i].out16 = (bf16_t*)a[i]->out16;
-    // (the path that writes it: 16-byte rows of sums, whole vectors)
-    if (a[i]->out16 && (sizeof(TIn) != 2 || a[i]->batches > 1 || a[i]->N % 4 || a[i]->ldo % 4 ||
-                        ((uintptr_t)a[i]->out & 15) || ((uintptr_t)a[i]->out16 & 7)))
+    p[i].rows = a[i]->rows;
+    // (the path that does so: 16-byte rows of sums, whole vectors)
+    if ((a[i]->out16 || a[i]->rows.order) &&
+        (sizeof(TIn) != 2 || a[i]->batches > 1 || a[i]->N % 4 || a[i]->ldo % 4 || ((uintptr_t)a[i]->out & 15) ||
+         ((uintptr_t)a[i]->out16 & 7)))
+      return hipErrorInvalidValue;
+    if (a[i]->rows.order &&
+        (i != 1 || C::BM != 256 || C::WM != 64 || C::BN > C::NTHREADS || a[i]->rows.col0 % 256))
       return hipErrorInvalidValue;
     if (a[i]->lim && (a[i]->lim_kind < 1 || a[i]->lim_kind > 2 || (a[i]->lim_kind == 2 && a[i]->lim_round % 8)))
       return hipErrorInvalidValue;
@@ -1821,7 +1864,7 @@ static hipError_t gemm_pair_t(const GemmArgs& a0, const GemmArgs& a1, hipStream_
   if (p[0].tiles + p[1].tiles == 0) return hipSuccess;
   const int n = (p[0].tiles + kNumXcd - 1) / kNumXcd * kNumXcd + p[1].tiles;
   if constexpr (sizeof(TIn) == 2) {
-    if (p[0].out16 || p[1].out16) {
+    if (p[0].out16 || p[1].out16 || p[1].rows.order) {
       hipLaunchKernelGGL((gemm_store_kernel<C, true>), dim3(n), dim3(C::NTHREADS), 0, st, p[0], p[1]);
       CKL_LAUNCH_CHECK();
       return hipSuccess;

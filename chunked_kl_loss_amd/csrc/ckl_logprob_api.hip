@@ -164,7 +164,7 @@ HeadFwdWs head_fwd_layout(const HeadPlan& q, bool masked) {
   return w;
 }
 struct HeadBwdWs {
-  size_t consts, tok, Ht, Wt, G, Gt, dH, dW, total;
+  size_t consts, tok, gtok, order, start, Ht, Wt, G, Gt, dH, dW, total;
   PackWs pk;
 };
 HeadBwdWs head_bwd_layout(const HeadPlan& q, bool masked, int32_t dh_dtype, int32_t dw_dtype) {
@@ -172,11 +172,16 @@ HeadBwdWs head_bwd_layout(const HeadPlan& q, bool masked, int32_t dh_dtype, int3
   Layout l;
   w.consts = l.take(q.Tp * 16);
   w.tok = l.take(q.Tp * 4);
+  if (q.bf16) {
+    w.gtok = l.take(q.Tp * 4);
+    w.order = l.take(q.Tp * 4);
+    w.start = l.take((q.Vp / 64 + 1) * 4);
+  }
   w.Ht = l.take((size_t)q.d * (q.Tp + kLdPad) * q.esz);
   w.Wt = l.take((size_t)q.d * (q.Vc + kLdPad) * q.esz);
   w.G = l.take((size_t)q.Tc * (q.Vc + kLdPad) * q.esz);
   w.Gt = q.bf16 ? 0 : l.take((size_t)q.Vc * (q.Tc + kLdPad) * q.esz);
-  w.dH = dh_dtype == CKL_BF16 || masked || q.Sh > 1 ? l.take((size_t)q.Sh * q.T * q.d * 4) : 0;
+  w.dH = q.bf16 || dh_dtype == CKL_BF16 || masked || q.Sh > 1 ? l.take((size_t)q.Sh * q.T * q.d * 4) : 0;
   // fp32 sums of a bf16 dW (bf16 inputs: needed only between blocks of rows)
   w.dW = dw_dtype == CKL_BF16 && (!q.bf16 || q.nT > 1) ? l.take((size_t)q.V * q.d * 4) : 0;
   if (masked) w.pk = pack_layout(q, &l);
@@ -378,6 +383,8 @@ ckl_status ckl_head_logprobs_backward(const void* H, const void* W, int32_t in_d
   char* b = (char*)ws;
   float4* consts = (float4*)(b + w.consts);
   int* tok = (int*)(b + w.tok);
+  float* gtok = (float*)(b + w.gtok);  // (bf16)
+  int *order = (int*)(b + w.order), *start = (int*)(b + w.start);
   char* Ht = b + w.Ht;
   void* Wt = b + w.Wt;
   void* G = b + w.G;
@@ -386,7 +393,7 @@ ckl_status ckl_head_logprobs_backward(const void* H, const void* W, int32_t in_d
   const void* Hs = H;
   if (mask) HIP_TRY(head_pack(q, b, w.pk, mask, &Hs, &r, st), "packing kept rows");
   // fp32 sums in the outputs themselves, or in the workspace where the output is bf16 or its rows are packed
-  const bool dh_parts = dh_dtype == CKL_BF16 || mask || q.Sh > 1;
+  const bool dh_parts = q.bf16 || dh_dtype == CKL_BF16 || mask || q.Sh > 1;
   float* dHacc = dh_parts ? (float*)(b + w.dH) : (float*)dH;
   const int64_t dh_stride = T * d;
   // bf16 inputs and dW: the last block of rows writes the rounded sums
@@ -398,6 +405,12 @@ ckl_status ckl_head_logprobs_backward(const void* H, const void* W, int32_t in_d
                                                  tok, st);
                 }),
           "head_consts");
+  if (dW && q.bf16)
+    HIP_TRY(timed(CKL_KERNEL_OTHER, st,
+                  [&] {
+                    return ckl::launch_head_buckets(tok, (int)T, r.n, (int)(q.Vp / 256), order, start, st);
+                  }),
+            "head_buckets");
   if (dW)
     HIP_TRY(timed(CKL_KERNEL_TRANSPOSE, st,
                   [&] {
@@ -420,7 +433,7 @@ ckl_status ckl_head_logprobs_backward(const void* H, const void* W, int32_t in_d
       pick_splits(trows / q.BN, vrows / q.BM, kGradSlots, &splits, &tps);
       HIP_TRY(timed(CKL_KERNEL_BWD_GRAD, st,
                     [&] {
-                      return ckl::launch_head_grad(q.bf16, Hs, W, (int)T, (int)d, (int)V, consts, tok, (int)tb0,
+                      return ckl::launch_head_grad(q.bf16, Hs, W, (int)T, (int)d, (int)V, consts, tok, gtok, (int)tb0,
                                                    (int)trows, (int)vb0, (int)vrows, (int)tps, G,
                                                    vrows + kLdPad, Gt, trows + kLdPad, r.n, st);
                     }),
@@ -438,6 +451,16 @@ ckl_status ckl_head_logprobs_backward(const void* H, const void* W, int32_t in_d
                         (int)trows, tb > 0};
       gdw.xt = q.bf16;
       if (dW && dw16 && tb == q.nT - 1) gdw.out16 = (char*)dW + vb0 * d * 2;
+      if (dW && q.bf16) {
+        gdw.rows.order = order;
+        gdw.rows.start = start;
+        gdw.rows.col = tok;
+        gdw.rows.scale = gtok;
+        gdw.rows.rows = Hs;
+        gdw.rows.col0 = (int)vb0;
+        gdw.rows.lo = (int)tb0;
+        gdw.rows.hi = (int)std::min(tb0 + trows, T);
+      }
       if (r.n) {
         gdw.lim = gdh.lim = r.n;
         gdw.lim_base = gdh.lim_base = (int)tb0;
@@ -455,7 +478,14 @@ ckl_status ckl_head_logprobs_backward(const void* H, const void* W, int32_t in_d
                     return ckl::launch_zero_masked_rows(r.rank, (int)T, d * (int64_t)esize(dh_dtype), dH, st);
                   }),
             "zero masked dH");
-  if (dH && dh_parts)
+  if (dH && q.bf16)
+    HIP_TRY(timed(CKL_KERNEL_OTHER, st,
+                  [&] {
+                    return ckl::launch_head_dh(dHacc, dh_stride, (int)q.Sh, (int)T, (int)d, tok, gtok, W, r, dH,
+                                               dh_dtype == CKL_BF16, st);
+                  }),
+            "sum dH");
+  else if (dH && dh_parts)
     HIP_TRY(timed(CKL_KERNEL_OTHER, st,
                   [&] {
                     return ckl::launch_splitk_sum(dHacc, dh_stride, (int)q.Sh, T * d, dH, dh_dtype == CKL_BF16, r.perm,

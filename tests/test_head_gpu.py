@@ -296,3 +296,32 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for g, w in zip(got, want):
         assert all(same_bits(a, b) for a, b in zip(g[1:], w[1:]))
+
+
+@pytest.mark.parametrize("kind", ["one", "two", "rising"])
+def test_tokens_that_repeat(kind):
+    # many rows of one token: their states are added to one row of dW in a fixed order
+    T, V = 1300, 900
+    H, W, tok = inputs(T, 72, V, torch.bfloat16, 5)
+    tok = {"one": torch.full((T,), 511), "two": torch.where(torch.arange(T) % 3 == 0, 256, 255),
+           "rising": torch.arange(T) % V}[kind]
+    check(H, W, tok, chunk=512)
+    got = [ckl.head_logprobs_backward(normal((T,), torch.float32, 1).cuda(), None, H.cuda(), W.cuda(), tok.cuda(),
+                                      *ckl.head_logprobs_forward(H.cuda(), W.cuda(), tok.cuda())[2:0:-1]) for _ in range(2)]
+    assert same_bits(got[0][0], got[1][0]) and same_bits(got[0][1], got[1][1])
+
+
+def test_gradients_lose_no_more_than_their_outputs_rounding():
+    # a row's token has its largest entry of G as a rule; in bf16 it would cost dH and dW as much again as their rounding
+    T, d, V = 400, 256, 3001
+    H, W, tok = normal((T, d), torch.bfloat16, 1), normal((V, d), torch.bfloat16, 2, d ** -0.5), some_tokens(T, V, 3)
+    a = normal((T,), torch.float32, 4)
+    Hg, Wg = H.cuda().requires_grad_(True), W.cuda().requires_grad_(True)
+    lp, _ = ckl.head_logprobs(Hg, Wg, tok.cuda())
+    got = torch.autograd.grad(lp, (Hg, Wg), a.cuda())
+    q = torch.softmax(H.double() @ W.double().t(), 1)
+    G = -q * a.double()[:, None]
+    G[torch.arange(T), tok] += a.double()
+    for g, w in zip(got, (G @ W.double(), G.t() @ H.double())):
+        off = float((g.double().cpu() - w).norm()), float((w.to(torch.bfloat16).double() - w).norm())
+        assert off[0] < 1.1 * off[1]
