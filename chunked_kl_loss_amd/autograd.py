@@ -29,6 +29,20 @@ from torch.autograd.function import once_differentiable
 from . import _binding, ops
 
 
+def _differentiable_once(backward):
+    """once_differentiable without its steps where no graph of the backward pass is recorded; where one is, whoever
+    differentiates the gradients gets its error, also where only the inputs and not the incoming gradients depend on
+    a leaf (as the decorator by itself does not see)."""
+    guarded = once_differentiable(backward)
+
+    def run(ctx, *grads):
+        if not torch.is_grad_enabled():
+            return backward(ctx, *grads)
+        return guarded(ctx, *(g.detach().requires_grad_() if torch.is_tensor(g) and g.is_floating_point() else g
+                              for g in grads))
+    return run
+
+
 class ChunkedKLLoss(torch.autograd.Function):
     @staticmethod
     def forward(ctx, H, W, idx, tlogit, mask=None, chunk: int = 2048, teacher_form: int = 0):
@@ -162,7 +176,7 @@ class TokenLogprobs(torch.autograd.Function):
         return logprob, entropy, top_idx, top_logprob
 
     @staticmethod
-    @once_differentiable
+    @_differentiable_once
     def backward(ctx, dlogprob, dentropy, _idx, _top):
         if dlogprob is None and dentropy is None:
             return None, None, None, None
@@ -181,7 +195,7 @@ class HeadLogprobs(torch.autograd.Function):
         return logprob, entropy
 
     @staticmethod
-    @once_differentiable
+    @_differentiable_once
     def backward(ctx, dlogprob, dentropy):
         if dlogprob is None and dentropy is None:
             return None, None, None, None, None
@@ -195,50 +209,39 @@ class HeadLogprobs(torch.autograd.Function):
 class Dropout(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, p, seed, offset):
-        ctx.p, ctx.offset = p, offset
-        ctx.seed, state = _saved_seed(seed)
-        ctx.save_for_backward(state)
+        # (a tensor is kept as it is now: the caller's may move on before the backward pass runs)
+        ctx.drop = p, seed.clone() if isinstance(seed, torch.Tensor) else seed, offset
         return ops.dropout_forward(x, p, seed, offset)
 
     @staticmethod
-    @once_differentiable
-    def backward(ctx, grad):
-        (state,) = ctx.saved_tensors
-        return ops.dropout_forward(grad.contiguous(), ctx.p, ctx.seed if state is None else state, ctx.offset), \
-            None, None, None
+    def backward(ctx, grad):  # (linear in grad, and so differentiable again)
+        return dropout(grad, *ctx.drop), None, None, None
 
 
 class AddRMSNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, residual, weight, eps, p, seed, offset):
         y, h, rstd = ops.add_norm_forward(x, residual, weight, eps, p, seed, offset)
-        ctx.p, ctx.offset, ctx.x_dtype = p, offset, x.dtype
-        ctx.seed, state = _saved_seed(seed) if p else (0, None)
-        ctx.save_for_backward(h, rstd, weight, state)
+        ctx.x_dtype = x.dtype
+        ctx.drop = p, seed.clone() if p and isinstance(seed, torch.Tensor) else seed, offset
+        ctx.save_for_backward(h, rstd, weight)
         ctx.set_materialize_grads(False)
         return y, h
 
     @staticmethod
-    @once_differentiable
+    @_differentiable_once
     def backward(ctx, dy, dh):
-        h, rstd, weight, state = ctx.saved_tensors
         if dy is None and dh is None:
             return None, None, None, None, None, None, None
+        h, rstd, weight = ctx.saved_tensors
         if dy is None:  # the norm's output was not used
             dy = torch.zeros_like(h, dtype=ctx.x_dtype)
-        dx, dresidual, dweight = ops.add_norm_backward(dy.contiguous(), _contiguous(dh), h, rstd, weight, ctx.p,
-                                                       ctx.seed if state is None else state, ctx.offset)
+        dx, dresidual, dweight = ops.add_norm_backward(dy.contiguous(), _contiguous(dh), h, rstd, weight, *ctx.drop)
         return dx, dresidual, dweight, None, None, None, None
 
 
 def _contiguous(t):
     return None if t is None else t.contiguous()
-
-
-def _saved_seed(seed):
-    """(seed, state) to keep for a backward pass: an integer, or a copy of the tensor as it is now (the caller's may
-    move on before the backward pass runs)."""
-    return (0, seed.clone()) if isinstance(seed, torch.Tensor) else (seed, None)
 
 
 def _needs_function(requires_grad: bool) -> bool:

@@ -202,7 +202,9 @@ __global__ __launch_bounds__(1024) void add_norm_kernel(const TX* __restrict__ x
     for (int i = 0; i < 8; ++i) ss += f[k][i] * f[k][i];
   }
   ss = row_sum<WAVE>(ss, row_threads, slots);
-  float r = 1.f / sqrtf(ss / (float)(nv * 8) + eps);
+  // (8 bits: roundings of r move values across the borders of codes, so there it has one)
+  float r = OUT == kOutRows ? 1.f / sqrtf(ss / (float)(nv * 8) + eps)
+                            : (float)(1.0 / sqrt((double)ss / (nv * 8) + (double)eps));
   if (ss == INFINITY) {
     // the squares' sum is past fp32 (values near 1e19 and more), or the row holds an infinity: once more with h 2^-96,
     // beside which eps is nothing
@@ -257,7 +259,11 @@ __global__ __launch_bounds__(1024) void add_norm_kernel(const TX* __restrict__ x
       if (live && v < nv) {
         float q[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = bad ? 0.f : fminf(fmaxf(f[k][i] * inv, -448.f), 448.f);
+        for (int i = 0; i < 8; ++i) {
+          q[i] = f[k][i] * inv;
+          q[i] = fmaf(fmaf(-q[i], scale, f[k][i]), inv, q[i]);  // the quotient, rounded once
+          q[i] = bad ? 0.f : fminf(fmaxf(q[i], -448.f), 448.f);
+        }
         __builtin_nontemporal_store(pack_e4m3(q), reinterpret_cast<u32x2*>((uint8_t*)out.y + (row * nv + v) * 8));
       }
     }

@@ -233,17 +233,45 @@ def test_add_norm_quant(T, d, types):
     res[T // 2, d // 2] = 90.0  # a column that stands out
     w = (1 + normal((d,), torch.float32, d, 0.2)).cuda()
     _, want_h = ckl.add_rms_norm(x, res, w)
-    # the same norm with its output in fp32: h as the residual, nothing added
-    y, _ = ckl.add_rms_norm(torch.zeros(T, d, device="cuda"), want_h.float(), w)
     codes, scales, h = ckl.add_norm_quant(x, res, w, form="int8")
-    want_codes, want_scales = ckl.act_encode(y)
-    assert same_bits(h, want_h) and same_bits(codes, want_codes) and same_bits(scales, want_scales)
+    assert same_bits(h, want_h)
+    hd = h.double().cpu()
+    y = hd / torch.sqrt((hd * hd).mean(1, keepdim=True) + 1e-6) * w.double().cpu()
+    # y before its coding: half of the sum of squares' d + 4 roundings and four more; a code is within half a step
+    rel = (d + 4) * EPS / 2 + 4 * EPS
+    held = ckl.act_decode(codes, scales, dtype=torch.float32).double().cpu()
+    blocks = torch.nn.functional.pad(y, (0, -d % 32)).view(T, -1, 32).abs().amax(2, keepdim=True)
+    step = torch.exp2(torch.floor(torch.log2(blocks * (1 + 2 * rel) / 127.5)) + 1).expand(-1, -1, 32).reshape(T, -1)[:, :d]
+    assert ((held - y).abs() <= step / 2 + rel * y.abs()).all()
+    near = torch.exp2(torch.floor(torch.log2(blocks / 127.5)) + 1 + 127)[:, :, 0]
+    border = (torch.log2(blocks / 127.5) - torch.log2(blocks / 127.5).round()).abs()[:, :, 0] < 2 * rel
+    assert ((scales.cpu().double() == torch.log2(near)) | border).all()  # the smallest power of two that will do
     codes, scales, h = ckl.add_norm_quant(x, res, w, form="e4m3")
-    y = y.cpu()
-    want_scales = y.abs().amax(1) / 448
-    q = (y * (1 / want_scales)[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn)
-    assert same_bits(h, want_h) and same_bits(scales.cpu(), want_scales) and same_bits(codes.cpu(), q)
-    assert codes.dtype == torch.float8_e4m3fn and float(codes.float().abs().max()) == 448.0
+    assert same_bits(h, want_h) and codes.dtype == torch.float8_e4m3fn
+    top = y.abs().amax(1)
+    assert ((scales.double().cpu() - top / 448).abs() <= top / 448 * (rel + EPS)).all()
+    c = codes.cpu().double()
+    q = y / scales.double().cpu()[:, None]
+    # three bits behind the first: half a step is 2^-4 of the power of two below, at least half of 2^-9
+    half = torch.exp2(torch.floor(torch.log2(q.abs().clamp(min=2.0 ** -6))) - 4)
+    assert ((c - q).abs() <= half + (rel + 2 * EPS) * q.abs()).all() and (c.abs().amax(1) == 448).all()
+
+
+def test_codes_are_those_of_the_rounded_quotients():
+    # values that are exact through the norm: h of one magnitude a row, the weight shapes it
+    T, d = 64, 64
+    h = torch.where(torch.rand(T, d, generator=torch.Generator().manual_seed(1)) < 0.5, -1.0, 1.0)
+    h = h * torch.exp2(torch.randint(-20, 20, (T, 1)).float())
+    w = normal((d,), torch.float32, 2)
+    # r = 1 / |h| is a power of two: y = +-w exactly
+    zero = torch.zeros(T, d).cuda()
+    codes, scales, _ = ckl.add_norm_quant(zero, h.cuda(), w.cuda(), eps=0.0, form="e4m3")
+    y = torch.sign(h) * w
+    want = (w.abs().max() / 448).expand(T)
+    assert same_bits(scales.cpu(), want.contiguous())
+    assert same_bits(codes.cpu(), (y / want[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn))
+    codes, scales, _ = ckl.add_norm_quant(zero, h.cuda(), w.cuda(), eps=0.0, form="int8")
+    assert all(same_bits(a, b) for a, b in zip((codes, scales), ckl.act_encode(y.cuda())))
 
 
 def test_quant_of_zeros_and_special_values():
@@ -365,3 +393,19 @@ def test_neighbours_stay_untouched():
     for b, m in [(b, n) for b in bufs.values()] + [(rstd, T), (dw, d), (drop, 1003)]:
         assert (b[:16] == -7).all() and (b[16 + m:] == -7).all() and not (b[16:16 + m] == -7).any()
     assert (ws[need.value:] == 0xAB).all()
+
+
+def test_second_derivatives_are_refused():
+    x, w = normal((4, 16), torch.float32, 2).cuda().requires_grad_(True), normal((16,), torch.float32, 3).cuda()
+    z, tok = normal((4, 9), torch.float32, 4).cuda().requires_grad_(True), torch.zeros(4, dtype=torch.int64, device="cuda")
+    head = normal((9, 16), torch.float32, 5).cuda()
+    for f, leaf in ((lambda: ckl.add_rms_norm(x, x.detach(), w)[0], x), (lambda: ckl.token_logprobs(z, tok)[1], z),
+                    (lambda: ckl.head_logprobs(x, head, tok)[0], x)):
+        (g,) = torch.autograd.grad(f().sum(), (leaf,), create_graph=True)
+        with pytest.raises(RuntimeError, match="once_differentiable"):
+            g.sum().backward()
+    v = normal((4, 16), torch.float32, 6).cuda().requires_grad_(True)
+    y = ckl.dropout(x, 0.5, 3)  # linear: its gradient can be differentiated
+    (g,) = torch.autograd.grad(y, (x,), v, create_graph=True)
+    (gg,) = torch.autograd.grad(g, (v,), x.detach())
+    assert same_bits(gg, y.detach())
