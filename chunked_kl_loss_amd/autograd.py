@@ -223,7 +223,8 @@ class AddRMSNorm(torch.autograd.Function):
     def forward(ctx, x, residual, weight, eps, p, seed, offset):
         y, h, rstd = ops.add_norm_forward(x, residual, weight, eps, p, seed, offset)
         ctx.x_dtype = x.dtype
-        ctx.drop = p, seed.clone() if p and isinstance(seed, torch.Tensor) else seed, offset
+        ctx.state = seed.clone() if p and isinstance(seed, torch.Tensor) else seed
+        ctx.drop = ops._drop_args(p, ctx.state, offset, x.device)
         ctx.save_for_backward(h, rstd, weight)
         ctx.set_materialize_grads(False)
         return y, h
@@ -236,7 +237,7 @@ class AddRMSNorm(torch.autograd.Function):
         h, rstd, weight = ctx.saved_tensors
         if dy is None:  # the norm's output was not used
             dy = torch.zeros_like(h, dtype=ctx.x_dtype)
-        dx, dresidual, dweight = ops.add_norm_backward(dy.contiguous(), _contiguous(dh), h, rstd, weight, *ctx.drop)
+        dx, dresidual, dweight = ops.add_norm_backward_saved(dy.contiguous(), _contiguous(dh), h, rstd, weight, ctx.drop)
         return dx, dresidual, dweight, None, None, None, None
 
 

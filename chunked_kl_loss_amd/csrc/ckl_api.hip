@@ -1047,6 +1047,6 @@ const char* ckl_status_string(ckl_status s) {
 
 const char* ckl_last_error(void) { return g_last_error.c_str(); }
 
-int32_t ckl_version(void) { return (2 << 16) | 1; }
+int32_t ckl_version(void) { return (2 << 16) | 2; }
 
 }  // extern "C"

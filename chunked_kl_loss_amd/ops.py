@@ -188,8 +188,7 @@ def token_logprobs_backward(dlogprob, dentropy, logits, tokens, lse, entropy, ma
     T, code, nb = tokens.numel(), _code(logits.dtype), _token_bytes(tokens)
     logits = _aligned(logits)
     dlogits = _new(logits.shape, logits.dtype, dev)
-    _call(dev, load_library().ckl_token_logprobs_backward, logits.data_ptr(), code, T, V, tokens.data_ptr(), nb,
-          mask_ptr, lse.data_ptr(), entropy.data_ptr(), _ptr(dlogprob), _ptr(dentropy), dlogits.data_ptr())
+    _call(dev, load_library().ckl_token_logprobs_backward, logits.data_ptr(), code, T, V, tokens.data_ptr(), nb, mask_ptr, lse.data_ptr(), entropy.data_ptr(), _ptr(dlogprob), _ptr(dentropy), dlogits.data_ptr())
     return dlogits
 
 
@@ -494,9 +493,15 @@ def add_norm_backward(dy, dh, h, rstd, weight, p: float = 0.0, seed=0, offset: i
         raise ValueError("dy and dh must have h's shape, and dh its type")
     dev = _check(*_given(dy=dy, h=h, rstd=rstd, weight=weight, dh=dh))
     _check_rstd(rstd, h.shape[:-1])
-    d, T, code, r_code = h.shape[-1], _rows(h), _code(dy.dtype), _code(h.dtype)
-    w_code = _weight_code(weight, d)
-    args = _drop_args(p, seed, offset, dev)
+    _weight_code(weight, h.shape[-1])
+    _code(dy.dtype), _code(h.dtype)
+    return add_norm_backward_saved(dy, dh, h, rstd, weight, _drop_args(p, seed, offset, dev))
+
+
+def add_norm_backward_saved(dy, dh, h, rstd, weight, args):
+    """add_norm_backward from what a forward call checked: args are its _drop_args."""
+    dev, d, T = h.device, h.shape[-1], _rows(h)
+    code, r_code, w_code = _CODES[dy.dtype], _CODES[h.dtype], _CODES[weight.dtype]
     dy, h, weight = _aligned(dy), _aligned(h), _aligned(weight)
     dh = None if dh is None else _aligned(dh)
     ws, ws_ptr, ws_bytes = _workspace(dev, "ckl_add_norm_workspace_size", T, d)

@@ -409,3 +409,16 @@ def test_second_derivatives_are_refused():
     (g,) = torch.autograd.grad(y, (x,), v, create_graph=True)
     (gg,) = torch.autograd.grad(g, (v,), x.detach())
     assert same_bits(gg, y.detach())
+
+
+def test_one_tensor_as_branch_and_residual():
+    T, d = 9, 64
+    w = (1 + normal((d,), torch.float32, 3, 0.2)).cuda()
+    x = normal((T, d), torch.float32, 1).cuda().requires_grad_(True)
+    y, h = ckl.add_rms_norm(x, x, w)
+    assert same_bits(h.detach(), x.detach() + x.detach())
+    dy = normal((T, d), torch.float32, 2).cuda()
+    (y * dy).sum().backward()
+    a, b = (x.detach().clone().requires_grad_(True) for _ in range(2))
+    (ckl.add_rms_norm(a, b, w)[0] * dy).sum().backward()
+    assert torch.equal(x.grad, a.grad + b.grad) and a.grad.data_ptr() != b.grad.data_ptr()
