@@ -19,12 +19,16 @@ namespace ckl {
 
 namespace {
 
-// Tiles (vocabulary x token rows, and a wave's share of them).  Few rows: W is read once whatever the tile, and a
-// narrow one leaves room for several workgroups on a compute unit, whose loads hide one another's latency.
+// Tiles (vocabulary x token rows, and a wave's share of them).  Few rows: W is read
+// once whatever the tile, and a narrow one leaves room for two workgroups or more on
+// a compute unit, whose loads hide one another's latency.  (2880 x 201088 bf16, us,
+// 256 x 32 / 128 x 32 / 64 x 32 for 8 rows: 199 / 243 / 209; 256 x 64 / 128 x 64 for 64:
+// 210 / 271; 128 x 128 / 256 x 128 / 256 x 256 for 128: 263 / 279 / 295; 256 x 256 / 256 x
+// 128 for 129: 300 / 395.  What a copy moves takes 221.)
 using CfgWide = Dma64Cfg<256, 256, 128, 64>;
-using CfgMiddle = Dma64Cfg<256, 128, 64, 64>;
-using CfgNarrow = Dma64Cfg<128, 64, 32, 32>;
-using CfgSlim = Dma64Cfg<128, 32, 32, 32>;
+using CfgMiddle = Dma64Cfg<128, 128, 64, 32>;
+using CfgNarrow = Dma64Cfg<256, 64, 64, 32>;
+using CfgSlim = Dma64Cfg<256, 32, 64, 32>;
 using CfgF32 = TileCfg<float, 128, 128, 64, 64>;
 using CfgF32Small = TileCfg<float, 64, 128, 32, 64>;
 using CfgF32Slim = TileCfg<float, 128, 32, 32, 32>;
