@@ -30,7 +30,7 @@ using CfgMiddle = Dma64Cfg<128, 128, 64, 32>;
 using CfgNarrow = Dma64Cfg<256, 64, 64, 32>;
 using CfgSlim = Dma64Cfg<256, 32, 64, 32>;
 using CfgF32 = TileCfg<float, 128, 128, 64, 64>;
-using CfgF32Small = TileCfg<float, 64, 128, 32, 64>;
+using CfgF32Small = TileCfg<float, 64, 64, 32, 32>;
 using CfgF32Slim = TileCfg<float, 128, 32, 32, 32>;
 
 constexpr float kExpZero = -1e4f;  // 2^x is zero from here on, and its product with x too
@@ -307,31 +307,36 @@ __global__ __launch_bounds__(256) void head_buckets_kernel(const int* __restrict
   }
 }
 
-// dH from its parts and the tokens' entries, eight columns a thread.
+// dH from its parts and the tokens' entries, eight columns a thread; zeros where the
+// row is masked.
 template <typename TOut>
 __global__ __launch_bounds__(256) void head_dh_kernel(const float* __restrict__ part, int64_t stride, int S, int T,
                                                       int nv, const int* __restrict__ tok,
                                                       const float* __restrict__ gtok, const bf16_t* __restrict__ W,
                                                       HeadRows rows, TOut* __restrict__ dH) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int r = (int)(i / nv), c = (int)(i - (int64_t)r * nv);
-  if (r >= (rows.n != nullptr ? min(T, *rows.n) : T)) return;
-  const int t = rows.perm != nullptr ? rows.perm[r] : r, k = tok[r];
-  float a[8], b[8];
-  load8(part + i * 8, a);
+  const int t = (int)(i / nv), c = (int)(i - (int64_t)t * nv);
+  if (t >= T) return;
+  const int r = rows.rank != nullptr ? rows.rank[t] : t;
+  float a[8] = {}, b[8];
+  if (r >= 0) {
+    const float* p = part + ((int64_t)r * nv + c) * 8;
+    load8(p, a);
 #pragma unroll 4
-  for (int s = 1; s < S; ++s) {
-    load8(part + s * stride + i * 8, b);
+    for (int s = 1; s < S; ++s) {
+      load8(p + s * stride, b);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) a[j] += b[j];
-  }
-  if (k >= 0) {
-    const float g = gtok[r];
-    load8(W + ((int64_t)k * nv + c) * 8, b);
+      for (int j = 0; j < 8; ++j) a[j] += b[j];
+    }
+    const int k = gtok != nullptr ? tok[r] : -1;
+    if (k >= 0) {
+      const float g = gtok[r];
+      load8(W + ((int64_t)k * nv + c) * 8, b);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) a[j] = fmaf(g, b[j], a[j]);
+      for (int j = 0; j < 8; ++j) a[j] = fmaf(g, b[j], a[j]);
+    }
   }
-  store8(dH + ((int64_t)t * nv + c) * 8, a);
+  store8(dH + i * 8, a);
 }
 
 // The G block of rows [tb0, tb0 + BN n_tblocks) and columns [vb0, vb0 + BM
@@ -491,7 +496,9 @@ HeadTile head_tile(int in_bf16, int64_t rows, int64_t V) {
   if (in_bf16)
     kind = rows <= 32 ? kSlim : rows <= 64 ? kNarrow : rows <= 128 ? kMiddle : kWide;
   else
-    kind = rows <= 32 ? kF32Slim : (rows + 127) / 128 * ((V + 127) / 128) < 256 ? kF32Small : kF32;
+    // (fp32, us, 64 x 64 / 128 x 128: 64 rows of 520, 5003 words 18 / 44, 301 of them 28 / 46; 500 of 768, 32000 words
+    // 245 / 230, 2048 of 1024 1237 / 1092)
+    kind = rows <= 32 ? kF32Slim : (rows + 127) / 128 * ((V + 127) / 128) < 512 ? kF32Small : kF32;
   HeadTile t{kind, 0, 0, 0};
   by_tile(kind, [&](auto cfg) {
     using C = decltype(cfg);
@@ -552,6 +559,8 @@ hipError_t launch_head_dh(const float* part, int64_t stride, int S, int T, int d
   return hipSuccess;
 }
 
+int head_grad_rows(int in_bf16) { return in_bf16 ? CfgWide::BN : CfgF32Small::BN; }
+
 hipError_t launch_head_grad(int in_bf16, const void* H, const void* W, int T, int d, int V, const float4* consts,
                             const int* tok, float* gtok, int tb0, int t_rows, int vb0, int v_rows, int tiles_per_split, void* G,
                             int64_t ldG, void* Gt, int64_t ldGt, const int* nrows, hipStream_t st) {
@@ -563,13 +572,12 @@ hipError_t launch_head_grad(int in_bf16, const void* H, const void* W, int T, in
         (const TIn*)H, (const TIn*)W, T, d, V, consts, tok, gtok, tb0, vb0, n_vtiles, tps, n_tblocks, splits, (TIn*)G, ldG,
         (TIn*)Gt, ldGt, nrows);
   };
-  // (fp32 tiles that would not fill the compute units: halves of them)
+  // (fp32 by 64 x 64, us, against 128 x 128: 226 rows of 520, 5003 words 30 and 48; 1000 of 512, 2000 words 44 and 93;
+  // 2048 of 1024, 32000 words 1274 and 1282)
   if (in_bf16)
     go(CfgWide{}, tiles_per_split);
-  else if ((int64_t)(t_rows / CfgF32::BN) * (v_rows / CfgF32::BM) < 256)
-    go(CfgF32Small{}, 1);
   else
-    go(CfgF32{}, tiles_per_split);
+    go(CfgF32Small{}, 1);
   CKL_LAUNCH_CHECK();
   return hipSuccess;
 }

@@ -1817,9 +1817,8 @@ hipError_t launch_bwd_grad(int in_bf16, const void* H, const void* W, int T, int
                                      n_splits, tiles_per_split, G, ldG, Gt, ldGt, nrows, st);
 }
 
-template <typename TIn>
+template <typename TIn, class C = typename CfgOf<TIn>::gemm>
 static hipError_t gemm_pair_t(const GemmArgs& a0, const GemmArgs& a1, hipStream_t st) {
-  using C = typename CfgOf<TIn>::gemm;
   GemmProblem<TIn> p[2];
   const GemmArgs* a[2] = {&a0, &a1};
   for (int i = 0; i < 2; ++i) {
@@ -1875,7 +1874,8 @@ static hipError_t gemm_pair_t(const GemmArgs& a0, const GemmArgs& a1, hipStream_
   return hipSuccess;
 }
 
-hipError_t launch_gemm_pair(int in_bf16, const GemmArgs& a0, const GemmArgs& a1, hipStream_t st) {
+hipError_t launch_gemm_pair(int in_bf16, const GemmArgs& a0, const GemmArgs& a1, hipStream_t st, int f32_small) {
+  if (!in_bf16 && f32_small) return gemm_pair_t<float, TileCfg<float, 64, 64, 32, 32>>(a0, a1, st);
   return in_bf16 ? gemm_pair_t<bf16_t>(a0, a1, st) : gemm_pair_t<float>(a0, a1, st);
 }
 
