@@ -62,11 +62,19 @@ def _new(shape, dtype, device):
     return t
 
 
+def _like(t):
+    """_new of the shape and type of a contiguous tensor (a third cheaper)."""
+    t = torch.empty_like(t)
+    if _binding.FILL_BYTE is not None and t.numel() > 0:
+        t.view(-1).view(torch.uint8).fill_(int(_binding.FILL_BYTE))
+    return t
+
+
 def _call(device, fn, *args) -> None:
     """fn(*args, stream) on the device's current stream.  The library launches on the current GPU: the tensors'
     own is made current where it is not."""
     index = device.index
-    if index == torch.cuda.current_device():
+    if index == torch._C._cuda_getDevice():  # (torch.cuda.current_device without its checks: there are GPU tensors)
         # (the raw handle: a Stream object costs as much as a launch)
         status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
@@ -187,7 +195,7 @@ def token_logprobs_backward(dlogprob, dentropy, logits, tokens, lse, entropy, ma
     _check_row_floats(lead, lse=lse, entropy=entropy, dlogprob=dlogprob, dentropy=dentropy)
     T, code, nb = tokens.numel(), _code(logits.dtype), _token_bytes(tokens)
     logits = _aligned(logits)
-    dlogits = _new(logits.shape, logits.dtype, dev)
+    dlogits = _like(logits)
     _call(dev, load_library().ckl_token_logprobs_backward, logits.data_ptr(), code, T, V, tokens.data_ptr(), nb, mask_ptr, lse.data_ptr(), entropy.data_ptr(), _ptr(dlogprob), _ptr(dentropy), dlogits.data_ptr())
     return dlogits
 
@@ -235,7 +243,7 @@ def head_logprobs_backward(dlogprob, dentropy, H, W, tokens, lse, entropy, mask=
     H, W = _aligned(H), _aligned(W)
     ws, ws_ptr, ws_bytes = _workspace(dev, "ckl_head_workspace_size", T, d, V, chunk, code, _code(dh_dtype),
                                       _code(dw_dtype), int(mask is not None), 1)
-    dH = _new(H.shape, dh_dtype, dev) if need_dh else None
+    dH = (_like(H) if dh_dtype == H.dtype else _new(H.shape, dh_dtype, dev)) if need_dh else None
     dW = _new(W.shape, dw_dtype, dev) if need_dw else None
     _call(dev, load_library().ckl_head_logprobs_backward, H.data_ptr(), W.data_ptr(), code, T, d, V,
           tokens.data_ptr(), nb, mask_ptr, chunk, lse.data_ptr(), entropy.data_ptr(), _ptr(dlogprob), _ptr(dentropy),
@@ -459,7 +467,7 @@ def dropout_forward(x, p: float, seed=0, offset: int = 0):
     dev, code = _check(("x",), x), _code(x.dtype)
     args = _drop_args(p, seed, offset, dev)
     x = _aligned(x)
-    out = _new(x.shape, x.dtype, dev)
+    out = _like(x)
     _call(dev, load_library().ckl_dropout, x.data_ptr(), code, x.numel(), *args, out.data_ptr())
     return out
 
@@ -479,7 +487,7 @@ def add_norm_forward(x, residual, weight, eps: float = 1e-6, p: float = 0.0, see
     dev, code, r_code, w_code = _check_branch(x, residual, weight)
     args = _drop_args(p, seed, offset, dev)
     x, residual, weight = _aligned(x), _aligned(residual), _aligned(weight)
-    y, h = _new(x.shape, x.dtype, dev), _new(x.shape, residual.dtype, dev)
+    y, h = _like(x), _like(residual)
     rstd = _new(x.shape[:-1], torch.float32, dev) if save else None
     _call(dev, load_library().ckl_add_norm_forward, x.data_ptr(), code, residual.data_ptr(), r_code, _rows(x),
           x.shape[-1], weight.data_ptr(), w_code, eps, *args, h.data_ptr(), y.data_ptr(), _ptr(rstd))
@@ -505,9 +513,9 @@ def add_norm_backward_saved(dy, dh, h, rstd, weight, args):
     dy, h, weight = _aligned(dy), _aligned(h), _aligned(weight)
     dh = None if dh is None else _aligned(dh)
     ws, ws_ptr, ws_bytes = _workspace(dev, "ckl_add_norm_workspace_size", T, d)
-    dresidual = _new(h.shape, h.dtype, dev)
-    dx = _new(h.shape, dy.dtype, dev) if args[0] > 0.0 or code != r_code else None
-    dweight = _new(weight.shape, weight.dtype, dev)
+    dresidual = _like(h)
+    dx = _like(dy) if args[0] > 0.0 or code != r_code else None
+    dweight = _like(weight)
     _call(dev, load_library().ckl_add_norm_backward, dy.data_ptr(), code, _ptr(dh), r_code, T, d, h.data_ptr(),
           rstd.data_ptr(), weight.data_ptr(), w_code, *args, _ptr(dx), dresidual.data_ptr(), dweight.data_ptr(),
           ws_ptr, ws_bytes)
@@ -526,7 +534,7 @@ def add_norm_quant(x, residual, weight, eps: float = 1e-6, form: str = "int8"):
     dev, code, r_code, w_code = _check_branch(x, residual, weight)
     x, residual, weight = _aligned(x), _aligned(residual), _aligned(weight)
     d, lead = x.shape[-1], x.shape[:-1]
-    h = _new(x.shape, residual.dtype, dev)
+    h = _like(residual)
     if form == "int8":
         codes, scales = _new(x.shape, torch.int8, dev), _new((*lead, -(-d // ACT_BLOCK)), torch.uint8, dev)
     else:
