@@ -132,29 +132,34 @@ __global__ __launch_bounds__(C::NTHREADS) void head_rows_kernel(
       mx = fmaxf(mx, __shfl_xor(mx, 32)) * kLog2e;
       const float crm = __shfl(rm, src);
       const float mn = fmaxf(crm, mx);
+      const float ref = mn == -INFINITY ? 0.f : mn;
       float ssum = 0.f, esum = 0.f;
       if (full) {
 #pragma unroll
         for (int mb = 0; mb < MBK; ++mb)
 #pragma unroll
           for (int r = 0; r < RPB; ++r) {
-            const float x = tile.acc[mb][nb][r] * kLog2e - mn, u = fast_exp2(x);
+            const float x = tile.acc[mb][nb][r] * kLog2e - ref, u = fast_exp2(x);
             ssum += u;
             esum = fmaf(u, x, esum);
           }
-      } else if (mn > -INFINITY) {
+      }
+      if (!full || esum != esum) {  // (there are -infinities, which count for nothing, or a NaN, which stays)
+        ssum = esum = 0.f;
 #pragma unroll
         for (int mb = 0; mb < MBK; ++mb)
 #pragma unroll
           for (int r = 0; r < RPB; ++r) {
-            const float x = fmaxf(tile.acc[mb][nb][r] * kLog2e - mn, kExpZero), u = fast_exp2(x);
+            float x = tile.acc[mb][nb][r] * kLog2e - ref;
+            x = x < kExpZero ? kExpZero : x;
+            const float u = fast_exp2(x);
             ssum += u;
             esum = fmaf(u, x, esum);
           }
       }
       ssum += __shfl_xor(ssum, 32);
       esum += __shfl_xor(esum, 32);
-      if (own && mn > -INFINITY) {
+      if (own && (mn > -INFINITY || ssum != ssum)) {
         const float dm = fmaxf(rm - mn, kExpZero), f = fast_exp2(dm);
         re = fmaf(f, fmaf(dm, rs, re), esum);
         rs = fmaf(f, rs, ssum);
@@ -211,10 +216,15 @@ __global__ __launch_bounds__(256) void head_finish_kernel(const float4* __restri
   if (sub != 0 || !live) return;
   const int t = rows.perm != nullptr ? rows.perm[p] : p;
   const float l2 = fast_log2(s), l = (m + l2) * kLn2;
-  const float ent = (l2 - e / s) * kLn2;
+  const float ent = s == 0.f ? 0.f : (l2 - e / s) * kLn2;
   lse[t] = l;
   entropy[t] = ent < 0.f ? 0.f : ent;
-  logprob[t] = token_column(rows, p, V) >= 0 ? ztok[i] - l : 0.f;
+  float z = 0.f;
+  if (token_column(rows, p, V) >= 0) {
+    z = ztok[i];
+    if (z != -INFINITY || l != l) z -= l;  // (-infinity has that log probability in a row of nothing else, too)
+  }
+  logprob[t] = z;
 }
 
 // --------------------------------------------------------------- backward --
@@ -350,8 +360,8 @@ __global__ __launch_bounds__(256) void head_dh_kernel(const float* __restrict__ 
 template <class C>
 __global__ __launch_bounds__(C::NTHREADS) void head_grad_kernel(
     const typename C::TIn* __restrict__ H, const typename C::TIn* __restrict__ W, int T, int d, int V,
-    const float4* __restrict__ consts, const int* __restrict__ tok, float* __restrict__ gtok, int tb0, int vb0, int n_vtiles,
-    int tiles_per_split, int n_tblocks, int n_splits, typename C::TIn* __restrict__ G, int64_t ldG,
+    const float4* __restrict__ consts, const int* __restrict__ tok, float* __restrict__ gtok, int tb0, int vb0,
+    int n_vtiles, int tiles_per_split, int n_tblocks, int n_splits, typename C::TIn* __restrict__ G, int64_t ldG,
     typename C::TIn* __restrict__ Gt, int64_t ldGt, const int* __restrict__ nrows) {
   using TIn = typename C::TIn;
   constexpr bool kStage = std::is_same<TIn, bf16_t>::value;
@@ -562,8 +572,8 @@ hipError_t launch_head_dh(const float* part, int64_t stride, int S, int T, int d
 int head_grad_rows(int in_bf16) { return in_bf16 ? CfgWide::BN : CfgF32Small::BN; }
 
 hipError_t launch_head_grad(int in_bf16, const void* H, const void* W, int T, int d, int V, const float4* consts,
-                            const int* tok, float* gtok, int tb0, int t_rows, int vb0, int v_rows, int tiles_per_split, void* G,
-                            int64_t ldG, void* Gt, int64_t ldGt, const int* nrows, hipStream_t st) {
+                            const int* tok, float* gtok, int tb0, int t_rows, int vb0, int v_rows, int tiles_per_split,
+                            void* G, int64_t ldG, void* Gt, int64_t ldGt, const int* nrows, hipStream_t st) {
   auto go = [&](auto cfg, int tps) {
     using C = decltype(cfg);
     using TIn = typename C::TIn;

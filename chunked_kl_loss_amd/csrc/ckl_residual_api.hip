@@ -13,7 +13,7 @@ using namespace ckl::host;
 
 namespace {
 
-constexpr int64_t kMaxElements = (int64_t)1 << 40;
+constexpr int64_t kMaxElements = (int64_t)1 << 36;  // (2^31 threads; a launch takes fewer than 2^32)
 
 ckl_status drop_args(double p, uint64_t seed, uint64_t offset, const int64_t* state, ckl::DropArgs* a) {
   if (!(p >= 0.0 && p <= 1.0)) return fail(CKL_ERR_INVALID_ARG, "p must be from 0 to 1");
@@ -48,7 +48,7 @@ extern "C" {
 ckl_status ckl_dropout(const void* x, int32_t dtype, int64_t n, double p, uint64_t seed, uint64_t offset,
                        const int64_t* state, void* out, void* stream) {
   if (n < 0) return fail(CKL_ERR_INVALID_ARG, "n=%lld must be >= 0", (long long)n);
-  if (n > kMaxElements) return fail(CKL_ERR_UNSUPPORTED, "n=%lld: at most 2^40 elements", (long long)n);
+  if (n > kMaxElements) return fail(CKL_ERR_UNSUPPORTED, "n=%lld: at most 2^36 elements", (long long)n);
   if (!dtype_ok(dtype)) return fail(CKL_ERR_INVALID_ARG, "dtype must be CKL_F32 (0) or CKL_BF16 (1)");
   ckl::DropArgs a;
   ckl_status s = drop_args(p, seed, offset, state, &a);

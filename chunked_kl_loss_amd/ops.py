@@ -196,7 +196,8 @@ def token_logprobs_backward(dlogprob, dentropy, logits, tokens, lse, entropy, ma
     T, code, nb = tokens.numel(), _code(logits.dtype), _token_bytes(tokens)
     logits = _aligned(logits)
     dlogits = _like(logits)
-    _call(dev, load_library().ckl_token_logprobs_backward, logits.data_ptr(), code, T, V, tokens.data_ptr(), nb, mask_ptr, lse.data_ptr(), entropy.data_ptr(), _ptr(dlogprob), _ptr(dentropy), dlogits.data_ptr())
+    _call(dev, load_library().ckl_token_logprobs_backward, logits.data_ptr(), code, T, V, tokens.data_ptr(), nb,
+          mask_ptr, lse.data_ptr(), entropy.data_ptr(), _ptr(dlogprob), _ptr(dentropy), dlogits.data_ptr())
     return dlogits
 
 

@@ -421,7 +421,9 @@ ckl_status ckl_token_logprobs_backward(const void* logits, int32_t dtype, int64_
  * never stored.  H [T, d], W [V, d] in_dtype; tokens, mask, logprob, entropy and
  * lse as above, chunk as in ckl_problem.  Masked rows are not computed and may
  * hold anything; their results are 0.  fp32 products and sums (bf16: exact
- * products, fp32 sums).
+ * products, fp32 sums).  A row with a NaN or +inf among its logits gives NaN; logits
+ * of -inf, to which finite states and words only overflow, are as above, but the
+ * row's gradients are then NaN.
  *   ws: ckl_head_workspace_size(T, d, V, chunk, in_dtype, dh_dtype, dw_dtype,
  *   masked, which) bytes; which 0: forward (the output dtypes do not matter), 1:
  *   backward; masked: 1 where a mask is given. */
@@ -436,7 +438,8 @@ ckl_status ckl_head_logprobs(const void* H, const void* W, int32_t in_dtype, int
  * about chunk x V entries of in_dtype (bf16 rounds it once).  dH [T, d] dh_dtype,
  * dW [V, d] dw_dtype, overwritten; one of them may be NULL and is then not
  * computed.  lse and entropy: from ckl_head_logprobs on the same inputs.  T = 0:
- * dW is zero. */
+ * dW is zero.  (Rows that are not masked take part in the products, also those with
+ * a = b = 0: a NaN in their states reaches dW.) */
 ckl_status ckl_head_logprobs_backward(const void* H, const void* W, int32_t in_dtype, int64_t T, int64_t d, int64_t V,
                                       const void* tokens, int32_t token_bytes, const uint8_t* mask, int64_t chunk,
                                       const float* lse, const float* entropy, const float* dlogprob,
@@ -450,7 +453,7 @@ ckl_status ckl_head_logprobs_backward(const void* H, const void* W, int32_t in_d
  * (0: the low one) of word (i % 8) / 2 of Philox4x32-10 with key (low, high word of
  * seed) and counter (low, high word of i / 8, low, high word of offset).  The
  * gradient is the same call on the incoming one.
- *   x, out: [n] dtype, n up to 2^40.  0 <= p <= 1 (1: all zeros).
+ *   x, out: [n] dtype, n up to 2^36.  0 <= p <= 1 (1: all zeros).
  *   state:  NULL, or 2 int64 in device memory, {seed, offset}, read when the kernel
  *           runs: the seed is then state[0] and state[1] is added to `offset`, so
  *           that a captured call draws anew when the memory changes. */

@@ -35,7 +35,7 @@ def drop(lib, x=P[0], dtype=1, n=100, p=0.5, seed=1, offset=0, state=None, out=P
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(n=-1), INV), (dict(n=(1 << 40) + 1), UNS), (dict(dtype=2), INV), (dict(p=-0.1), INV), (dict(p=1.1), INV),
+    (dict(n=-1), INV), (dict(n=(1 << 36) + 1), UNS), (dict(dtype=2), INV), (dict(p=-0.1), INV), (dict(p=1.1), INV),
     (dict(p=float("nan")), INV), (dict(x=None), INV), (dict(out=None), INV), (dict(x=P[0] + 2), INV),
     (dict(out=P[1] + 8), INV), (dict(out=P[0]), INV), (dict(out=P[0] + 192), INV), (dict(state=P[2] + 4), INV),
     (dict(state=P[1] + 16), INV)])

@@ -325,3 +325,52 @@ def test_gradients_lose_no_more_than_their_outputs_rounding():
     for g, w in zip(got, (G @ W.double(), G.t() @ H.double())):
         off = float((g.double().cpu() - w).norm()), float((w.to(torch.bfloat16).double() - w).norm())
         assert off[0] < 1.1 * off[1]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [5, 100, 300])
+@pytest.mark.parametrize("words", [(0, 1), (0, 256), (3, 260), (512, 513), (899, 900), (768, 900), (0, 900)])
+def test_a_nan_in_the_head_reaches_every_row(words, T, dtype):
+    H, W, tok = inputs(T, 64, 900, DT[dtype], 3)
+    W[words[0]:words[1], 7] = math.nan
+    for t in ckl.head_logprobs_forward(H.cuda(), W.cuda(), tok.clamp(0, 899).cuda()):
+        assert t.isnan().all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [8, 100, 304])
+def test_a_state_that_is_not_finite_stays_in_its_row(T, dtype):
+    H, W, tok = inputs(T, 64, 900, DT[dtype], 3)
+    want = ckl.head_logprobs_forward(H.cuda(), W.cuda(), tok.cuda())
+    bad = torch.arange(T) % 8 == 3
+    H[bad, 5] = torch.tensor([math.nan, math.inf, -math.inf]).to(H.dtype).repeat(T)[:int(bad.sum())]
+    tok[bad] = 7
+    W[::9, 5] = 0.0  # infinity times zero
+    clean = ckl.head_logprobs_forward(torch.where(bad[:, None], 0.0, H.float()).to(H.dtype).cuda(), W.cuda(), tok.cuda())
+    for t, w in zip(ckl.head_logprobs_forward(H.cuda(), W.cuda(), tok.cuda()), clean):
+        assert t[bad].isnan().all() and same_bits(t[~bad], w[~bad])
+    assert all(not w.isnan().any() for w in want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [8, 100, 304])
+def test_logits_that_overflow_to_minus_infinity_count_for_nothing(T, dtype):
+    # a row's logits are a column of W: H holds one 2^100 a row, W the logits times 2^-100, and -2^60 for -infinity
+    V = 900
+    z = grid((8, V), torch.float32, 1, 0.25)
+    gone = torch.zeros(8, V, dtype=torch.bool)
+    for r, (a, b) in enumerate([(0, 0), (0, 300), (0, 899), (1, 900), (768, 900), (897, 900), (256, 512), (0, 900)]):
+        gone[r, a:b] = True
+    W = torch.where(gone, -2.0 ** 60, z * 2.0 ** -100).t().contiguous().to(DT[dtype])
+    H = torch.zeros(T, 8, dtype=DT[dtype])
+    H[torch.arange(T), torch.arange(T) % 8] = 2.0 ** 100
+    z = torch.where(gone, -math.inf, z.double())[torch.arange(T) % 8]
+    tok = torch.randint(0, V, (T,), generator=gen(2))
+    lp, ent, lse = (t.cpu() for t in ckl.head_logprobs_forward(H.cuda(), W.cuda(), tok.cuda()))
+    some = torch.arange(T) % 8 != 7
+    r = rows_reference(z[some], tok[some])
+    there = r["logprob"] > -math.inf
+    assert (lp[some][~there] == -math.inf).all()
+    assert within(lp[some][there], r["logprob"][there], (r["tol_lp"] + 4 * EPS * r["lse"].abs())[there])
+    assert within(ent[some], r["entropy"], r["tol_ent"])
+    assert (lse[~some] == -math.inf).all() and (lp[~some] == -math.inf).all() and (ent[~some] == 0).all()
