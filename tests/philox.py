@@ -11,16 +11,17 @@ def philox4x32(counter, key, rounds=10):
     k = [int(key[0]), int(key[1])]
     for _ in range(rounds):
         a, b = c[0] * np.uint64(0xD2511F53), c[2] * np.uint64(0xCD9E8D57)
-        c = [(b >> np.uint64(32)) ^ c[1] ^ np.uint64(k[0]), b & LOW, (a >> np.uint64(32)) ^ c[3] ^ np.uint64(k[1]), a & LOW]
+        c = [(b >> np.uint64(32)) ^ c[1] ^ np.uint64(k[0]), b & LOW, (a >> np.uint64(32)) ^ c[3] ^ np.uint64(k[1]),
+             a & LOW]
         k = [(k[0] + 0x9E3779B9) & 0xFFFFFFFF, (k[1] + 0xBB67AE85) & 0xFFFFFFFF]
     return c
 
 
-def keep_mask(n, p, seed, offset):
-    """(mask of the n elements, the factor of the kept ones)."""
-    vec = np.arange(-(-n // 8), dtype=np.uint64)
-    c = philox4x32([vec & LOW, vec >> np.uint64(32), np.full_like(vec, offset & 0xFFFFFFFF), np.full_like(vec, offset >> 32)],
-                   (seed & 0xFFFFFFFF, seed >> 32))
+def keep_mask(n, p, seed, offset, first=0):
+    """(mask of the n elements from `first` on, a multiple of 8, the factor of the kept ones)."""
+    vec = np.arange(-(-n // 8), dtype=np.uint64) + np.uint64(first // 8)
+    c = philox4x32([vec & LOW, vec >> np.uint64(32), np.full_like(vec, offset & 0xFFFFFFFF),
+                    np.full_like(vec, offset >> 32)], (seed & 0xFFFFFFFF, seed >> 32))
     bits = np.empty((vec.size, 8), dtype=np.uint64)
     for i, w in enumerate(c):
         bits[:, 2 * i], bits[:, 2 * i + 1] = w & np.uint64(0xFFFF), w >> np.uint64(16)

@@ -38,6 +38,49 @@ def dropped(x, p, seed, offset):
     return torch.from_numpy(y.astype(np.float32)).view(x.shape).to(x.dtype), torch.from_numpy(keep).view(x.shape)
 
 
+def test_offsets_past_32_bits():
+    # the last rows lie more than 2^32 elements behind the first
+    T, d, p = 2_900_000, 1512, 0.3
+    x = torch.zeros(T, d, dtype=torch.bfloat16, device="cuda")
+    last, dlast = normal((2, d), torch.bfloat16, 1), normal((2, d), torch.bfloat16, 2)
+    x[-2:] = last.cuda()
+    keep, scale = keep_mask(2 * d, p, 7, 9, (T - 2) * d)
+
+    def drop(t):
+        return torch.where(torch.from_numpy(keep).view(2, d), t.float() * scale, 0.0).bfloat16()
+    y = ckl.dropout(x, p, 7, 9)
+    assert same_bits(y[-2:].cpu(), drop(last)) and not y[:-2].any()
+    del y
+    w = (1 + normal((d,), torch.float32, 3, 0.1)).bfloat16().cuda()
+    y, h, rstd = ckl.add_norm_forward(x, x, w, 1e-6, p, 7, 9)
+    hl = (last.float() + torch.where(torch.from_numpy(keep).view(2, d), last.float() * scale, 0.0)).bfloat16()
+    want = ckl.add_norm_forward(torch.zeros_like(hl).cuda(), hl.cuda(), w)
+    for got, v in zip((y, h, rstd), want):
+        assert same_bits(got[-2:], v)
+    assert not y[:-2].any() and not h[:-2].any() and (rstd[:-2] == rstd[0]).all()
+    del y, want
+    x.zero_()
+    x[-2:] = dlast.cuda()
+    dx, dres, dw = ckl.add_norm_backward(x, None, h, rstd, w, p, 7, 9)
+    _, small, dw2 = ckl.add_norm_backward(dlast.cuda(), None, hl.cuda(), rstd[-2:].contiguous(), w)
+    assert same_bits(dres[-2:], small) and not dres[:-2].any() and not dx[:-2].any()
+    # (dx is scaled before dres is rounded: three roundings between the two)
+    assert ((dx[-2:].cpu() != 0) == (torch.from_numpy(keep).view(2, d) & (small.cpu() != 0))).all()
+    assert ((dx[-2:].cpu().double() - drop(small.cpu()).double()).abs() <= 2 ** -6 * drop(small.cpu()).double().abs()).all()
+    # (a workgroup may hold both rows or each its own: sums of two terms)
+    assert ((dw.double() - dw2.double()).abs() <= 2 ** -6 * dw2.double().abs() + 1e-6).all()
+    del x, h, dx, dres
+    z = torch.zeros(T, d, dtype=torch.bfloat16, device="cuda")
+    z[-2:] = last.cuda()
+    for form in ("int8", "e4m3"):
+        codes, scales, h = ckl.add_norm_quant(z, z, w, form=form)
+        small = ckl.add_norm_quant(last.cuda(), last.cuda(), w, form=form)
+        for got, v in zip((codes, scales, h), small):
+            assert same_bits(got[-2:], v)
+        assert not codes[:-2].view(torch.uint8).any()
+        del codes, scales, h
+
+
 # ---------------------------------------------------------------- dropout --
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("n,p,seed,offset", [

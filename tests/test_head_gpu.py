@@ -219,6 +219,52 @@ def test_neighbours_and_rows_past_the_last():
             assert torch.allclose(b[16:16 + n].float(), w.reshape(-1).float(), rtol=1e-5, atol=1e-6)
 
 
+@pytest.mark.parametrize("T,d,V,chunk", [(40, 2880, 800_000, 2048), (2900, 64, 800_000, 1 << 20), (3, 8, 4_000_000, 1)])
+def test_offsets_past_32_bits(T, d, V, chunk):
+    # W, or the block of logit gradients, holds more than 2^31 elements; the last holds the most words there are
+    H = grid((T, d), torch.bfloat16, 1, 0.25).cuda()
+    gen_cuda = torch.Generator("cuda")
+    gen_cuda.manual_seed(2)
+    step = 2.0 ** round(math.log2(2.0 / (4.9 * 0.25 * 4.9 * math.sqrt(d))))
+    W = torch.randint(-8, 9, (V, d), generator=gen_cuda, device="cuda", dtype=torch.int8).bfloat16() * step
+    tok = some_tokens(T, V, 3)
+    tok[-1] = V - 1
+    rows = torch.tensor(sorted({0, 1, T // 2, T - 2, T - 1}))
+    tok = tok.cuda()
+    lp, ent, lse = ckl.head_logprobs_forward(H, W, tok)
+    a, b = normal((T,), torch.float32, 3), normal((T,), torch.float32, 4, 0.3)
+    dH, dW = ckl.head_logprobs_backward(a.cuda(), b.cuda(), H, W, tok, lse, ent, chunk=chunk, dw_dtype=torch.bfloat16)
+    # some rows over all words, by blocks of words
+    blocks = range(0, V, 50_000)
+    z = torch.cat([(H[rows].double() @ W[v:v + 50_000].double().t()).cpu() for v in blocks], 1)
+    r = rows_reference(z, tok.cpu()[rows])
+    assert within(lse[rows], r["lse"], r["tol_lse"])
+    assert within(lp[rows], r["logprob"], r["tol_lp"] + 4 * EPS * r["lse"].abs())
+    assert within(ent[rows], r["entropy"], r["tol_ent"])
+    G, tol = dz_reference(z, tok.cpu()[rows], r, a[rows], b[rows])
+    tol = tol + (HALF[torch.bfloat16] + (V + 8) * EPS) * G.abs()
+    want, off = torch.zeros(len(rows), d, dtype=torch.float64), torch.zeros(len(rows), d, dtype=torch.float64)
+    for v in blocks:
+        part = W[v:v + 50_000].double()
+        want += (G[:, v:v + 50_000].cuda() @ part).cpu()
+        off += (tol[:, v:v + 50_000].cuda() @ part.abs()).cpu()
+    assert within(dH[rows], want, off + HALF[torch.bfloat16] * want.abs())
+    # all rows over some words
+    words = torch.cat([torch.arange(3), torch.arange(V // 2, V // 2 + 300), torch.arange(V - 300, V)])
+    at = torch.full((V,), -1)
+    at[words] = torch.arange(len(words))
+    z = (H.double() @ W[words.cuda()].double().t()).cpu()
+    # (4,000,000 terms a sum: tolerances of 9.4e-4 and, with a mean distance of 10 from the maximum, 0.027)
+    r = dict(lse=lse.double().cpu(), entropy=ent.double().cpu(), tol_lse=torch.full((T,), 1e-3), tol_ent=torch.full((T,), 3e-2))
+    inside = (tok.cpu() >= 0) & (tok.cpu() < V)
+    mapped = torch.where(inside, at[torch.where(inside, tok.cpu(), 0)], -1)
+    G, tol = dz_reference(z, mapped, r, torch.where(inside, a, 0.0), b)
+    G = G - torch.where(inside & (mapped < 0), a.double(), 0.0)[:, None] * torch.exp(z - r["lse"][:, None])
+    tol = tol + (HALF[torch.bfloat16] + (T + 8) * EPS) * G.abs() + 1e-3 * a.abs().double()[:, None] * torch.exp(z - r["lse"][:, None])
+    want = G.t().cuda() @ H.double()
+    assert within(dW[words.cuda()], want, tol.t().cuda() @ H.double().abs() + HALF[torch.bfloat16] * want.abs() + 1e-37)
+
+
 # ------------------------------------------------------- all of it, used together --
 def full_step(x, res, nw, W, tok, idx, tl, mask, state, adv):
     """A branch's output behind dropout, the residual's sum and the norm into the head: distillation, a policy term
