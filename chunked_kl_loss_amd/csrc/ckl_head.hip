@@ -255,18 +255,21 @@ __global__ __launch_bounds__(256) void head_consts_kernel(HeadRows rows, int T, 
   tok[i] = c;
 }
 
-// The rows by the 64 words that hold their token, in their order: a workgroup lists
-// four such groups, behind the number of rows whose token lies below them (2048 rows
-// are 8 KB, read by every workgroup from the caches).
-__global__ __launch_bounds__(256) void head_buckets_kernel(const int* __restrict__ tok, int T,
+// A block's rows by the 64 words that hold their token, in their order: a workgroup
+// lists four such groups, behind the number of rows whose token lies below them (2048
+// rows are 8 KB, read by every workgroup from the caches; 786 groups of 256 words 10 us).
+__global__ __launch_bounds__(256) void head_buckets_kernel(const int* __restrict__ tok, int T, int Tc,
                                                            const int* __restrict__ n, int* __restrict__ order,
                                                            int* __restrict__ start) {
   __shared__ int counts[5][4], mine[2][4][4];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int v0 = blockIdx.x * 256;
   if (n != nullptr) T = min(T, *n);
+  const int t0 = blockIdx.y * Tc;
+  T = min(T, t0 + Tc);
+  start += blockIdx.y * (gridDim.x * 4 + 1);
   int sum[5] = {};  // rows below the four groups, in the first, ..
-  for (int i = threadIdx.x; i < T; i += 256) {
+  for (int i = t0 + threadIdx.x; i < T; i += 256) {
     const int c = tok[i], g = (c - v0) >> 6;
     sum[0] += c >= 0 && c < v0 ? 1 : 0;
 #pragma unroll
@@ -279,7 +282,7 @@ __global__ __launch_bounds__(256) void head_buckets_kernel(const int* __restrict
     if (lane == 0) counts[k][wave] = sum[k];
   }
   __syncthreads();
-  int at[4], all = 0;
+  int at[4], all = t0;
 #pragma unroll
   for (int k = 0; k < 5; ++k) {
     all += counts[k][0] + counts[k][1] + counts[k][2] + counts[k][3];
@@ -292,7 +295,7 @@ __global__ __launch_bounds__(256) void head_buckets_kernel(const int* __restrict
   }
   if (all == at[0]) return;  // no row's token is here
   int side = 0;
-  for (int i0 = 0; i0 < T; i0 += 256) {
+  for (int i0 = t0; i0 < T; i0 += 256) {
     const int i = i0 + threadIdx.x;
     const int c = i < T ? tok[i] : -1;
     const int g = c >= v0 && c < v0 + 256 ? (c - v0) >> 6 : -1;
@@ -552,8 +555,9 @@ hipError_t launch_head_consts(const HeadRows& rows, int T, int Tp, int V, const 
   return hipSuccess;
 }
 
-hipError_t launch_head_buckets(const int* tok, int T, const int* n, int tiles, int* order, int* start, hipStream_t st) {
-  head_buckets_kernel<<<tiles, 256, 0, st>>>(tok, T, n, order, start);
+hipError_t launch_head_buckets(const int* tok, int T, int Tc, const int* n, int tiles, int* order, int* start,
+                               hipStream_t st) {
+  head_buckets_kernel<<<dim3(tiles, (T + Tc - 1) / Tc), 256, 0, st>>>(tok, T, Tc, n, order, start);
   CKL_LAUNCH_CHECK();
   return hipSuccess;
 }

@@ -31,9 +31,11 @@ hipError_t launch_head_finish(const float4* part, int S, int count, int V, const
 // dlogprob or dentropy may be NULL (zero).
 hipError_t launch_head_consts(const HeadRows& rows, int T, int Tp, int V, const float* lse, const float* entropy,
                               const float* dlogprob, const float* dentropy, float4* consts, int* tok, hipStream_t st);
-// The rows below T (or *n) by the 64 words that hold their token: order, ascending in
-// each group, and start [4 tiles + 1] of `tiles` times 256 words; rows without a token are in none.
-hipError_t launch_head_buckets(const int* tok, int T, const int* n, int tiles, int* order, int* start, hipStream_t st);
+// Each block of Tc of the rows below T (or *n) by the 64 words that hold their token:
+// order, ascending in each group, and start [blocks][4 tiles + 1] of `tiles` times 256
+// words; rows without a token are in none.
+hipError_t launch_head_buckets(const int* tok, int T, int Tc, const int* n, int tiles, int* order, int* start,
+                               hipStream_t st);
 // dH: a row's sum of its S parts, + gtok W[tok] where gtok is not NULL (W in bf16); zeros where it is masked.
 hipError_t launch_head_dh(const float* part, int64_t stride, int S, int T, int d, const int* tok, const float* gtok,
                           const void* W, const HeadRows& rows, void* dH, int dh_bf16, hipStream_t st);
@@ -41,7 +43,7 @@ hipError_t launch_head_dh(const float* part, int64_t stride, int S, int T, int d
 // head_grad_rows rows up to the one that holds the last row below it.
 int head_grad_rows(int in_bf16);
 hipError_t launch_head_grad(int in_bf16, const void* H, const void* W, int T, int d, int V, const float4* consts,
-                            const int* tok, float* gtok, int tb0, int t_rows, int vb0, int v_rows, int tiles_per_split, void* G, int64_t ldG, void* Gt,
-                            int64_t ldGt, const int* nrows, hipStream_t st);
+                            const int* tok, float* gtok, int tb0, int t_rows, int vb0, int v_rows, int tiles_per_split,
+                            void* G, int64_t ldG, void* Gt, int64_t ldGt, const int* nrows, hipStream_t st);
 
 }  // namespace ckl

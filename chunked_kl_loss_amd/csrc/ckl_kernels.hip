@@ -1461,31 +1461,38 @@ __global__ __launch_bounds__(C::NTHREADS) void gemm_store_kernel(GemmProblem<typ
           __syncthreads();
           if constexpr (MORE) {
             if (second && p1.rows.order != nullptr) {
-              // a thread takes one column of every row that falls in this part, in the list's order
+              // a thread takes one column of every row that falls in this part, in the list's order; a lane fetches what
+              // belongs to one row of 64 and hands it round, and sixteen rows' loads are under way together
               const GemmRows& q = p1.rows;
               const int v0 = q.col0 + m0 + part * PART, e1 = row_start[part + 1];
               const int c = threadIdx.x;
-              bool any = false;
-              for (int e0 = row_start[part]; e0 < e1; e0 += 8) {
-                int to[8];
-                float x[8];
+              if (c < C::BN) {
+                const bf16_t* from = reinterpret_cast<const bf16_t*>(q.rows) + min(n0 + c, N - 1);
+                for (int e0 = row_start[part]; e0 < e1; e0 += 64) {
+                  const int mine = q.order[min(e0 + lane, e1 - 1)];
+                  const int row = q.col[mine] - v0;
+                  const float by = q.scale[mine];
+                  const int left = min(64, e1 - e0);
+                  int j0 = 0;
+                  auto add = [&](auto count) {  // (those past the last are fetched, and not added)
+                    constexpr int NR = decltype(count)::value;
+                    bf16_t x[NR];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {  // (eight rows' loads under way together)
-                  const int i = e0 + j < e1 ? q.order[e0 + j] : -1;
-                  const int ml = i >= 0 ? q.col[i] - v0 : -1;
-                  const bool here = i >= q.lo && i < q.hi;
-                  to[j] = here ? ml : -1;
-                  x[j] = here && c < C::BN && n0 + c < N
-                             ? q.scale[i] * (float)reinterpret_cast<const bf16_t*>(q.rows)[(int64_t)i * N + n0 + c]
-                             : 0.f;
-                }
+                    for (int j = 0; j < NR; ++j) x[j] = from[(int64_t)__builtin_amdgcn_readlane(mine, j0 + j) * N];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                  any |= to[j] >= 0;
-                  if (to[j] >= 0 && c < C::BN) st[to[j] * C::BN + (c ^ stage_swz(to[j]))] += x[j];
+                    for (int j = 0; j < NR; ++j) {
+                      const int to = __builtin_amdgcn_readlane(row, j0 + j);
+                      const float g = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(by), j0 + j));
+                      float* o = st + to * C::BN + (c ^ stage_swz(to));
+                      if (j0 + j < left) *o = fmaf(g, (float)x[j], *o);
+                    }
+                    j0 += NR;
+                  };
+                  while (left - j0 > 4) add(std::integral_constant<int, 16>{});
+                  if (j0 < left) add(std::integral_constant<int, 4>{});
                 }
               }
-              if (any) __syncthreads();
+              if (row_start[part] < e1) __syncthreads();
             }
           }
           for (int i = threadIdx.x; i < PART * CPR; i += C::NTHREADS) {

@@ -88,15 +88,15 @@ hipError_t launch_bwd_grad(int in_bf16, const void* H, const void* W, int T, int
                            const float* p_s, const float* Mrow, const float* lse, const float* srow, int tb0,
                            int t_rows, int vb0, int v_rows, int n_splits, int tiles_per_split, void* G, int64_t ldG,
                            void* Gt, int64_t ldGt, const int* nrows, hipStream_t st);
-// Rows added to a product in fp32: out[col[i] - col0] += scale[i] rows[i], i from
-// lo to below hi, in the order of i.  order lists the i by col / 64, ascending in it;
-// those of group g lie from start[g] to below start[g + 1]; col0 is a multiple of 256,
-// and there are whole 256s of groups.
+// Rows added to a product in fp32: out[col[i] - col0] += scale[i] rows[i], in the
+// order of i.  order lists the i by col / 64, ascending in it; those of group g lie
+// from start[g] to below start[g + 1]; col0 is a multiple of 256, and the groups
+// cover whole tiles of as many.
 struct GemmRows {
   const int *order = nullptr, *start = nullptr, *col = nullptr;
   const float* scale = nullptr;
   const void* rows = nullptr;  // bf16, N columns each
-  int col0 = 0, lo = 0, hi = 0;
+  int col0 = 0;
 };
 // out[m, n] (+)= sum_k X[m, k] Y[n, k]; row-major operands contiguous in k.
 // batches > 1: that many products xb / yb / ob elements apart, the last with

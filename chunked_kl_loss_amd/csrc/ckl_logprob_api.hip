@@ -55,6 +55,9 @@ LogprobWs logprob_layout(int64_t T, int64_t V, int64_t top) {
 // Row padding (elements) of the matrices whose leading dimension is chosen here:
 // 256 bytes keep the rows of a load on different memory channels.
 constexpr int64_t kLdPad = 128;
+// Rows a launch of the forward takes (8192 rows of 512, 1000 words, bf16, in launches of 2048 97 us, in one FWDA;
+// 32768 of 1024, 50264 words, in 16 3048, in two FWDB).
+constexpr int64_t kForwardRows = 16384;
 constexpr int64_t kGradSlots = 256;  // workgroups of head_grad at once: one to a compute unit
 
 // Vocabulary splits of a launch over row blocks: the count that finishes in the
@@ -122,7 +125,8 @@ ckl_status head_plan(int64_t T, int64_t d, int64_t V, int64_t chunk, int32_t in_
   const int64_t share = (dh_tiles * q->Vc + dw_tiles * q->Tc) / (kGradSlots * 4);
   q->Vs = std::min(round_up(std::max<int64_t>(share, 512), 64), q->Vc);
   q->Sh = ceil_div(q->Vc, q->Vs);
-  q->Cs = std::min(round_up(chunk, 256), round_up(p.T, 256));
+  // (the forward keeps 16 bytes a row and split: its blocks of rows need not be short)
+  q->Cs = std::min(std::max(round_up(chunk, 256), kForwardRows), round_up(p.T, 256));
   q->nS = ceil_div(p.T, q->Cs);
   const int64_t rows = std::min(q->Cs, p.T);
   q->tile = ckl::head_tile(q->bf16, rows, V);
@@ -175,7 +179,7 @@ HeadBwdWs head_bwd_layout(const HeadPlan& q, bool masked, int32_t dh_dtype, int3
   if (q.bf16) {
     w.gtok = l.take(q.Tp * 4);
     w.order = l.take(q.Tp * 4);
-    w.start = l.take((q.Vp / 64 + 1) * 4);
+    w.start = l.take(q.nT * (q.Vp / 64 + 1) * 4);
   }
   w.Ht = l.take((size_t)q.d * (q.Tp + kLdPad) * q.esz);
   w.Wt = l.take((size_t)q.d * (q.Vc + kLdPad) * q.esz);
@@ -408,7 +412,7 @@ ckl_status ckl_head_logprobs_backward(const void* H, const void* W, int32_t in_d
   if (dW && q.bf16)
     HIP_TRY(timed(CKL_KERNEL_OTHER, st,
                   [&] {
-                    return ckl::launch_head_buckets(tok, (int)T, r.n, (int)(q.Vp / 256), order, start, st);
+                    return ckl::launch_head_buckets(tok, (int)T, (int)q.Tc, r.n, (int)(q.Vp / 256), order, start, st);
                   }),
             "head_buckets");
   if (dW)
@@ -455,13 +459,11 @@ ckl_status ckl_head_logprobs_backward(const void* H, const void* W, int32_t in_d
       if (dW && dw16 && tb == q.nT - 1) gdw.out16 = (char*)dW + vb0 * d * 2;
       if (dW && q.bf16) {
         gdw.rows.order = order;
-        gdw.rows.start = start;
+        gdw.rows.start = start + tb * (q.Vp / 64 + 1);
         gdw.rows.col = tok;
         gdw.rows.scale = gtok;
         gdw.rows.rows = Hs;
         gdw.rows.col0 = (int)vb0;
-        gdw.rows.lo = (int)tb0;
-        gdw.rows.hi = (int)std::min(tb0 + trows, T);
       }
       if (r.n) {
         gdw.lim = gdh.lim = r.n;

@@ -76,6 +76,21 @@ def test_chunks(chunk, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("share", [None, 0.98, 0.5])
+def test_more_rows_than_a_launch_takes(share, dtype):
+    T = 17000
+    H, W, tok = inputs(T, 16, 300, DT[dtype], 1)
+    mask = None if share is None else torch.rand(T, generator=gen(2)) < share
+    check(H, W, tok, mask, chunk=4096)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,V,chunk", [(8192, 500, 2048), (6001, 600, 512), (3000, 64, 1 << 20)])
+def test_many_rows_of_few_words(T, V, chunk, dtype):
+    check(*inputs(T, 136, V, DT[dtype], 1), chunk=chunk)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("kind", ["some", "all", "none", "one", "packed"])
 def test_masks_and_tokens_outside(kind, dtype):
     T, V = 700, 900
