@@ -352,6 +352,40 @@ __global__ __launch_bounds__(256) void head_dh_kernel(const float* __restrict__ 
   store8(dH + i * 8, a);
 }
 
+// The same from parts of dH's transpose ([d][ldt]): 32 rows by 8 columns a workgroup,
+// turned in the LDS; a thread sums one element.
+template <typename TOut>
+__global__ __launch_bounds__(256) void head_dh_t_kernel(const float* __restrict__ part, int64_t stride, int64_t ldt,
+                                                        int S, int T, int d, const int* __restrict__ tok,
+                                                        const float* __restrict__ gtok, const bf16_t* __restrict__ W,
+                                                        HeadRows rows, TOut* __restrict__ dH) {
+  __shared__ float turn[8][33];
+  const int c0 = blockIdx.x * 8, t0 = blockIdx.y * 32;
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  const int t = t0 + tx;
+  const int r = t >= T ? -1 : rows.rank != nullptr ? rows.rank[t] : t;
+  float a = 0.f;
+  if (r >= 0) {
+    const float* p = part + (int64_t)(c0 + ty) * ldt + r;
+#pragma unroll 16
+    for (int s = 0; s < S; ++s) a += p[s * stride];
+  }
+  turn[ty][tx] = a;
+  __syncthreads();
+  if (threadIdx.x >= 32 || t >= T) return;
+  float f[8], w[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = turn[j][tx];
+  const int k = r >= 0 ? tok[r] : -1;
+  if (k >= 0) {
+    const float g = gtok[r];
+    load8(W + (int64_t)k * d + c0, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = fmaf(g, w[j], f[j]);
+  }
+  store8(dH + (int64_t)t * d + c0, f);
+}
+
 // The G block of rows [tb0, tb0 + BN n_tblocks) and columns [vb0, vb0 + BM
 // n_vtiles): G[t - tb0][v - vb0], and for fp32 also its transpose Gt.  bf16 rounds
 // G once, to what the contractions read, but for each row's largest entry as a rule,
@@ -407,7 +441,7 @@ __global__ __launch_bounds__(C::NTHREADS) void head_grad_kernel(
     const bool full = vbase + C::WM <= V;
 #pragma unroll
     for (int nb = 0; nb < C::NB; ++nb) {
-      const int tl = opaque(wave_n * C::WN + nb * 32 + (lane & 31));  // (addresses formed here, not held across the loop)
+      const int tl = opaque(wave_n * C::WN + nb * 32 + (lane & 31));  // (formed here, not held across the loop)
       const float4 rc = s_row[tl];
 #pragma unroll
       for (int mb = 0; mb < C::MB; ++mb)
@@ -573,7 +607,17 @@ hipError_t launch_head_dh(const float* part, int64_t stride, int S, int T, int d
   return hipSuccess;
 }
 
-int head_grad_rows(int in_bf16) { return in_bf16 ? CfgWide::BN : CfgF32Small::BN; }
+hipError_t launch_head_dh_t(const float* part, int64_t stride, int64_t ldt, int S, int T, int d, const int* tok,
+                            const float* gtok, const void* W, const HeadRows& rows, void* dH, int dh_bf16,
+                            hipStream_t st) {
+  const dim3 grid(d / 8, (T + 31) / 32);
+  if (dh_bf16)
+    head_dh_t_kernel<<<grid, 256, 0, st>>>(part, stride, ldt, S, T, d, tok, gtok, (const bf16_t*)W, rows, (bf16_t*)dH);
+  else
+    head_dh_t_kernel<<<grid, 256, 0, st>>>(part, stride, ldt, S, T, d, tok, gtok, (const bf16_t*)W, rows, (float*)dH);
+  CKL_LAUNCH_CHECK();
+  return hipSuccess;
+}
 
 hipError_t launch_head_grad(int in_bf16, const void* H, const void* W, int T, int d, int V, const float4* consts,
                             const int* tok, float* gtok, int tb0, int t_rows, int vb0, int v_rows, int tiles_per_split,
@@ -583,8 +627,8 @@ hipError_t launch_head_grad(int in_bf16, const void* H, const void* W, int T, in
     using TIn = typename C::TIn;
     const int n_vtiles = v_rows / C::BM, n_tblocks = t_rows / C::BN, splits = (n_vtiles + tps - 1) / tps;
     head_grad_kernel<C><<<n_tblocks * splits, C::NTHREADS, 0, st>>>(
-        (const TIn*)H, (const TIn*)W, T, d, V, consts, tok, gtok, tb0, vb0, n_vtiles, tps, n_tblocks, splits, (TIn*)G, ldG,
-        (TIn*)Gt, ldGt, nrows);
+        (const TIn*)H, (const TIn*)W, T, d, V, consts, tok, gtok, tb0, vb0, n_vtiles, tps, n_tblocks, splits, (TIn*)G,
+        ldG, (TIn*)Gt, ldGt, nrows);
   };
   // (fp32 by 64 x 64, us, against 128 x 128: 226 rows of 520, 5003 words 30 and 48; 1000 of 512, 2000 words 44 and 93;
   // 2048 of 1024, 32000 words 1274 and 1282)

@@ -39,9 +39,12 @@ hipError_t launch_head_buckets(const int* tok, int T, int Tc, const int* n, int 
 // dH: a row's sum of its S parts, + gtok W[tok] where gtok is not NULL (W in bf16); zeros where it is masked.
 hipError_t launch_head_dh(const float* part, int64_t stride, int S, int T, int d, const int* tok, const float* gtok,
                           const void* W, const HeadRows& rows, void* dH, int dh_bf16, hipStream_t st);
+// The same from parts of the transpose, [d][ldt] each (bf16: gtok is not NULL).
+hipError_t launch_head_dh_t(const float* part, int64_t stride, int64_t ldt, int S, int T, int d, const int* tok,
+                            const float* gtok, const void* W, const HeadRows& rows, void* dH, int dh_bf16,
+                            hipStream_t st);
 // bf16: the tokens' own entries go to gtok in fp32, and are 0 in G.  nrows: G is formed in blocks of
-// head_grad_rows rows up to the one that holds the last row below it.
-int head_grad_rows(int in_bf16);
+// 256 rows (fp32: 64) up to the one that holds the last row below it.
 hipError_t launch_head_grad(int in_bf16, const void* H, const void* W, int T, int d, int V, const float4* consts,
                             const int* tok, float* gtok, int tb0, int t_rows, int vb0, int v_rows, int tiles_per_split,
                             void* G, int64_t ldG, void* Gt, int64_t ldGt, const int* nrows, hipStream_t st);

@@ -1861,8 +1861,8 @@ static hipError_t gemm_pair_t(const GemmArgs& a0, const GemmArgs& a1, hipStream_
       return hipErrorInvalidValue;
     if (a[i]->lim && (a[i]->lim_kind < 1 || a[i]->lim_kind > 2 || (a[i]->lim_kind == 2 && a[i]->lim_round % 8)))
       return hipErrorInvalidValue;
-    // k-major X: every tile reads BM whole columns of each k row
-    if (a[i]->xt && (!kXtOK<C> || a[i]->batches > 1 || (int64_t)(a[i]->M + C::BM - 1) / C::BM * C::BM > a[i]->ldx))
+    // k-major X: whole 16-byte chunks of each k row
+    if (a[i]->xt && (!kXtOK<C> || (a[i]->M + 7) / 8 * 8 > a[i]->ldx || a[i]->ldx % 8 || a[i]->xb % 8))
       return hipErrorInvalidValue;
     p[i].tiles_m = a[i]->M > 0 ? (a[i]->M + C::BM - 1) / C::BM : 0;
     p[i].tiles = a[i]->M > 0 && a[i]->N > 0 ? p[i].tiles_m * ((a[i]->N + C::BN - 1) / C::BN) * p[i].batches : 0;

@@ -111,8 +111,8 @@ struct GemmArgs {
   int M, N, kdim, beta;
   int batches = 1, kdim_last = 0;
   int64_t xb = 0, yb = 0, ob = 0;
-  // X stored k-major: element (m, k) at X[k ldx + m] (bf16 only; the
-  // buffer must hold whole 256-column tiles along m)
+  // X stored k-major: element (m, k) at X[k ldx + m] (bf16 only, M <= ldx; kdim need
+  // then not be a multiple of 8 where Y is zero up to one)
   int xt = 0;
   // packed rows: lim_kind 1 bounds M by *lim - lim_base (tiles past it are
   // skipped), 2 bounds kdim by it rounded up to lim_round (a multiple of 8)

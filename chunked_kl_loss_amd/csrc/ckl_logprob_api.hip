@@ -58,6 +58,8 @@ constexpr int64_t kLdPad = 128;
 // Rows a launch of the forward takes (8192 rows of 512, 1000 words, bf16, in launches of 2048 97 us, in one FWDA;
 // 32768 of 1024, 50264 words, in 16 3048, in two FWDB).
 constexpr int64_t kForwardRows = 16384;
+constexpr int64_t kTurnedTile = 400;
+constexpr int64_t kTileElements = (int64_t)1 << 30;  // of bf16, what a tile's byte offsets reach
 constexpr int64_t kGradSlots = 256;  // workgroups of head_grad at once: one to a compute unit
 
 // Vocabulary splits of a launch over row blocks: the count that finishes in the
@@ -85,6 +87,8 @@ struct HeadPlan {
   int64_t Cs, nS, splits, tps;
   // backward: G blocks of Tc rows x Vc columns; dH as Sh sums over Vs columns of a block each
   int64_t BM, BN, Tp, Vp, Tc, Vc, nT, nV, Sh, Vs;
+  int64_t dh_rows;  // rows (turned: columns) of a part of dH
+  bool turned;  // the sums are of dH's transpose, which needs no transpose of W
 };
 ckl_status head_plan(int64_t T, int64_t d, int64_t V, int64_t chunk, int32_t in_dtype, int32_t dh_dtype,
                      int32_t dw_dtype, HeadPlan* q) {
@@ -121,10 +125,17 @@ ckl_status head_plan(int64_t T, int64_t d, int64_t V, int64_t chunk, int32_t in_
   // dH has few tiles of a long sum, dW many of a short one: dH is cut into parts of about a quarter of a compute
   // unit's share of both (but not below the 512 columns that cost as much as storing a part's tile)
   const int64_t gm = ckl::gemm_tile_m(q->bf16), gn = ckl::gemm_tile_n(q->bf16);
-  const int64_t dh_tiles = ceil_div(q->Tc, gm) * ceil_div(d, gn), dw_tiles = ceil_div(q->Vc, gm) * ceil_div(d, gn);
+  int64_t dh_tiles = ceil_div(q->Tc, gm) * ceil_div(d, gn);
+  const int64_t dw_tiles = ceil_div(q->Vc, gm) * ceil_div(d, gn);
+  // (one block of rows, bf16: W^T G^T with W as it lies, where that takes no more tiles than the transpose of W costs.)
+  const int64_t turned_tiles = ceil_div(d, gm) * ceil_div(p.T, gn);
+  q->turned = q->bf16 && q->nT == 1 && (turned_tiles - dh_tiles) * kTurnedTile <= d &&
+              std::min(p.T, gn) * (q->Vc + kLdPad) < kTileElements;
+  if (q->turned) dh_tiles = turned_tiles;
+  q->dh_rows = q->turned ? round_up(T, 8) : T;
   const int64_t share = (dh_tiles * q->Vc + dw_tiles * q->Tc) / (kGradSlots * 4);
   q->Vs = std::min(round_up(std::max<int64_t>(share, 512), 64), q->Vc);
-  q->Sh = ceil_div(q->Vc, q->Vs);
+  q->Sh = ceil_div(q->turned ? std::min(q->Vc, V) : q->Vc, q->Vs);
   // (the forward keeps 16 bytes a row and split: its blocks of rows need not be short)
   q->Cs = std::min(std::max(round_up(chunk, 256), kForwardRows), round_up(p.T, 256));
   q->nS = ceil_div(p.T, q->Cs);
@@ -182,10 +193,10 @@ HeadBwdWs head_bwd_layout(const HeadPlan& q, bool masked, int32_t dh_dtype, int3
     w.start = l.take(q.nT * (q.Vp / 64 + 1) * 4);
   }
   w.Ht = l.take((size_t)q.d * (q.Tp + kLdPad) * q.esz);
-  w.Wt = l.take((size_t)q.d * (q.Vc + kLdPad) * q.esz);
+  w.Wt = q.turned ? 0 : l.take((size_t)q.d * (q.Vc + kLdPad) * q.esz);
   w.G = l.take((size_t)q.Tc * (q.Vc + kLdPad) * q.esz);
   w.Gt = q.bf16 ? 0 : l.take((size_t)q.Vc * (q.Tc + kLdPad) * q.esz);
-  w.dH = q.bf16 || dh_dtype == CKL_BF16 || masked || q.Sh > 1 ? l.take((size_t)q.Sh * q.T * q.d * 4) : 0;
+  w.dH = q.bf16 || dh_dtype == CKL_BF16 || masked || q.Sh > 1 ? l.take((size_t)q.Sh * q.dh_rows * q.d * 4) : 0;
   // fp32 sums of a bf16 dW (bf16 inputs: needed only between blocks of rows)
   w.dW = dw_dtype == CKL_BF16 && (!q.bf16 || q.nT > 1) ? l.take((size_t)q.V * q.d * 4) : 0;
   if (masked) w.pk = pack_layout(q, &l);
@@ -399,7 +410,7 @@ ckl_status ckl_head_logprobs_backward(const void* H, const void* W, int32_t in_d
   // fp32 sums in the outputs themselves, or in the workspace where the output is bf16 or its rows are packed
   const bool dh_parts = q.bf16 || dh_dtype == CKL_BF16 || mask || q.Sh > 1;
   float* dHacc = dh_parts ? (float*)(b + w.dH) : (float*)dH;
-  const int64_t dh_stride = T * d;
+  const int64_t dh_stride = q.dh_rows * d;
   // bf16 inputs and dW: the last block of rows writes the rounded sums
   const bool dw16 = q.bf16 && dw_dtype == CKL_BF16;
   float* dWacc = dw_dtype != CKL_BF16 ? (float*)dW : w.dW ? (float*)(b + w.dW) : nullptr;
@@ -424,7 +435,7 @@ ckl_status ckl_head_logprobs_backward(const void* H, const void* W, int32_t in_d
   const int64_t ldWt = q.Vc + kLdPad;
   for (int64_t vb = 0; vb < q.nV; ++vb) {
     const int64_t vb0 = vb * q.Vc, vrows = std::min(q.Vc, q.Vp - vb0);
-    if (dH)
+    if (dH && !q.turned)
       HIP_TRY(timed(CKL_KERNEL_TRANSPOSE, st,
                     [&] {
                       return ckl::launch_transpose_pad(q.bf16, (const char*)W + vb0 * d * q.esz,
@@ -450,9 +461,25 @@ ckl_status ckl_head_logprobs_backward(const void* H, const void* W, int32_t in_d
       gdh.kdim_last = (int)(vrows - (gdh.batches - 1) * q.Vs);
       gdh.xb = gdh.yb = q.Vs;
       gdh.ob = dh_stride;
+      if (q.turned) {
+        const int64_t cols = std::min(vrows, V - vb0);  // (W's rows)
+        gdh.batches = (int)ceil_div(cols, q.Vs);
+        gdh.kdim = (int)std::min(q.Vs, cols);
+        gdh.kdim_last = (int)(cols - (gdh.batches - 1) * q.Vs);
+        gdh.X = (const char*)W + vb0 * d * 2;
+        gdh.ldx = d;
+        gdh.xt = 1;
+        gdh.xb = q.Vs * d;
+        gdh.Y = G;
+        gdh.ldy = vrows + kLdPad;
+        gdh.out = dHacc;
+        gdh.ldo = q.dh_rows;
+        gdh.M = dH ? (int)d : 0;
+        gdh.N = (int)T;
+      }
       ckl::GemmArgs gdw{q.bf16 ? G : Gt, q.bf16 ? vrows + kLdPad : trows + kLdPad, Ht + tb0 * q.esz, q.Tp + kLdPad,
                         dWacc ? dWacc + vb0 * d : nullptr, d, dW ? (int)std::min(vrows, V - vb0) : 0, (int)d,
-                        (int)trows, tb > 0};
+                        (int)std::min(trows, round_up(T - tb0, 64)), tb > 0};
       gdw.xt = q.bf16;
       // (fp32 by 64 x 64, us, against 128 x 128: 226 rows of 520, 5003 words 41 and 53; 1000 of 512, 2000 words 80 and 164;
       // 2048 of 1024, 32000 words 2437 and 2427)
@@ -466,11 +493,15 @@ ckl_status ckl_head_logprobs_backward(const void* H, const void* W, int32_t in_d
         gdw.rows.col0 = (int)vb0;
       }
       if (r.n) {
-        gdw.lim = gdh.lim = r.n;
-        gdw.lim_base = gdh.lim_base = (int)tb0;
+        gdw.lim = r.n;
+        gdw.lim_base = (int)tb0;
         gdw.lim_kind = 2;
-        gdw.lim_round = ckl::head_grad_rows(q.bf16);
-        gdh.lim_kind = 1;
+        gdw.lim_round = 64;  // (G's rows are formed in blocks of as many or more)
+        if (!q.turned) {
+          gdh.lim = r.n;
+          gdh.lim_base = (int)tb0;
+          gdh.lim_kind = 1;
+        }
       }
       HIP_TRY(timed(CKL_KERNEL_GEMM_DHDW, st, [&] { return ckl::launch_gemm_pair(q.bf16, gdh, gdw, st, 1); }),
               "gemm dH + dW");
@@ -479,6 +510,9 @@ ckl_status ckl_head_logprobs_backward(const void* H, const void* W, int32_t in_d
   if (dH && dh_parts)
     HIP_TRY(timed(CKL_KERNEL_OTHER, st,
                   [&] {
+                    if (q.turned)
+                      return ckl::launch_head_dh_t(dHacc, dh_stride, q.dh_rows, (int)q.Sh, (int)T, (int)d, tok, gtok, W, r,
+                                                   dH, dh_dtype == CKL_BF16, st);
                     return ckl::launch_head_dh(dHacc, dh_stride, (int)q.Sh, (int)T, (int)d, tok,
                                                q.bf16 ? gtok : nullptr, W, r, dH, dh_dtype == CKL_BF16, st);
                   }),

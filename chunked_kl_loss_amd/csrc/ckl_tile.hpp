@@ -318,8 +318,10 @@ struct Dma64Cfg {
 // of BM columns; slot s = (i NWAVES + wave) 64 + lane of load i takes k row
 // s / (BM / 8), 16-byte chunk (s % (BM / 8)) ^ 4 (k % 4), so that the
 // transposing fragment reads below touch distinct banks.  Each slice gets a
-// buffer resource of its own, based at its first k row and bounded by the
-// rows below kdim (so operands larger than 4 GiB work).
+// buffer resource of its own, based at its first k row and bounded by the chunk
+// of column xrows - 1 of the last row below kdim (so operands larger than 4 GiB
+// work, and nothing behind the operand is read; columns past xrows of other rows
+// are whatever lies there).
 template <class C, bool XT = false>
 struct K64Loader {
   static_assert(!XT || C::BM % 128 == 0, "k-major X: at least 16 chunks per k row");
@@ -332,7 +334,7 @@ struct K64Loader {
   // steps are workgroup-uniform)
   uint32_t off[2];
   uint32_t xstep, ystep;
-  int wave, lchunk, kdim;
+  int wave, lchunk, kdim, xcols;
   __device__ __forceinline__ K64Loader(const bf16_t* X_, int64_t ldx, int xrows, const bf16_t* Y_, int64_t ldy,
                                        int yrows, int kdim_)
       : X(X_),
@@ -342,7 +344,8 @@ struct K64Loader {
         ldx_(ldx),
         xstep((uint32_t)(C::NWAVES * 8 * ldx * 2)),
         ystep((uint32_t)(C::NWAVES * 8 * ldy * 2)),
-        kdim(kdim_) {
+        kdim(kdim_),
+        xcols(min((xrows + 7) & ~7, C::BM)) {
     const int lane = threadIdx.x & 63;
     wave = wave_id();
     const int lrow = lane >> 3;
@@ -369,7 +372,8 @@ struct K64Loader {
     if constexpr (XT) {
       if (i < C::X_LOADS) {
         const int rows = min(C::BK, kdim - kt * C::BK);
-        const __amdgpu_buffer_rsrc_t r = make_rsrc(X + (int64_t)kt * C::BK * ldx_, (uint32_t)(rows * ldx_ * 2));
+        const __amdgpu_buffer_rsrc_t r = make_rsrc(X + (int64_t)kt * C::BK * ldx_,
+                                                    (uint32_t)(((rows - 1) * ldx_ + xcols) * 2));
         lds_dma_buf(r, xoff[i], 0u, lds_at(smem, kt, i));
         return;
       }
