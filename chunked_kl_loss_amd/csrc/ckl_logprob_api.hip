@@ -55,11 +55,15 @@ LogprobWs logprob_layout(int64_t T, int64_t V, int64_t top) {
 // Row padding (elements) of the matrices whose leading dimension is chosen here:
 // 256 bytes keep the rows of a load on different memory channels.
 constexpr int64_t kLdPad = 128;
-// Rows a launch of the forward takes (8192 rows of 512, 1000 words, bf16, in launches of 2048 97 us, in one FWDA;
-// 32768 of 1024, 50264 words, in 16 3048, in two FWDB).
-constexpr int64_t kForwardRows = 16384;
-constexpr int64_t kTurnedTile = 400;
 constexpr int64_t kTileElements = (int64_t)1 << 30;  // of bf16, what a tile's byte offsets reach
+// Rows a launch of the forward takes (8192 rows of 512, 1000 words, bf16, in launches of 2048 97 us, in one 25;
+// 32768 of 1024, 50264 words, in 16 3048, in two 2700).
+constexpr int64_t kForwardRows = 16384;
+// Columns of W whose transpose costs as much as one more tile of dH (its transpose against dH, us, with dW, 201088
+// words of 2880: 16 rows 1090 and 1540, 300 1650 and 2190, 1024, of 12 more tiles, 3660 and 3920, 2048, of 12 more,
+// 6550 and 6890; 100000 words: 512 rows of 264, 2 more, 263 and 288, 1024 of 520, 4 more, 598 and 590, 2048 of 1544,
+// 9 more, 2090 and 2065, 1024 of 264, 4 more, 431 and 390).
+constexpr int64_t kTurnedTile = 230;
 constexpr int64_t kGradSlots = 256;  // workgroups of head_grad at once: one to a compute unit
 
 // Vocabulary splits of a launch over row blocks: the count that finishes in the
@@ -127,7 +131,8 @@ ckl_status head_plan(int64_t T, int64_t d, int64_t V, int64_t chunk, int32_t in_
   const int64_t gm = ckl::gemm_tile_m(q->bf16), gn = ckl::gemm_tile_n(q->bf16);
   int64_t dh_tiles = ceil_div(q->Tc, gm) * ceil_div(d, gn);
   const int64_t dw_tiles = ceil_div(q->Vc, gm) * ceil_div(d, gn);
-  // (one block of rows, bf16: W^T G^T with W as it lies, where that takes no more tiles than the transpose of W costs.)
+  // One block of rows, bf16: dH^T = W^T G^T reads W as it lies, at the price of tiles the other way round.  (More blocks
+  // share one transpose of W.)
   const int64_t turned_tiles = ceil_div(d, gm) * ceil_div(p.T, gn);
   q->turned = q->bf16 && q->nT == 1 && (turned_tiles - dh_tiles) * kTurnedTile <= d &&
               std::min(p.T, gn) * (q->Vc + kLdPad) < kTileElements;
@@ -481,8 +486,8 @@ ckl_status ckl_head_logprobs_backward(const void* H, const void* W, int32_t in_d
                         dWacc ? dWacc + vb0 * d : nullptr, d, dW ? (int)std::min(vrows, V - vb0) : 0, (int)d,
                         (int)std::min(trows, round_up(T - tb0, 64)), tb > 0};
       gdw.xt = q.bf16;
-      // (fp32 by 64 x 64, us, against 128 x 128: 226 rows of 520, 5003 words 41 and 53; 1000 of 512, 2000 words 80 and 164;
-      // 2048 of 1024, 32000 words 2437 and 2427)
+      // (the contraction, us, fp32 by 64 x 64 against 128 x 128: 226 rows of 520, 5003 words 41 and 53; 1000 of 512,
+      // 2000 words 80 and 164; 2048 of 1024, 32000 words 2437 and 2427)
       if (dW && dw16 && tb == q.nT - 1) gdw.out16 = (char*)dW + vb0 * d * 2;
       if (dW && q.bf16) {
         gdw.rows.order = order;
@@ -511,8 +516,8 @@ ckl_status ckl_head_logprobs_backward(const void* H, const void* W, int32_t in_d
     HIP_TRY(timed(CKL_KERNEL_OTHER, st,
                   [&] {
                     if (q.turned)
-                      return ckl::launch_head_dh_t(dHacc, dh_stride, q.dh_rows, (int)q.Sh, (int)T, (int)d, tok, gtok, W, r,
-                                                   dH, dh_dtype == CKL_BF16, st);
+                      return ckl::launch_head_dh_t(dHacc, dh_stride, q.dh_rows, (int)q.Sh, (int)T, (int)d, tok, gtok, W,
+                                                   r, dH, dh_dtype == CKL_BF16, st);
                     return ckl::launch_head_dh(dHacc, dh_stride, (int)q.Sh, (int)T, (int)d, tok,
                                                q.bf16 ? gtok : nullptr, W, r, dH, dh_dtype == CKL_BF16, st);
                   }),
