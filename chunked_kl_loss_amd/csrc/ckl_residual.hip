@@ -204,7 +204,7 @@ __global__ __launch_bounds__(1024) void add_norm_kernel(const TX* __restrict__ x
   if constexpr (DROP) p = philox_key(drop.seed, drop.offset, drop.state);
   float f[NV][8];
   // (8 bits: what y's own roundings move across the border of two codes is a whole step there, so there the sum is held
-  // in 64 bits, r in two floats and their product with h, and y is rounded once; the bytes hide it)
+  // in 64 bits, r and its product with h in two floats, and y is rounded once; the bytes hide it)
   std::conditional_t<CODES, double, float> ss = 0;
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
@@ -270,6 +270,23 @@ __global__ __launch_bounds__(1024) void add_norm_kernel(const TX* __restrict__ x
       const int v = k * row_threads + tid;
       const uint32_t e = block_exponent(top_bits(f[k]));  // (lanes past the row hold zeros)
       if (live && v < nv) {
+        // a value that its rounding to fp32, at most 2^-18 steps, may have taken past the middle of two codes is formed
+        // again in 64 bits (one vector in four thousand)
+        const float inv = e == 255 ? 0.f : __uint_as_float((254u - e) << 23);
+        bool close = false;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float t = f[k][i] * inv;
+          close |= fabsf(t - rintf(t)) > 0.5f - 0x1p-16f;
+        }
+        if (close) {
+          float n[8], w[8];
+          load8(h + (row * nv + v) * 8, n);
+          load8_any(weight, weight_bf16, (int64_t)v * 8, w);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            f[k][i] = (float)rint((double)n[i] * ((double)r + r_low) * w[i] * inv) * block_step(e);
+        }
         __builtin_nontemporal_store(encode8(f[k], e), reinterpret_cast<u32x2*>((int8_t*)out.y + (row * nv + v) * 8));
         if ((v & 3) == 0) ((uint8_t*)out.scales)[row * nb + v / 4] = (uint8_t)e;
       }
