@@ -363,7 +363,7 @@ __global__ __launch_bounds__(256) void head_dh_t_kernel(const float* __restrict_
                                                         const float* __restrict__ gtok, const bf16_t* __restrict__ W,
                                                         HeadRows rows, TOut* __restrict__ dH) {
   __shared__ float turn[8][33];
-  const int c0 = blockIdx.x * 8, t0 = blockIdx.y * 32;
+  const int c0 = blockIdx.y * 8, t0 = blockIdx.x * 32;
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int t = t0 + tx;
   const int r = t >= T ? -1 : rows.rank != nullptr ? rows.rank[t] : t;
@@ -614,7 +614,7 @@ hipError_t launch_head_dh(const float* part, int64_t stride, int S, int T, int d
 hipError_t launch_head_dh_t(const float* part, int64_t stride, int64_t ldt, int S, int T, int d, const int* tok,
                             const float* gtok, const void* W, const HeadRows& rows, void* dH, int dh_bf16,
                             hipStream_t st) {
-  const dim3 grid(d / 8, (T + 31) / 32);
+  const dim3 grid((T + 31) / 32, d / 8);
   if (dh_bf16)
     head_dh_t_kernel<<<grid, 256, 0, st>>>(part, stride, ldt, S, T, d, tok, gtok, (const bf16_t*)W, rows, (bf16_t*)dH);
   else

@@ -103,6 +103,19 @@ def test_masks_and_tokens_outside(kind, dtype):
     check(H, W, tok, mask, chunk=256)
 
 
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("T,d,V,chunk", [(200, 72, 3001, 1), (200, 264, 20001, 20), (31, 328, 12345, 40),
+                                         (513, 72, 9000, 200)])
+def test_few_rows_in_blocks_of_words(T, d, V, chunk, masked):
+    H, W, tok = inputs(T, d, V, torch.bfloat16, 3)
+    mask = (torch.rand(T, generator=gen(1)) < 0.6) if masked else None
+    check(H, W, tok, mask, chunk=chunk)
+
+
+def test_one_block_of_millions_of_rows():
+    check(*inputs(2_200_000, 8, 8, torch.bfloat16, 3), chunk=2 ** 40)
+
+
 def test_larger_products():
     check(*inputs(512, 512, 30011, torch.bfloat16, 3))
 
