@@ -1828,6 +1828,7 @@ hipError_t launch_bwd_grad(int in_bf16, const void* H, const void* W, int T, int
 
 template <typename TIn, class C = typename CfgOf<TIn>::gemm>
 static hipError_t gemm_pair_t(const GemmArgs& a0, const GemmArgs& a1, hipStream_t st) {
+  constexpr bool kMore = sizeof(TIn) == 2 && std::is_same<C, typename CfgOf<TIn>::gemm>::value;
   GemmProblem<TIn> p[2];
   const GemmArgs* a[2] = {&a0, &a1};
   for (int i = 0; i < 2; ++i) {
@@ -1855,7 +1856,7 @@ static hipError_t gemm_pair_t(const GemmArgs& a0, const GemmArgs& a1, hipStream_
     p[i].rows = a[i]->rows;
     // (the path that does so: 16-byte rows of sums, whole vectors)
     if ((a[i]->out16 || a[i]->rows.order) &&
-        (sizeof(TIn) != 2 || a[i]->batches > 1 || a[i]->N % 4 || a[i]->ldo % 4 || ((uintptr_t)a[i]->out & 15) ||
+        (!kMore || a[i]->batches > 1 || a[i]->N % 4 || a[i]->ldo % 4 || ((uintptr_t)a[i]->out & 15) ||
          ((uintptr_t)a[i]->out16 & 7)))
       return hipErrorInvalidValue;
     if (a[i]->rows.order &&
@@ -1871,7 +1872,7 @@ static hipError_t gemm_pair_t(const GemmArgs& a0, const GemmArgs& a1, hipStream_
   }
   if (p[0].tiles + p[1].tiles == 0) return hipSuccess;
   const int n = (p[0].tiles + kNumXcd - 1) / kNumXcd * kNumXcd + p[1].tiles;
-  if constexpr (sizeof(TIn) == 2) {
+  if constexpr (kMore) {
     if (p[0].out16 || p[1].out16 || p[1].rows.order) {
       hipLaunchKernelGGL((gemm_store_kernel<C, true>), dim3(n), dim3(C::NTHREADS), 0, st, p[0], p[1]);
       CKL_LAUNCH_CHECK();
@@ -1883,8 +1884,9 @@ static hipError_t gemm_pair_t(const GemmArgs& a0, const GemmArgs& a1, hipStream_
   return hipSuccess;
 }
 
-hipError_t launch_gemm_pair(int in_bf16, const GemmArgs& a0, const GemmArgs& a1, hipStream_t st, int f32_small) {
-  if (!in_bf16 && f32_small) return gemm_pair_t<float, TileCfg<float, 64, 64, 32, 32>>(a0, a1, st);
+hipError_t launch_gemm_pair(int in_bf16, const GemmArgs& a0, const GemmArgs& a1, hipStream_t st, int small) {
+  if (!in_bf16 && small) return gemm_pair_t<float, TileCfg<float, 64, 64, 32, 32>>(a0, a1, st);
+  if (small) return gemm_pair_t<bf16_t, Dma64Cfg<256, 64, 64, 32>>(a0, a1, st);
   return in_bf16 ? gemm_pair_t<bf16_t>(a0, a1, st) : gemm_pair_t<float>(a0, a1, st);
 }
 

@@ -123,8 +123,8 @@ struct GemmArgs {
   GemmRows rows;  // bf16 inputs, no batches, the second product of a launch
 };
 // Two independent products in one launch (problem 0's tiles are scheduled first).
-// f32_small: fp32 by tiles of 64 x 64 instead of 128 x 128.
-hipError_t launch_gemm_pair(int in_bf16, const GemmArgs& a0, const GemmArgs& a1, hipStream_t st, int f32_small = 0);
+// small: fp32 by tiles of 64 x 64 instead of 128 x 128, bf16 by 256 x 64 instead of 256 x 320.
+hipError_t launch_gemm_pair(int in_bf16, const GemmArgs& a0, const GemmArgs& a1, hipStream_t st, int small = 0);
 
 // Tile extents of the contraction kernels: G blocks are whole tiles.
 int tile_rows_m(int in_bf16);  // vocabulary rows per logit tile (BM)

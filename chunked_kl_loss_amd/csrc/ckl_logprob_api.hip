@@ -64,6 +64,10 @@ constexpr int64_t kForwardRows = 16384;
 // 6550 and 6890; 100000 words: 512 rows of 264, 2 more, 263 and 288, 1024 of 520, 4 more, 598 and 590, 2048 of 1544,
 // 9 more, 2090 and 2065, 1024 of 264, 4 more, 431 and 390).
 constexpr int64_t kTurnedTile = 230;
+// Rows up to which dH's transpose takes tiles of 256 x 64, in a launch of its own, instead of 256 x 320 beside dW's (us, dH
+// with dW and alone: 16 rows of 2880, 201088 words 1027 and 500, against 1089 and 623; 64 of 2048, 32000 words 167 and
+// 84, 193 and 110; 64 of 64, 100000 words 88 and 49, 95 and 60; 64 of 512, 1000 words 63 and 35, 58 and 48).
+constexpr int64_t kNarrowRows = 64;
 constexpr int64_t kGradSlots = 256;  // workgroups of head_grad at once: one to a compute unit
 
 // Vocabulary splits of a launch over row blocks: the count that finishes in the
@@ -92,6 +96,7 @@ struct HeadPlan {
   // backward: G blocks of Tc rows x Vc columns; dH as Sh sums over Vs columns of a block each
   int64_t BM, BN, Tp, Vp, Tc, Vc, nT, nV, Sh, Vs;
   int64_t dh_rows;  // rows (turned: columns) of a part of dH
+  bool narrow;  // turned, and of so few rows that narrow tiles hold them
   bool turned;  // the sums are of dH's transpose, which needs no transpose of W
 };
 ckl_status head_plan(int64_t T, int64_t d, int64_t V, int64_t chunk, int32_t in_dtype, int32_t dh_dtype,
@@ -139,7 +144,12 @@ ckl_status head_plan(int64_t T, int64_t d, int64_t V, int64_t chunk, int32_t in_
   if (q->turned) dh_tiles = turned_tiles;
   q->dh_rows = q->turned ? round_up(T, 8) : T;
   const int64_t share = (dh_tiles * q->Vc + dw_tiles * q->Tc) / (kGradSlots * 4);
-  q->Vs = std::min(round_up(std::max<int64_t>(share, 512), 64), q->Vc);
+  q->narrow = q->turned && T <= kNarrowRows;
+  if (q->narrow)  // (one round of the two workgroups that a compute unit holds of these tiles)
+    q->Vs = std::max<int64_t>(ceil_div(q->Vc, std::max<int64_t>(2 * kGradSlots / dh_tiles, 1)), 512);
+  else
+    q->Vs = std::max<int64_t>(share, 512);
+  q->Vs = std::min(round_up(q->Vs, 64), q->Vc);
   q->Sh = ceil_div(q->turned ? std::min(q->Vc, V) : q->Vc, q->Vs);
   // (the forward keeps 16 bytes a row and split: its blocks of rows need not be short)
   q->Cs = std::min(std::max(round_up(chunk, 256), kForwardRows), round_up(p.T, 256));
@@ -508,8 +518,15 @@ ckl_status ckl_head_logprobs_backward(const void* H, const void* W, int32_t in_d
           gdh.lim_kind = 1;
         }
       }
-      HIP_TRY(timed(CKL_KERNEL_GEMM_DHDW, st, [&] { return ckl::launch_gemm_pair(q.bf16, gdh, gdw, st, 1); }),
-              "gemm dH + dW");
+      if (q.narrow && dH) {
+        HIP_TRY(timed(CKL_KERNEL_GEMM_DHDW, st, [&] { return ckl::launch_gemm_pair(1, gdh, ckl::GemmArgs{}, st, 1); }),
+                "gemm dH");
+        gdh.M = 0;
+      }
+      if (!q.narrow || dW)
+        HIP_TRY(timed(CKL_KERNEL_GEMM_DHDW, st,
+                      [&] { return ckl::launch_gemm_pair(q.bf16, gdh, gdw, st, !q.bf16); }),
+                "gemm dH + dW");
     }
   }
   if (dH && dh_parts)
