@@ -295,8 +295,9 @@ def head_logprobs(H, W, tokens, mask=None, chunk: int = 2048):
     and W [V, d] (bf16 or fp32), whose logits are never stored: the cross entropy of hard labels beside the
     distillation loss, a policy's log probabilities, the score of a text.  Masked rows (mask uint8 / bool [...] 0)
     are not computed, whatever H holds there; they get 0 and no gradient.  A token outside [0, V) gets a log
-    probability of 0 and no gradient through it.  chunk bounds what the backward pass holds (about chunk x V logit
-    gradients), which multiplies the logits again."""
+    probability of 0 and no gradient through it.  The backward pass multiplies the logits again; chunk bounds the
+    logit gradients that it holds (about chunk x V, no fewer than 256 rows' or 256 words'), beside which it holds the
+    transposes of H and of a block of W, and sums in fp32: dH's and, where dW is bf16, dW's once rows are cut."""
     H, W, tokens, mask = H.contiguous(), W.contiguous(), tokens.contiguous(), _contiguous(mask)
     if not _needs_function(H.requires_grad or W.requires_grad):
         return ops.head_logprobs_forward(H, W, tokens, mask, chunk)[:2]

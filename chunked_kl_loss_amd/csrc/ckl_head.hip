@@ -322,36 +322,40 @@ __global__ __launch_bounds__(256) void head_buckets_kernel(const int* __restrict
   }
 }
 
-// dH from its parts and the tokens' entries, eight columns a thread; zeros where the
-// row is masked.  Bound by the parts' bytes (2048 x 2880 of three parts 46 us).
+// A block of rows of dH from its parts, what earlier blocks of words left (`sums`, may
+// be NULL and may be `out`) and the tokens' entries, eight columns a thread; zeros in
+// the block's rows of the call that are masked.  Bound by the parts' bytes.
 template <typename TOut>
-__global__ __launch_bounds__(256) void head_dh_kernel(const float* __restrict__ part, int64_t stride, int S, int T,
-                                                      int nv, const int* __restrict__ tok,
-                                                      const float* __restrict__ gtok, const bf16_t* __restrict__ W,
-                                                      HeadRows rows, TOut* __restrict__ dH) {
+__global__ __launch_bounds__(256) void head_dh_kernel(const float* __restrict__ part, int64_t stride, int S,
+                                                      const float* sums, int row0, int count, int nv,
+                                                      const int* __restrict__ tok, const float* __restrict__ gtok,
+                                                      const bf16_t* __restrict__ W, HeadRows rows, TOut* out) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int t = (int)(i / nv), c = (int)(i - (int64_t)t * nv);
-  if (t >= T) return;
-  const int r = rows.rank != nullptr ? rows.rank[t] : t;
+  const int t = (int)(i / nv), c = (int)(i - (int64_t)t * nv), r = row0 + t;
+  if (t >= count) return;
   float a[8] = {}, b[8];
-  if (r >= 0) {
-    const float* p = part + ((int64_t)r * nv + c) * 8;
-    load8(p, a);
+  if (rows.rank != nullptr && rows.rank[r] < 0) store8(out + ((int64_t)r * nv + c) * 8, a);
+  if (rows.n != nullptr && r >= *rows.n) return;
+  const float* p = part + i * 8;
+  int s = 0;
+  if (sums != nullptr)
+    load8(sums + ((int64_t)r * nv + c) * 8, a);
+  else
+    load8(p, a), s = 1;
 #pragma unroll 4
-    for (int s = 1; s < S; ++s) {
-      load8(p + s * stride, b);
+  for (; s < S; ++s) {
+    load8(p + s * stride, b);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) a[j] += b[j];
-    }
-    const int k = gtok != nullptr ? tok[r] : -1;
-    if (k >= 0) {
-      const float g = gtok[r];
-      load8(W + ((int64_t)k * nv + c) * 8, b);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) a[j] = fmaf(g, b[j], a[j]);
-    }
+    for (int j = 0; j < 8; ++j) a[j] += b[j];
   }
-  store8(dH + i * 8, a);
+  const int k = gtok != nullptr ? tok[r] : -1;
+  if (k >= 0) {
+    const float g = gtok[r];
+    load8(W + ((int64_t)k * nv + c) * 8, b);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a[j] = fmaf(g, b[j], a[j]);
+  }
+  store8(out + ((int64_t)(rows.perm != nullptr ? rows.perm[r] : r) * nv + c) * 8, a);
 }
 
 // The same from parts of dH's transpose ([d][ldt]): 32 rows by 8 columns a workgroup,
@@ -600,13 +604,16 @@ hipError_t launch_head_buckets(const int* tok, int T, int Tc, const int* n, int 
   return hipSuccess;
 }
 
-hipError_t launch_head_dh(const float* part, int64_t stride, int S, int T, int d, const int* tok, const float* gtok,
-                          const void* W, const HeadRows& rows, void* dH, int dh_bf16, hipStream_t st) {
-  const unsigned blocks = (unsigned)(((int64_t)T * (d / 8) + 255) / 256);
-  if (dh_bf16)
-    head_dh_kernel<<<blocks, 256, 0, st>>>(part, stride, S, T, d / 8, tok, gtok, (const bf16_t*)W, rows, (bf16_t*)dH);
+hipError_t launch_head_dh(const float* part, int64_t stride, int S, const float* sums, int row0, int count, int d,
+                          const int* tok, const float* gtok, const void* W, const HeadRows& rows, void* out,
+                          int out_bf16, hipStream_t st) {
+  const unsigned blocks = (unsigned)(((int64_t)count * (d / 8) + 255) / 256);
+  if (out_bf16)
+    head_dh_kernel<<<blocks, 256, 0, st>>>(part, stride, S, sums, row0, count, d / 8, tok, gtok, (const bf16_t*)W, rows,
+                                           (bf16_t*)out);
   else
-    head_dh_kernel<<<blocks, 256, 0, st>>>(part, stride, S, T, d / 8, tok, gtok, (const bf16_t*)W, rows, (float*)dH);
+    head_dh_kernel<<<blocks, 256, 0, st>>>(part, stride, S, sums, row0, count, d / 8, tok, gtok, (const bf16_t*)W, rows,
+                                           (float*)out);
   CKL_LAUNCH_CHECK();
   return hipSuccess;
 }

@@ -36,10 +36,13 @@ hipError_t launch_head_consts(const HeadRows& rows, int T, int Tp, int V, const 
 // words; rows without a token are in none.
 hipError_t launch_head_buckets(const int* tok, int T, int Tc, const int* n, int tiles, int* order, int* start,
                                hipStream_t st);
-// dH: a row's sum of its S parts, + gtok W[tok] where gtok is not NULL (W in bf16); zeros where it is masked.
-hipError_t launch_head_dh(const float* part, int64_t stride, int S, int T, int d, const int* tok, const float* gtok,
-                          const void* W, const HeadRows& rows, void* dH, int dh_bf16, hipStream_t st);
-// The same from parts of the transpose, [d][ldt] each (bf16: gtok is not NULL).
+// dH's rows row0 .. row0 + count: the sum of S parts, [count][d] each, and of `sums` [rows][d] where it is not NULL (S may
+// then be 0), + gtok W[tok] where gtok is not NULL (W in bf16).  Packed row i goes to row perm[i] (perm NULL: i),
+// and those of the call's rows row0 .. row0 + count that are masked (rank not NULL) get zeros.  out may be `sums`.
+hipError_t launch_head_dh(const float* part, int64_t stride, int S, const float* sums, int row0, int count, int d,
+                          const int* tok, const float* gtok, const void* W, const HeadRows& rows, void* out,
+                          int out_bf16, hipStream_t st);
+// All T rows from parts of the transpose, [d][ldt] each (bf16: gtok is not NULL).
 hipError_t launch_head_dh_t(const float* part, int64_t stride, int64_t ldt, int S, int T, int d, const int* tok,
                             const float* gtok, const void* W, const HeadRows& rows, void* dH, int dh_bf16,
                             hipStream_t st);

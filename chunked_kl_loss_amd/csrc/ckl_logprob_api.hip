@@ -95,7 +95,8 @@ struct HeadPlan {
   int64_t Cs, nS, splits, tps;
   // backward: G blocks of Tc rows x Vc columns; dH as Sh sums over Vs columns of a block each
   int64_t BM, BN, Tp, Vp, Tc, Vc, nT, nV, Sh, Vs;
-  int64_t dh_rows;  // rows (turned: columns) of a part of dH
+  int64_t dh_rows;  // rows (turned: columns) of a part of dH: a block's
+  bool carried;  // rows and words are both cut: dH's sums go from one block of words to the next in fp32 [T][d]
   bool narrow;  // turned, and of so few rows that narrow tiles hold them
   bool turned;  // the sums are of dH's transpose, which needs no transpose of W
 };
@@ -142,8 +143,12 @@ ckl_status head_plan(int64_t T, int64_t d, int64_t V, int64_t chunk, int32_t in_
   q->turned = q->bf16 && q->nT == 1 && (turned_tiles - dh_tiles) * kTurnedTile <= d &&
               std::min(p.T, gn) * (q->Vc + kLdPad) < kTileElements;
   if (q->turned) dh_tiles = turned_tiles;
-  q->dh_rows = q->turned ? round_up(T, 8) : T;
-  const int64_t share = (dh_tiles * q->Vc + dw_tiles * q->Tc) / (kGradSlots * 4);
+  q->dh_rows = q->turned ? round_up(T, 8) : std::min(q->Tc, T);
+  q->carried = q->nT > 1 && q->nV > 1;
+  // (twice that share where a block's sums pass through memory: half the parts, us, against a quarter's and all of a
+  // unit's share: 65536 rows of 1024, 32000 words, chunk 1024 20400, 22000 and 21700; 32768, 50264 words, 2048 12920,
+  // 13170 and 13280; 1024 14490, 15150 and 15870; 256 27960, 28700 and 23790)
+  const int64_t share = (dh_tiles * q->Vc + dw_tiles * q->Tc) / (kGradSlots * (q->carried ? 2 : 4));
   q->narrow = q->turned && T <= kNarrowRows;
   if (q->narrow)  // (one round of the two workgroups that a compute unit holds of these tiles)
     q->Vs = std::max<int64_t>(ceil_div(q->Vc, std::max<int64_t>(2 * kGradSlots / dh_tiles, 1)), 512);
@@ -194,9 +199,13 @@ HeadFwdWs head_fwd_layout(const HeadPlan& q, bool masked) {
   return w;
 }
 struct HeadBwdWs {
-  size_t consts, tok, gtok, order, start, Ht, Wt, G, Gt, dH, dW, total;
+  size_t consts, tok, gtok, order, start, Ht, Wt, G, Gt, parts, sums, dW, total;
   PackWs pk;
 };
+// Whether dH is finished from fp32 sums, or is them.
+bool dh_summed(const HeadPlan& q, bool masked, int32_t dh_dtype) {
+  return q.bf16 || dh_dtype == CKL_BF16 || masked || q.Sh > 1;
+}
 HeadBwdWs head_bwd_layout(const HeadPlan& q, bool masked, int32_t dh_dtype, int32_t dw_dtype) {
   HeadBwdWs w{};
   Layout l;
@@ -211,7 +220,12 @@ HeadBwdWs head_bwd_layout(const HeadPlan& q, bool masked, int32_t dh_dtype, int3
   w.Wt = q.turned ? 0 : l.take((size_t)q.d * (q.Vc + kLdPad) * q.esz);
   w.G = l.take((size_t)q.Tc * (q.Vc + kLdPad) * q.esz);
   w.Gt = q.bf16 ? 0 : l.take((size_t)q.Vc * (q.Tc + kLdPad) * q.esz);
-  w.dH = q.bf16 || dh_dtype == CKL_BF16 || masked || q.Sh > 1 ? l.take((size_t)q.Sh * q.dh_rows * q.d * 4) : 0;
+  // dH: one block's parts, which a plan's choice of Vs holds near a tile for each quarter of a compute unit's share,
+  // whatever T; and, where it is carried and dH itself cannot hold them, all rows' sums
+  if (dh_summed(q, masked, dh_dtype)) {
+    if (!q.carried || q.Sh > 1) w.parts = l.take((size_t)q.Sh * q.dh_rows * q.d * 4);
+    if (q.carried && (dh_dtype == CKL_BF16 || masked)) w.sums = l.take((size_t)q.T * q.d * 4);
+  }
   // fp32 sums of a bf16 dW (bf16 inputs: needed only between blocks of rows)
   w.dW = dw_dtype == CKL_BF16 && (!q.bf16 || q.nT > 1) ? l.take((size_t)q.V * q.d * 4) : 0;
   if (masked) w.pk = pack_layout(q, &l);
@@ -423,8 +437,10 @@ ckl_status ckl_head_logprobs_backward(const void* H, const void* W, int32_t in_d
   const void* Hs = H;
   if (mask) HIP_TRY(head_pack(q, b, w.pk, mask, &Hs, &r, st), "packing kept rows");
   // fp32 sums in the outputs themselves, or in the workspace where the output is bf16 or its rows are packed
-  const bool dh_parts = q.bf16 || dh_dtype == CKL_BF16 || mask || q.Sh > 1;
-  float* dHacc = dh_parts ? (float*)(b + w.dH) : (float*)dH;
+  const bool summed = dh_summed(q, mask != nullptr, dh_dtype);
+  float* parts = (float*)(b + w.parts);
+  float* sums = !summed || (dh_dtype == CKL_F32 && !mask) ? (float*)dH : (float*)(b + w.sums);
+  const bool in_sums = !summed || (q.carried && q.Sh == 1);  // the contraction adds to them itself
   const int64_t dh_stride = q.dh_rows * d;
   // bf16 inputs and dW: the last block of rows writes the rounded sums
   const bool dw16 = q.bf16 && dw_dtype == CKL_BF16;
@@ -470,9 +486,11 @@ ckl_status ckl_head_logprobs_backward(const void* H, const void* W, int32_t in_d
               "head_grad");
       // dH[tb0 ..) (+)= G W[vb0 ..) by parts of the vocabulary block (the longer sums: scheduled first),
       // dW[vb0 ..) (+)= G^T H[tb0 ..) (bf16: G read k-major)
-      ckl::GemmArgs gdh{G, vrows + kLdPad, Wt, ldWt, dH ? dHacc + tb0 * d : nullptr, d,
-                        dH ? (int)std::min(trows, T - tb0) : 0, (int)d, (int)std::min(q.Vs, vrows), vb > 0};
-      gdh.batches = (int)ceil_div(vrows, q.Vs);
+      const int rows_here = (int)std::min(trows, T - tb0);
+      ckl::GemmArgs gdh{G, vrows + kLdPad, Wt, ldWt, !dH ? nullptr : in_sums ? sums + tb0 * d : parts, d,
+                        dH ? rows_here : 0, (int)d, (int)std::min(q.Vs, vrows),
+                        vb > 0 && (in_sums || !q.carried)};
+      const int gdh_parts = gdh.batches = (int)ceil_div(vrows, q.Vs);
       gdh.kdim_last = (int)(vrows - (gdh.batches - 1) * q.Vs);
       gdh.xb = gdh.yb = q.Vs;
       gdh.ob = dh_stride;
@@ -487,7 +505,6 @@ ckl_status ckl_head_logprobs_backward(const void* H, const void* W, int32_t in_d
         gdh.xb = q.Vs * d;
         gdh.Y = G;
         gdh.ldy = vrows + kLdPad;
-        gdh.out = dHacc;
         gdh.ldo = q.dh_rows;
         gdh.M = dH ? (int)d : 0;
         gdh.N = (int)T;
@@ -527,18 +544,25 @@ ckl_status ckl_head_logprobs_backward(const void* H, const void* W, int32_t in_d
         HIP_TRY(timed(CKL_KERNEL_GEMM_DHDW, st,
                       [&] { return ckl::launch_gemm_pair(q.bf16, gdh, gdw, st, !q.bf16); }),
                 "gemm dH + dW");
+      // the block's rows of dH: finished behind the last block of words, until then kept where they are carried
+      const bool last = vb == q.nV - 1;
+      if (dH && summed && (last || (q.carried && !in_sums)))
+        HIP_TRY(timed(CKL_KERNEL_OTHER, st,
+                      [&] {
+                        if (q.turned)
+                          return ckl::launch_head_dh_t(parts, dh_stride, q.dh_rows, (int)q.Sh, (int)T, (int)d, tok,
+                                                       gtok, W, r, dH, dh_dtype == CKL_BF16, st);
+                        const int n = in_sums ? 0 : q.carried ? gdh_parts : (int)q.Sh;
+                        const float* before = in_sums || (q.carried && vb > 0) ? sums : nullptr;
+                        if (last)
+                          return ckl::launch_head_dh(parts, dh_stride, n, before, (int)tb0, rows_here, (int)d, tok,
+                                                     q.bf16 ? gtok : nullptr, W, r, dH, dh_dtype == CKL_BF16, st);
+                        return ckl::launch_head_dh(parts, dh_stride, n, before, (int)tb0, rows_here, (int)d, nullptr,
+                                                   nullptr, nullptr, {nullptr, 0, nullptr, nullptr, r.n}, sums, 0, st);
+                      }),
+                "sum dH");
     }
   }
-  if (dH && dh_parts)
-    HIP_TRY(timed(CKL_KERNEL_OTHER, st,
-                  [&] {
-                    if (q.turned)
-                      return ckl::launch_head_dh_t(dHacc, dh_stride, q.dh_rows, (int)q.Sh, (int)T, (int)d, tok, gtok, W,
-                                                   r, dH, dh_dtype == CKL_BF16, st);
-                    return ckl::launch_head_dh(dHacc, dh_stride, (int)q.Sh, (int)T, (int)d, tok,
-                                               q.bf16 ? gtok : nullptr, W, r, dH, dh_dtype == CKL_BF16, st);
-                  }),
-            "sum dH");
   if (dW && dw_dtype == CKL_BF16 && !dw16)
     HIP_TRY(timed(CKL_KERNEL_OTHER, st, [&] { return ckl::launch_cast_f32_bf16(dWacc, dW, V * d, st); }), "cast dW");
   return CKL_OK;

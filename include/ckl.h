@@ -435,9 +435,12 @@ ckl_status ckl_head_logprobs(const void* H, const void* W, int32_t in_dtype, int
 
 /* Its gradients dH = G W and dW = G^T H with G[t, v] as dlogits above (dlogprob or
  * dentropy NULL: zero).  The logits are multiplied again, and G is kept in blocks of
- * about chunk x V entries of in_dtype (bf16 rounds it once).  dH [T, d] dh_dtype,
- * dW [V, d] dw_dtype, overwritten; one of them may be NULL and is then not
- * computed.  lse and entropy: from ckl_head_logprobs on the same inputs.  T = 0:
+ * about chunk x V entries of in_dtype (bf16 rounds it once).  Besides them ws holds
+ * H^T, W^T of a block of words, a mask's packed rows, the parts of dH of one block
+ * of rows (up to 340 MB) and, in fp32, all of dH where rows and words are both cut
+ * and dH itself is bf16 or masked, and all of dW where it is bf16 and rows are cut
+ * (or the inputs are fp32).  dH [T, d] dh_dtype, dW [V, d] dw_dtype, overwritten;
+ * one of them may be NULL and is then not computed.  lse and entropy: from ckl_head_logprobs on the same inputs.  T = 0:
  * dW is zero.  (Rows that are not masked take part in the products, also those with
  * a = b = 0: a NaN in their states reaches dW.) */
 ckl_status ckl_head_logprobs_backward(const void* H, const void* W, int32_t in_dtype, int64_t T, int64_t d, int64_t V,
