@@ -94,9 +94,19 @@ __global__ void fill_i32_kernel(int* p, int n, int v) {
   if (i < n) p[i] = v;
 }
 
-__global__ void fill_f32_kernel(float* p, int64_t n, float v) {
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i < n) p[i] = v;
+// The kernels below that take one piece a thread walk on by the grid's size: a launch
+// of 2^32 threads or more is cut to its low 32 bits without an error, so more than
+// kFlatBlocks workgroups are not asked for.
+constexpr int64_t kFlatBlocks = (int64_t)1 << 23;
+static dim3 flat_blocks(int64_t n) {
+  const int64_t blocks = (n + 255) / 256;
+  return dim3((unsigned)(blocks < kFlatBlocks ? blocks : kFlatBlocks));
+}
+__device__ __forceinline__ int64_t flat_first() { return (int64_t)blockIdx.x * 256 + threadIdx.x; }
+__device__ __forceinline__ int64_t flat_step() { return (int64_t)gridDim.x * 256; }
+
+__global__ __launch_bounds__(256) void fill_f32_kernel(float* p, int64_t n, float v) {
+  for (int64_t i = flat_first(); i < n; i += flat_step()) p[i] = v;
 }
 
 // N = number of kept rows (mask NULL: all T).  One workgroup, fixed order.
@@ -168,13 +178,14 @@ __global__ __launch_bounds__(1024) void compact_rows_kernel(const uint8_t* __res
 __global__ __launch_bounds__(256) void gather_rows_kernel(const u32x4* __restrict__ src, int64_t chunks,
                                                           const int* __restrict__ perm, const int* __restrict__ N,
                                                           int rows, u32x4* __restrict__ dst) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= (int64_t)rows * chunks) return;
-  const int r = (int)(i / chunks);
-  const int64_t c = i - (int64_t)r * chunks;
-  u32x4 v = {0u, 0u, 0u, 0u};
-  if (r < *N) v = src[(int64_t)perm[r] * chunks + c];
-  dst[i] = v;
+  const int n = *N;
+  for (int64_t i = flat_first(); i < (int64_t)rows * chunks; i += flat_step()) {
+    const int r = (int)(i / chunks);
+    const int64_t c = i - (int64_t)r * chunks;
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (r < n) v = src[(int64_t)perm[r] * chunks + c];
+    dst[i] = v;
+  }
 }
 
 // dst[i] = src[perm[i]] for i < *N, 0 for *N <= i < rows.
@@ -198,28 +209,26 @@ __global__ __launch_bounds__(256) void scatter_f32_kernel(const float* __restric
 // for a masked row; four elements per thread.
 __global__ __launch_bounds__(256) void scatter_rows_kernel(const float* __restrict__ src, const int* __restrict__ rank,
                                                            int T, int d, void* __restrict__ dst, int dst_bf16) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int q = d / 4;
-  if (i >= (int64_t)T * q) return;
-  const int t = (int)(i / q);
-  const int c = (int)(i - (int64_t)t * q);
-  const int r = rank[t];
-  f32x4 a = {0.f, 0.f, 0.f, 0.f};
-  if (r >= 0) a = reinterpret_cast<const f32x4*>(src + (int64_t)r * d)[c];
-  if (dst_bf16)
-    *reinterpret_cast<u32x2*>(reinterpret_cast<bf16_t*>(dst) + (int64_t)t * d + 4 * c) =
-        u32x2{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3])};
-  else
-    reinterpret_cast<f32x4*>(reinterpret_cast<float*>(dst) + (int64_t)t * d)[c] = a;
+  for (int64_t i = flat_first(); i < (int64_t)T * q; i += flat_step()) {
+    const int t = (int)(i / q);
+    const int c = (int)(i - (int64_t)t * q);
+    const int r = rank[t];
+    f32x4 a = {0.f, 0.f, 0.f, 0.f};
+    if (r >= 0) a = reinterpret_cast<const f32x4*>(src + (int64_t)r * d)[c];
+    if (dst_bf16)
+      *reinterpret_cast<u32x2*>(reinterpret_cast<bf16_t*>(dst) + (int64_t)t * d + 4 * c) =
+          u32x2{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3])};
+    else
+      reinterpret_cast<f32x4*>(reinterpret_cast<float*>(dst) + (int64_t)t * d)[c] = a;
+  }
 }
 
 // Rows t of dst (`chunks` 16-byte pieces each) with rank[t] < 0 set to zero.
 __global__ __launch_bounds__(256) void zero_masked_rows_kernel(const int* __restrict__ rank, int T, int64_t chunks,
                                                                u32x4* __restrict__ dst) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= (int64_t)T * chunks) return;
-  const int t = (int)(i / chunks);
-  if (rank[t] < 0) dst[i] = u32x4{0u, 0u, 0u, 0u};
+  for (int64_t i = flat_first(); i < (int64_t)T * chunks; i += flat_step())
+    if (rank[(int)(i / chunks)] < 0) dst[i] = u32x4{0u, 0u, 0u, 0u};
 }
 
 // dst[i] = scale * src[i], rounded once to dst's type; four per thread.
@@ -227,14 +236,14 @@ __global__ __launch_bounds__(256) void zero_masked_rows_kernel(const int* __rest
 // same thread overwrites it)
 __global__ __launch_bounds__(256) void scale_cast_kernel(const float* src, void* dst, int64_t n4, int dst_bf16,
                                                          const float* __restrict__ scale) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= n4) return;
   const float g = scale ? *scale : 1.f;
-  const f32x4 a = reinterpret_cast<const f32x4*>(src)[i] * g;
-  if (dst_bf16)
-    reinterpret_cast<u32x2*>(dst)[i] = u32x2{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3])};
-  else
-    reinterpret_cast<f32x4*>(dst)[i] = a;
+  for (int64_t i = flat_first(); i < n4; i += flat_step()) {
+    const f32x4 a = reinterpret_cast<const f32x4*>(src)[i] * g;
+    if (dst_bf16)
+      reinterpret_cast<u32x2*>(dst)[i] = u32x2{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3])};
+    else
+      reinterpret_cast<f32x4*>(dst)[i] = a;
+  }
 }
 
 // One wavefront per row.  Softmax of the K cached logits (fp32), then a
@@ -770,9 +779,9 @@ __global__ __launch_bounds__(256, 4) void transpose_bf16_kernel(const bf16_t* __
   }
 }
 
-__global__ void cast_f32_bf16_kernel(const float* __restrict__ src, bf16_t* __restrict__ dst, int64_t n) {
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i < n) {
+__global__ __launch_bounds__(256) void cast_f32_bf16_kernel(const float* __restrict__ src, bf16_t* __restrict__ dst,
+                                                            int64_t n) {
+  for (int64_t i = flat_first(); i < n; i += flat_step()) {
     const uint32_t b = f32_to_bf16_bits(src[i]);
     reinterpret_cast<uint16_t*>(dst)[i] = (uint16_t)b;
   }
@@ -1258,21 +1267,21 @@ __global__ __launch_bounds__(256) void splitk_sum_kernel(const float* __restrict
                                                          int64_t n4, void* __restrict__ out, int out_bf16,
                                                          const int* __restrict__ rowmap, const int* __restrict__ nrows,
                                                          int row0, int d) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= n4) return;
-  int64_t o = i;
-  if (rowmap != nullptr) {
-    const int q = d / 4;
-    const int r = (int)(i / q);
-    if (r >= *nrows - row0) return;
-    o = (int64_t)rowmap[r] * q + (i - (int64_t)r * q);
+  for (int64_t i = flat_first(); i < n4; i += flat_step()) {
+    int64_t o = i;
+    if (rowmap != nullptr) {
+      const int q = d / 4;
+      const int r = (int)(i / q);
+      if (r >= *nrows - row0) return;  // (later rows too)
+      o = (int64_t)rowmap[r] * q + (i - (int64_t)r * q);
+    }
+    f32x4 a = reinterpret_cast<const f32x4*>(part)[i];
+    for (int s = 1; s < S; ++s) a += reinterpret_cast<const f32x4*>(part + s * pstride)[i];
+    if (out_bf16)
+      store4<bf16_t>(reinterpret_cast<bf16_t*>(out) + 4 * o, a[0], a[1], a[2], a[3]);
+    else
+      reinterpret_cast<f32x4*>(out)[o] = a;
   }
-  f32x4 a = reinterpret_cast<const f32x4*>(part)[i];
-  for (int s = 1; s < S; ++s) a += reinterpret_cast<const f32x4*>(part + s * pstride)[i];
-  if (out_bf16)
-    store4<bf16_t>(reinterpret_cast<bf16_t*>(out) + 4 * o, a[0], a[1], a[2], a[3]);
-  else
-    reinterpret_cast<f32x4*>(out)[o] = a;
 }
 
 // ------------------------------------------------------ plain contraction --
@@ -1618,7 +1627,7 @@ hipError_t launch_fill_i32(int* p, int n, int v, hipStream_t st) {
 
 hipError_t launch_fill_f32(float* p, int64_t n, float v, hipStream_t st) {
   if (n <= 0) return hipSuccess;
-  hipLaunchKernelGGL(fill_f32_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, p, n, v);
+  hipLaunchKernelGGL(fill_f32_kernel, flat_blocks(n), dim3(256), 0, st, p, n, v);
   CKL_LAUNCH_CHECK();
   return hipSuccess;
 }
@@ -1647,7 +1656,7 @@ hipError_t launch_gather_rows(const void* src, int rows, int64_t row_bytes, cons
   if (row_bytes % 16) return hipErrorInvalidValue;
   const int64_t chunks = row_bytes / 16, n = (int64_t)rows * chunks;
   if (n <= 0) return hipSuccess;
-  hipLaunchKernelGGL(gather_rows_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, (const u32x4*)src,
+  hipLaunchKernelGGL(gather_rows_kernel, flat_blocks(n), dim3(256), 0, st, (const u32x4*)src,
                      chunks, perm, N, rows, (u32x4*)dst);
   CKL_LAUNCH_CHECK();
   return hipSuccess;
@@ -1672,7 +1681,7 @@ hipError_t launch_scatter_rows(const float* src, const int* rank, int T, int d, 
   if (d % 4) return hipErrorInvalidValue;
   const int64_t n = (int64_t)T * (d / 4);
   if (n <= 0) return hipSuccess;
-  hipLaunchKernelGGL(scatter_rows_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, src, rank, T, d, dst,
+  hipLaunchKernelGGL(scatter_rows_kernel, flat_blocks(n), dim3(256), 0, st, src, rank, T, d, dst,
                      dst_bf16);
   CKL_LAUNCH_CHECK();
   return hipSuccess;
@@ -1682,7 +1691,7 @@ hipError_t launch_zero_masked_rows(const int* rank, int T, int64_t row_bytes, vo
   if (row_bytes % 16) return hipErrorInvalidValue;
   const int64_t chunks = row_bytes / 16, n = (int64_t)T * chunks;
   if (n <= 0) return hipSuccess;
-  hipLaunchKernelGGL(zero_masked_rows_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, rank, T, chunks,
+  hipLaunchKernelGGL(zero_masked_rows_kernel, flat_blocks(n), dim3(256), 0, st, rank, T, chunks,
                      (u32x4*)dst);
   CKL_LAUNCH_CHECK();
   return hipSuccess;
@@ -1693,7 +1702,7 @@ hipError_t launch_scale_cast(const float* src, void* dst, int64_t n, int dst_bf1
   if (n % 4) return hipErrorInvalidValue;
   const int64_t n4 = n / 4;
   if (n4 <= 0) return hipSuccess;
-  hipLaunchKernelGGL(scale_cast_kernel, dim3((unsigned)((n4 + 255) / 256)), dim3(256), 0, st, src, dst, n4, dst_bf16,
+  hipLaunchKernelGGL(scale_cast_kernel, flat_blocks(n4), dim3(256), 0, st, src, dst, n4, dst_bf16,
                      scale);
   CKL_LAUNCH_CHECK();
   return hipSuccess;
@@ -1795,7 +1804,7 @@ hipError_t launch_transpose_pad(int in_bf16, const void* src, int R, int C, int 
 
 hipError_t launch_cast_f32_bf16(const float* src, void* dst, int64_t n, hipStream_t st) {
   if (n <= 0) return hipSuccess;
-  hipLaunchKernelGGL(cast_f32_bf16_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, src, (bf16_t*)dst, n);
+  hipLaunchKernelGGL(cast_f32_bf16_kernel, flat_blocks(n), dim3(256), 0, st, src, (bf16_t*)dst, n);
   CKL_LAUNCH_CHECK();
   return hipSuccess;
 }
@@ -1936,7 +1945,7 @@ hipError_t launch_splitk_sum(const float* part, int64_t pstride, int S, int64_t 
   if (n % 4 || pstride % 4 || (rowmap && (d % 4 || n % d))) return hipErrorInvalidValue;
   const int64_t n4 = n / 4;
   if (n4 <= 0) return hipSuccess;
-  hipLaunchKernelGGL(splitk_sum_kernel, dim3((unsigned)((n4 + 255) / 256)), dim3(256), 0, st, part, pstride, S, n4,
+  hipLaunchKernelGGL(splitk_sum_kernel, flat_blocks(n4), dim3(256), 0, st, part, pstride, S, n4,
                      out, out_bf16, rowmap, nrows, row0, d);
   CKL_LAUNCH_CHECK();
   return hipSuccess;

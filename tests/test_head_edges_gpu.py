@@ -1,4 +1,5 @@
-"""Gradients of log probabilities from states and head on the GPU, cut into blocks of rows and of words."""
+"""Log probabilities from states and head on the GPU: gradients cut into blocks of rows and of words, and more elements
+than a launch has threads."""
 import math
 
 import pytest
@@ -6,7 +7,7 @@ import torch
 
 import chunked_kl_loss_amd as ckl
 from tests.test_head_gpu import check, inputs
-from tests.test_logprob_gpu import DT, gen, normal, same_bits
+from tests.test_logprob_gpu import DT, EPS, gen, normal, rows_reference, same_bits, within
 
 pytestmark = pytest.mark.gpu
 
@@ -51,3 +52,66 @@ def test_blocks_past_the_last_kept_row(share):
     mask = torch.arange(T) >= T * (1 - share)
     H[~mask] = math.nan
     check(H, W, tok, mask, chunk=100)
+
+
+# A launch of 2^32 threads or more loses those past its low 32 bits without an error.
+def wide():
+    V, d = 65600, 65536  # V d is past 2^32
+    torch.cuda.empty_cache()
+    return V, d
+
+
+def test_a_zero_gradient_of_more_elements_than_a_launch_has_threads():
+    V, d = wide()
+    W = torch.ones(V, d, dtype=torch.bfloat16, device="cuda")
+    H = torch.ones(0, d, dtype=torch.bfloat16, device="cuda")
+    none = torch.zeros(0, device="cuda")
+    _, dW = ckl.head_logprobs_backward(none, none, H, W, none.long(), none, none)
+    assert float(dW.amax()) == float(dW.amin()) == 0
+
+
+def test_a_rounded_gradient_of_more_elements_than_a_launch_has_threads():
+    V, d = wide()
+    g = torch.Generator("cuda")
+    g.manual_seed(1)
+    W = torch.empty(V, d, device="cuda").normal_(0.0, 2.0 ** -8, generator=g)
+    H = torch.zeros(2, d, device="cuda")
+    H[:, :4], H[:, -4:] = 1.0, 2.0
+    tok = torch.tensor([V - 1, 3], device="cuda")
+    lp, ent, lse = ckl.head_logprobs_forward(H, W, tok)
+    a = torch.tensor([8.0, -2.0], device="cuda")
+    _, dW = ckl.head_logprobs_backward(a, None, H, W, tok, lse, ent, need_dh=False, dw_dtype=torch.bfloat16)
+    for words in (slice(0, 40), slice(V // 2, V // 2 + 40), slice(V - 40, V)):
+        z = H.double() @ W[words].double().t()
+        G = -torch.exp(z - lse.double()[:, None]) * a.double()[:, None]
+        for i in range(2):
+            at = int(tok[i]) - words.start
+            if 0 <= at < 40:
+                G[i, at] += a[i].double()
+        want = G.t() @ H.double()
+        # z: 8 products of at most 2^-5 (|z| < 1) that sum up in fp32, lse its tolerance: relative 2^-18 of G; one rounding
+        assert ((dW[words].double() - want).abs() <= (2.0 ** -18 + 2.0 ** -8) * (G.abs().t() @ H.double()) + 1e-37).all()
+    assert not dW[:, 4:-4].any()
+
+
+def test_packed_states_of_more_pieces_than_a_launch_has_threads():
+    T, d, V = 524_400, 65536, 8  # T d / 8 is past 2^32
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 160 << 30:
+        pytest.skip("needs 160 GiB")
+    H = torch.zeros(T, d, dtype=torch.bfloat16, device="cuda")
+    last = inputs(200, d, V, torch.bfloat16, 1)
+    H[-200:] = last[0].cuda()
+    W = last[1].cuda()
+    tok = torch.zeros(T, dtype=torch.int64, device="cuda")
+    tok[-200:] = last[2].cuda()
+    mask = torch.ones(T, dtype=torch.bool, device="cuda")
+    mask[3] = False
+    lp, ent, lse = ckl.head_logprobs_forward(H, W, tok, mask)
+    want = ckl.head_logprobs_forward(last[0].cuda(), W, last[2].cuda())
+    assert float(lp[3]) == 0 and (lp[:-200][torch.arange(T - 200, device="cuda") != 3] == lp[0]).all()
+    z = last[0].double() @ last[1].double().t()
+    r = rows_reference(z, last[2])
+    for got, w, key, tol in zip((lp, ent, lse), want, ("logprob", "entropy", "lse"), ("tol_lp", "tol_ent", "tol_lse")):
+        t = r[tol] + 4 * EPS * r["lse"].abs()
+        assert within(got[-200:], r[key], t) and within(w, r[key], t)
