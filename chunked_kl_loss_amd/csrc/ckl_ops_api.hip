@@ -98,6 +98,8 @@ ckl_status ckl_embedding_forward(const void* W, int32_t dtype, int64_t V, int64_
                                  void* stream) {
   ckl_status s = check_embedding(T, d, V, v_offset);
   if (s != CKL_OK) return s;
+  // (32 elements a thread, and a launch keeps the low 32 bits of its number of threads)
+  if (ceil_div(T * (d / 8), 1024) >= ((int64_t)1 << 24)) return fail(CKL_ERR_UNSUPPORTED, "T*d: at most 2^37 - 8192");
   if (!dtype_ok(dtype)) return fail(CKL_ERR_INVALID_ARG, "dtype must be CKL_F32 (0) or CKL_BF16 (1)");
   if (token_bytes != 4 && token_bytes != 8) return fail(CKL_ERR_INVALID_ARG, "token_bytes must be 4 or 8");
   if (T == 0) return CKL_OK;

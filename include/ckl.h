@@ -316,7 +316,8 @@ ckl_status ckl_teacher_topk(const void* logits, int32_t dtype, int64_t T, int64_
  * row: its output row is zero.  So negative ids can pad a batch, and with W one
  * vocabulary shard the outputs of all shards add up to the whole table's.
  *   W: [V, d] dtype.  tokens: [T] int32 or int64 (token_bytes 4 or 8), aligned
- *   to their size.  out: [T, d] dtype.  0 <= v_offset, v_offset + V < 2^63. */
+ *   to their size.  out: [T, d] dtype, T*d <= 2^37 - 8192.  0 <= v_offset, v_offset
+ *   + V < 2^63. */
 ckl_status ckl_embedding_forward(const void* W, int32_t dtype, int64_t V, int64_t d, int64_t v_offset,
                                  const void* tokens, int32_t token_bytes, int64_t T, float scale, void* out,
                                  void* stream);
