@@ -489,14 +489,17 @@ struct RowAcc {
   template <typename R>
   __device__ __forceinline__ float add(const R& raw, float vm) {
     if (vm > m + 4.f) {
+      const float to = -vm * kLog2e;
       if (m > -INFINITY) {
         settle();
-        const float d = fmaxf((m - vm) * kLog2e, kExpZero), f = fast_exp2(d);
+        // (what is there takes the new neg's rounding, which will be divided out of it with the rest)
+        const float d = fmaxf((m - vm) * kLog2e, kExpZero) + (fabsf(to) < kTopkNegLimit ? fmaf(vm, kLog2e, to) : 0.f);
+        const float f = fast_exp2(d);
         e = f * (e + d * s);
         s *= f;
       }
       m = vm;
-      neg = -vm * kLog2e;
+      neg = to;
     }
     float sum = 0.f, es = 0.f;
     if (fabsf(neg) < kTopkNegLimit) {
