@@ -224,7 +224,9 @@ __global__ __launch_bounds__(256) void head_finish_kernel(const float4* __restri
   float z = 0.f;
   if (token_column(rows, p, V) >= 0) {
     z = ztok[i];
-    if (z != -INFINITY || l != l) z -= l;  // (-infinity has that log probability in a row of nothing else, too)
+    // from differences, as z - l would carry the rounding of l (-infinity has that log probability in a row of nothing
+    // else, too)
+    if (z != -INFINITY || l != l) z = (fmaf(z, kLog2e, -m) - l2) * kLn2;
   }
   logprob[t] = z;
 }
@@ -232,7 +234,8 @@ __global__ __launch_bounds__(256) void head_finish_kernel(const float4* __restri
 // --------------------------------------------------------------- backward --
 // With q = 2^x, x = z log2 e - lse log2 e, the gradient of a row's logits is
 //   q (c0 + c1 x) + 1[v = token] a,   c0 = -(a + b entropy),   c1 = -b ln 2
-// for its incoming gradients a (log probability) and b (entropy).  Row i:
+// for its incoming gradients a (log probability) and b (entropy); q carries the
+// rounding of lse, 2^-24 |lse|.  Row i:
 // consts[i] = (c0, lse log2 e, c1, a), its token.  Rows past the last one and rows
 // with no gradient get an lse that makes q zero.
 __global__ __launch_bounds__(256) void head_consts_kernel(HeadRows rows, int T, int Tp, int V,

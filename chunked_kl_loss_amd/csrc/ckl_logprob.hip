@@ -84,7 +84,7 @@ __global__ __launch_bounds__(THREADS) void row_stats_kernel(const T* __restrict_
   if (tid == 0) {
     const float l = s == s ? m + logf(s) : s;
     lse[row] = l;
-    row_outputs(out, logits, row, V, l, s, e);
+    row_outputs(out, logits, row, V, l, m, s, e);
   }
 }
 
@@ -294,19 +294,19 @@ __global__ __launch_bounds__(THREADS, 8) void row_top_kernel(const T* __restrict
   const float l = (top != top || top == INFINITY || top == -INFINITY) ? top : m + logf(s);
   if (lane < K) {
     float v = key_value((uint32_t)(best >> 32));
-    if (v != -INFINITY) v -= l;  // a logit of -inf has log probability -inf in every row
+    if (v != -INFINITY) v = row_logprob(v, m, logf(s));  // a logit of -inf has log probability -inf in every row
     idx[lane] = (int)~(uint32_t)best;
     val[lane] = v;
   }
   if (lane == 0) {
     lse[row] = l;
-    row_outputs(out, logits, row, V, l, s, e);
+    row_outputs(out, logits, row, V, l, m, s, e);
   }
 }
 
 // ---------------------------------------------------------------- gradient --
-// dz = a (1[v = token] - q) - b q (log q + entropy), q = exp(z - lse), for a row's
-// incoming gradients a (log probability) and b (entropy).  A row whose mask is 0,
+// dz = a (1[v = token] - q) - b q (log q + entropy), q = exp(z - lse) (the lse as it
+// was rounded: q carries 2^-24 |lse|), for a row's incoming gradients a (log probability) and b (entropy).  A row whose mask is 0,
 // whose a and b are 0 or that has no column left (lse = -inf) gets zeros and is
 // not read.  One pass; a thread takes VECS vectors of a row, one for short rows.  Bound
 // by memory where there are many rows: 2048 x 201088 bf16 282 us, 5.8 TB/s read and

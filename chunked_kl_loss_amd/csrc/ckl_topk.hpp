@@ -356,13 +356,18 @@ __device__ __forceinline__ void topk_reduce_state(float& m, float& s, S& sh) {
   for (int w = 1; w < 4; ++w) exp_merge(m, s, sh.wave_m[w], sh.wave_s[w]);
 }
 
+// Log probability of a logit from its row's reference m and ln s.  (z - (m + ln s)
+// would carry the rounding of a sum of m's size: 5e-4 for logits near 10^4.)
+__device__ __forceinline__ float row_logprob(float z, float m, float ln_s) { return (z - m) - ln_s; }
+
 // The K largest of a row's n words in order, and its state, as the row's
 // results.  The words are put into bins over the range of their keys, and in its
 // bin a word's place is the number of larger words there.  Where a bin that
 // matters holds more than 256 words (keys that are mostly equal, or a far
 // outlier) a bitonic sort does it.  Returns the log sum exp.  (2048 rows of 100000 bf16, K = 2048: 352 us
-// a call with this, 580 with the bitonic sort.)
-template <int CAP, typename S>
+// a call with this, 580 with the bitonic sort.)  ENT: log probabilities are taken
+// from differences (see row_logprob).
+template <int CAP, bool ENT, typename S>
 __device__ __forceinline__ float topk_finish(uint64_t* buf, int n, int K, float m, float s, int logprob, int* idx,
                                             float* val, float* lse, S& sh) {
   constexpr int W = CAP <= 4096 ? 10 : 24, limit = W * kTopkThreads;  // words that go into the bins
@@ -387,9 +392,10 @@ __device__ __forceinline__ float topk_finish(uint64_t* buf, int n, int K, float 
   // a NaN anywhere in the row comes first, then an infinity
   const float l = (top != top || top == INFINITY || top == -INFINITY) ? top : m + logf(s);
   if (tid == 0) *lse = l;
+  const float ln_s = ENT ? logf(s) : 0.f;
   auto put = [&](int place, uint64_t word) {
     float v = key_value((uint32_t)(word >> 32));
-    if (logprob && v != -INFINITY) v -= l;  // a logit of -inf has log-probability -inf in every row
+    if (logprob && v != -INFINITY) v = ENT ? row_logprob(v, m, ln_s) : v - l;  // a logit of -inf has log-probability -inf in every row
     idx[place] = (int)~(uint32_t)word;
     val[place] = v;
   };
@@ -551,7 +557,7 @@ __device__ __forceinline__ void ent_reduce(float& m, float& s, float& e, float* 
 }
 // What a row of logits leaves besides its alternatives, by one thread: the log
 // probability of its token (0 where the token is no column) and its entropy.  l:
-// the row's log sum exp.
+// the row's log sum exp, with (m, s, e) its sums.
 struct RowOut {
   const void* tokens;
   int tokens64;
@@ -563,15 +569,16 @@ __device__ __forceinline__ int64_t token_at(const void* tokens, int tokens64, in
   return tokens64 ? reinterpret_cast<const int64_t*>(tokens)[i] : (int64_t)reinterpret_cast<const int32_t*>(tokens)[i];
 }
 template <typename T>
-__device__ __forceinline__ void row_outputs(const RowOut& o, const T* logits, int64_t row, int V, float l, float s,
-                                            float e) {
+__device__ __forceinline__ void row_outputs(const RowOut& o, const T* logits, int64_t row, int V, float l, float m,
+                                            float s, float e) {
   const int64_t tok = token_at(o.tokens, o.tokens64, row);
+  const float ln_s = logf(s);
   float lp = 0.f;
   if (tok >= 0 && tok < V) {
     const float z = (float)logits[row * (int64_t)V + tok];
-    lp = z == -INFINITY && l == l ? z : z - l;  // (a logit of -inf has log probability -inf in every row)
+    lp = z == -INFINITY && l == l ? z : row_logprob(z, m, ln_s);  // (a logit of -inf has log probability -inf in every row)
   }
-  float ent = logf(s) - kLn2 * (e / s);
+  float ent = ln_s - kLn2 * (e / s);
   ent = ent < 0.f ? 0.f : ent;
   if (l == -INFINITY) ent = 0.f;             // no column is left
   if (!(l < INFINITY)) ent = __uint_as_float(0x7fc00000u);
@@ -871,8 +878,8 @@ __global__ __launch_bounds__(kTopkThreads, CAP <= 4096 ? 4 : 2) void topk_rows_k
     topk_reduce_state(m, s, sh);
   }
   if (segments == 1) {
-    const float l = topk_finish<CAP>(buf, n, K, m, s, logprob, idx + row * K, val + row * K, lse + row, sh);
-    if (ENT && tid == 0) row_outputs(out, logits, row, V, l, s, e);
+    const float l = topk_finish<CAP, ENT>(buf, n, K, m, s, logprob, idx + row * K, val + row * K, lse + row, sh);
+    if (ENT && tid == 0) row_outputs(out, logits, row, V, l, m, s, e);
   } else {
     const int slots = topk_slots(K);
     if (n > slots) {
@@ -942,8 +949,8 @@ __global__ __launch_bounds__(kTopkThreads, CAP <= 4096 ? 4 : 2) void topk_merge_
     ent_reduce(m, s, e, sh.wave_m, sh.wave_s, sh.wave_e);
   else
     topk_reduce_state(m, s, sh);
-  const float l = topk_finish<CAP>(buf, n, K, m, s, logprob, idx + row * K, val + row * K, lse + row, sh);
-  if (ENT && tid == 0) row_outputs(out, logits, row, V, l, s, e);
+  const float l = topk_finish<CAP, ENT>(buf, n, K, m, s, logprob, idx + row * K, val + row * K, lse + row, sh);
+  if (ENT && tid == 0) row_outputs(out, logits, row, V, l, m, s, e);
 }
 
 }  // namespace

@@ -390,12 +390,13 @@ ckl_status ckl_norm_backward(const void* dy, int32_t dtype, int64_t T, int64_t d
  * alternatives, from logits in one pass.
  *   logits: [T, V] dtype.  tokens: [T] int32 or int64 (token_bytes 4 or 8),
  *   aligned to their size.  mask: [T] uint8 (nonzero = keep) or NULL.
- *   logprob: [T] float32, logit of the token - lse; 0 where the token is outside
- *   [0, V) (padding).
+ *   logprob: [T] float32, logit of the token - lse, from differences with the row's
+ *   largest logits (it rounds at its own size, not at lse's); 0 where the token is
+ *   outside [0, V) (padding).
  *   entropy: [T] float32, lse - sum_v q_v z_v = -sum_v q_v log q_v, q = softmax(z).
  *   lse:     [T] float32, as ckl_teacher_topk's.
  *   top_idx [T, top] int32, top_logprob [T, top] float32: as ckl_teacher_topk with
- *   K = top and CKL_TEACHER_LOGPROBS.  top may be 0 (both may then be NULL).
+ *   K = top and CKL_TEACHER_LOGPROBS, but from differences.  top may be 0 (both may then be NULL).
  * A logit of -inf (a forbidden token) has log probability -inf and adds nothing to
  * the entropy; a row of nothing but -inf has lse -inf and entropy 0.  A row that
  * holds a NaN gives NaN; one that holds +inf has lse +inf and entropy NaN.  Rows
@@ -411,7 +412,8 @@ ckl_status ckl_token_logprobs(const void* logits, int32_t dtype, int64_t T, int6
 /* Gradient of the first two: with a = dlogprob[t] (0 for a token outside) and b =
  * dentropy[t] (NULL: zero),
  *   dlogits[t, v] = a (1[v = token] - q_v) - b q_v (log q_v + entropy[t]),
- * in fp32, rounded once to dtype.  lse and entropy: from ckl_token_logprobs.  Rows
+ * in fp32, rounded once to dtype, with q = exp(z - lse) of the lse in float32 (whose
+ * rounding, 2^-24 |lse|, q carries).  lse and entropy: from ckl_token_logprobs.  Rows
  * with mask 0, with a = b = 0 or with lse -inf get zeros and are not read. */
 ckl_status ckl_token_logprobs_backward(const void* logits, int32_t dtype, int64_t T, int64_t V, const void* tokens,
                                        int32_t token_bytes, const uint8_t* mask, const float* lse,

@@ -1,15 +1,37 @@
-"""Log probabilities from states and head on the GPU: gradients cut into blocks of rows and of words, and more elements
-than a launch has threads."""
+"""Log probabilities from states and head on the GPU: logits far from zero, gradients cut into blocks of rows and of
+words, and more elements than a launch has threads."""
 import math
 
 import pytest
 import torch
 
 import chunked_kl_loss_amd as ckl
-from tests.test_head_gpu import check, inputs
-from tests.test_logprob_gpu import DT, EPS, gen, normal, rows_reference, same_bits, within
+from tests.test_head_gpu import check, grid, inputs
+from tests.test_logprob_gpu import DT, EPS, gen, normal, rows_reference, same_bits, some_tokens, within
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("base", [128, -128])
+@pytest.mark.parametrize("T,V", [(3, 3001), (40, 1500), (100, 5003), (300, 2049)])
+def test_log_probabilities_of_logits_far_from_zero(T, V, base, dtype):
+    # one column adds 2^14 or its negative to all logits: multiples of 2^-6 below 2^15, exact in fp32
+    d = 16
+    H, W = grid((T, d), DT[dtype], 1, 0.25), grid((V, d), DT[dtype], 2, 2.0 ** -4)
+    H[:, 0], W[:, 0] = 128, base
+    tok = some_tokens(T, V, 3)
+    z = H.double() @ W.double().t()
+    r = rows_reference(z, tok)
+    s = r["lse"] - z.max(1).values
+    lp, ent, lse = ckl.head_logprobs_forward(H.cuda(), W.cuda(), tok.cuda())
+    # (z - m) - ln s: the sum's tolerance (tests/test_logprob_gpu.py), and a rounding of each difference, of the
+    # logarithm, of log2 e and of ln 2
+    tol = (V / 256 + 40) * EPS + 2.0 ** -22 + 6 * EPS * (r["logprob"].abs() + 2 * s + 1)
+    assert within(lp, r["logprob"], tol)
+    assert within(ent, r["entropy"], r["tol_ent"])
+    # ln 2 (m + log2 s): a rounding of m, of the sum, of the product and of either constant
+    assert within(lse, r["lse"], tol + 6 * EPS * r["lse"].abs())
 
 
 @pytest.mark.parametrize("masked", [False, True])
