@@ -41,6 +41,7 @@ from ._binding import (  # noqa: F401
     workspace_size,
 )
 from .autograd import (  # noqa: F401
+    AddNormQuant,
     AddRMSNorm,
     ChunkedKLLoss,
     ChunkedKLLoss8Bit,
@@ -50,6 +51,7 @@ from .autograd import (  # noqa: F401
     HeadLogprobs,
     RMSNorm8Bit,
     TokenLogprobs,
+    add_norm_quant,
     add_rms_norm,
     chunked_kl_loss,
     dropout,
@@ -63,7 +65,6 @@ from .ops import (  # noqa: F401
     act_encode,
     add_norm_backward,
     add_norm_forward,
-    add_norm_quant,
     dropout_forward,
     embedding_backward,
     embedding_forward,

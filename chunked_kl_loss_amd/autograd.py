@@ -241,6 +241,19 @@ class AddRMSNorm(torch.autograd.Function):
         return dx, dresidual, dweight, None, None, None, None
 
 
+class AddNormQuant(torch.autograd.Function):
+    """The norm in 8 bits for inputs that require a gradient: there is none, and whoever asks for it is told."""
+    @staticmethod
+    def forward(ctx, x, residual, weight, eps, form):
+        codes, scales, h = ops.add_norm_quant(x, residual, weight, eps, form)
+        ctx.mark_non_differentiable(*((codes, scales) if form == "int8" else (codes,)))
+        return codes, scales, h
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise NotImplementedError("add_norm_quant has no gradient; use add_rms_norm where one is needed")
+
+
 def _contiguous(t):
     return None if t is None else t.contiguous()
 
@@ -325,6 +338,15 @@ def add_rms_norm(x, residual, weight, eps: float = 1e-6, p: float = 0.0, seed=0,
     if not _needs_function(x.requires_grad or residual.requires_grad or weight.requires_grad):
         return ops.add_norm_forward(x, residual, weight, eps, p, seed, offset, save=False)[:2]
     return AddRMSNorm.apply(x, residual, weight, eps, p, seed, offset)
+
+
+def add_norm_quant(x, residual, weight, eps: float = 1e-6, form: str = "int8"):
+    if not _needs_function(x.requires_grad or residual.requires_grad or weight.requires_grad):
+        return ops.add_norm_quant(x, residual, weight, eps, form)
+    return AddNormQuant.apply(x, residual, weight, eps, form)
+
+
+add_norm_quant.__doc__ = ops.add_norm_quant.__doc__
 
 
 def chunked_kl_loss(H, W, idx, tlogit, mask=None, chunk: int = 2048, fused: bool = False, teacher_form: int = 0,

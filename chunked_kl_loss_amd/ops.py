@@ -527,7 +527,8 @@ _FORMS = {"int8": CKL_QUANT_INT8, "e4m3": CKL_QUANT_E4M3}
 
 
 def add_norm_quant(x, residual, weight, eps: float = 1e-6, form: str = "int8"):
-    """The norm behind a residual's addition with its output in 8 bits (no gradient): (codes, scales, h).  form "int8":
+    """The norm behind a residual's addition with its output in 8 bits: (codes, scales, h), without a gradient (one that
+    is asked for is an error, tangents are refused).  form "int8":
     codes int8 [..., d] and scales uint8 [..., ceil(d / 32)] as act_encode writes them, for act_decode; "e4m3":
     codes float8_e4m3fn [..., d] that stand for code * scale, scales float32 [...]."""
     if form not in _FORMS:

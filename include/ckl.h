@@ -494,8 +494,8 @@ ckl_status ckl_add_norm_backward(const void* dy, int32_t x_dtype, const void* dh
                                  int32_t weight_dtype, double p, uint64_t seed, uint64_t offset, const int64_t* state,
                                  void* dx, void* dresidual, void* dweight, void* ws, size_t ws_bytes, void* stream);
 
-/* The norm's output in 8 bits, for a product that reads them: h as above without
- * dropout, and y, which is not rounded before its int8 code and once, to fp32,
+/* The norm's output in 8 bits, for a product that reads them (no gradient): h as
+ * above without dropout, and y, which is not rounded before its int8 code and once, to fp32,
  * before its e4m3 code, as
  *   CKL_QUANT_INT8: codes int8 [T, d] and scales uint8 [T, ceil(d / CKL_ACT_BLOCK)], the
  *     form of ckl_act_encode, which ckl_act_decode restores;
