@@ -19,7 +19,8 @@ norm that saves its input in 8 bits.
 
 TokenLogprobs and HeadLogprobs: log probabilities of given tokens and entropies,
 from logits and from states and head.  Dropout and AddRMSNorm: dropout with a mask
-that is formed again in the backward pass, and the norm with the residual's addition."""
+that is formed again in the backward pass, and the norm with the residual's addition;
+AddNormQuant: its output in 8 bits, whose gradient is an error."""
 from __future__ import annotations
 
 import torch
@@ -295,7 +296,8 @@ def token_logprobs(logits, tokens, top: int = 0, mask=None):
     differentiable with respect to the logits; and the `top` most likely columns in descending order (equal ones by
     index) with their log probabilities, [..., top], without gradient (top 0: empty).  Rows whose mask (uint8 / bool
     [...]) is 0 are not read; they get 0 and no gradient.  A logit of -inf is a forbidden token: log probability
-    -inf, no entropy, no gradient; a row of nothing else has entropy 0."""
+    -inf, no entropy, no gradient (but that of its own log probability where it is the given token, as for any
+    other); a row of nothing else has entropy 0 and no gradient."""
     logits, tokens, mask = logits.contiguous(), tokens.contiguous(), _contiguous(mask)
     if not _needs_function(logits.requires_grad):
         logprob, entropy, _, top_idx, top_logprob = ops.token_logprobs_forward(logits, tokens, top, mask)
@@ -308,9 +310,10 @@ def head_logprobs(H, W, tokens, mask=None, chunk: int = 2048):
     and W [V, d] (bf16 or fp32), whose logits are never stored: the cross entropy of hard labels beside the
     distillation loss, a policy's log probabilities, the score of a text.  Masked rows (mask uint8 / bool [...] 0)
     are not computed, whatever H holds there; they get 0 and no gradient.  A token outside [0, V) gets a log
-    probability of 0 and no gradient through it.  The backward pass multiplies the logits again; chunk bounds the
-    logit gradients that it holds (about chunk x V, no fewer than 256 rows' or 256 words'), beside which it holds the
-    transposes of H and of a block of W, and sums in fp32: dH's and, where dW is bf16, dW's once rows are cut."""
+    probability of 0 and no gradient through it, so W is the whole head, not a shard of it.  The backward pass
+    multiplies the logits again; chunk bounds the logit gradients that it holds (about chunk x V, at least 256 x 256),
+    beside which it holds the transposes of H and of a block of W, and sums in fp32: dH's and, where dW is bf16, dW's
+    once rows are cut."""
     H, W, tokens, mask = H.contiguous(), W.contiguous(), tokens.contiguous(), _contiguous(mask)
     if not _needs_function(H.requires_grad or W.requires_grad):
         return ops.head_logprobs_forward(H, W, tokens, mask, chunk)[:2]
@@ -319,8 +322,9 @@ def head_logprobs(H, W, tokens, mask=None, chunk: int = 2048):
 
 def dropout(x, p: float, seed=0, offset: int = 0):
     """x / (1 - p) where kept, 0 elsewhere, differentiable; the mask is a function of (seed, offset, element), formed
-    again in the backward pass and never stored.  Different layers or steps take different seeds or offsets.  p is
-    taken to the nearest multiple of 2^-16.  seed: an integer, or an int64 tensor (seed, offset) on the GPU, read
+    again in the backward pass and never stored.  Different layers and steps have to be given different seeds or
+    offsets: two calls with the same ones, the defaults among them, draw the same mask.  p is taken to the nearest
+    multiple of 2^-16.  seed: an integer, or an int64 tensor (seed, offset) on the GPU, read
     when the kernels run (a captured graph draws anew when the tensor changes between replays); its offset is added
     to this one."""
     x = x.contiguous()

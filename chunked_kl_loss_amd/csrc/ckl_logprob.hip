@@ -47,8 +47,9 @@ __device__ __forceinline__ float vec_max(const Raw8<T>& r) {
 // ---------------------------------------------------- without alternatives --
 // One workgroup a row, in one pass: sums of 2^a and a 2^a behind a running
 // reference (RowAcc), four vectors a thread under way while four are looked at.
-// Bound by memory where there are many rows (2048 x 201088 bf16: 151 us, 5.5 TB/s;
-// 8192 x 12000 fp32 68 us, 5.8).
+// Bound by memory where there are many rows (2048 x 201088 bf16: 154 us, 5.4 TB/s;
+// fp32 274, 6.0) and by one workgroup's way along the row where there are few: 1 to 64
+// rows of 32000 words 7 to 8 us, of 201088 19 to 23 (the host's part of a call 14).
 constexpr int kRowVecs = 4;
 
 template <typename T, int THREADS>
@@ -98,7 +99,8 @@ __global__ __launch_bounds__(THREADS) void row_stats_kernel(const T* __restrict_
 // place by one comparison of all lanes and a shift, or, where many come at once,
 // 64 are sorted and merged.  No barrier until the waves' lists are joined.  Bound by
 // the latency of the words' steps: without alternatives 8192 x 12000 bf16 takes 47 us,
-// with 5 of them 81, with 20 99.
+// with 5 of them 72 to 81, with 20 99.  Eight waves a SIMD leave 64 registers, of which 2
+// or 3 (and 21 to 27 scalar ones) are spilled around the words' steps.
 __device__ __forceinline__ uint64_t lane_word(uint64_t w, int lane) {
   return ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(w >> 32), lane) << 32) |
          (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)w, lane);

@@ -66,7 +66,8 @@ constexpr int64_t kForwardRows = 16384;
 constexpr int64_t kTurnedTile = 230;
 // Rows up to which dH's transpose takes tiles of 256 x 64, in a launch of its own, instead of 256 x 320 beside dW's (us, dH
 // with dW and alone: 16 rows of 2880, 201088 words 1027 and 500, against 1089 and 623; 64 of 2048, 32000 words 167 and
-// 84, 193 and 110; 64 of 64, 100000 words 88 and 49, 95 and 60; 64 of 512, 1000 words 63 and 35, 58 and 48).
+// 84, 193 and 110; 64 of 64, 100000 words 88 and 49, 95 and 60; 64 of 512, 1000 words 63 and 35, 58 and 48, where the
+// second launch costs more than the wide tiles: the one of these that a rule by rows alone loses).
 constexpr int64_t kNarrowRows = 64;
 constexpr int64_t kGradSlots = 256;  // workgroups of head_grad at once: one to a compute unit
 

@@ -33,7 +33,9 @@ struct TokenRows {
 // 0.15 us, a row of the latter about 8 us.  (us, registers / buffer: 60000 x 1500 bf16,
 // top 5 / 20 / 64: 97 / 164 / 333 against 690 to 760; 8192 x 12000 bf16, top 5 / 20 / 64:
 // 81 / 99 / 154 against 122 / 122 / 127, fp32 99 / 134 / 196 against 134 to 137; 2000 x 32000
-// bf16, top 5 / 20: 40 / 57 against 46 / 50; 2048 x 201088, top 10 / 20: 179 / 199 against 170.)
+// bf16, top 5 / 20: 40 / 57 against 44 / 50; 2048 x 201088, top 10 / 20: 179 / 199 against 170.  The border
+// in words is where 20 alternatives cost about the same; 5 of them are cheaper in registers up to 32000 words: 2000 x
+// 16384 28, x 16385 by the buffer 41.)
 inline bool logprob_in_registers(int64_t V, int64_t top) { return V <= 2048 ? top <= 64 : V <= 16384 && top <= 24; }
 hipError_t launch_token_logprobs(const void* logits, int bf16, int64_t rows, int64_t V, int top, const TokenRows& t,
                                  float* lse, int* idx, float* val, uint64_t* cand, float2* state, float* state_e,

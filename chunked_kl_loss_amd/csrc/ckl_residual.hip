@@ -102,7 +102,7 @@ __global__ __launch_bounds__(256) void dropout_kernel(const T* __restrict__ x, i
 // (WAVE: the first kind.)  A row is held in registers between the sum of squares and
 // the output, so everything is read once.  Bound by memory: 32768 x 2880 bf16 125 us, 6.0
 // TB/s; 262144 x 64 6.3, 65536 x 520 5.9, 32768 x 2048 7.0, 8192 x 8192 7.0, 2048 x 65536
-// 5.3.  The output in 8 bits: 65536 x 2880 as int8 224 us, 5.9 TB/s.
+// 5.3.  The output in 8 bits: 65536 x 2880 as int8 230 us, 5.8 TB/s, as e4m3 221, 6.0.
 struct RowShape {
   int threads, per;  // threads a row takes, vectors of eight a thread
 };
@@ -328,7 +328,8 @@ __global__ __launch_bounds__(1024) void add_norm_kernel(const TX* __restrict__ x
 // columns' share of dw in registers; norm_dweight adds the workgroups.  Rows of
 // more than two vectors a thread are read a second time (from the caches) instead
 // of being held.  Bound by memory: 32768 x 2880 bf16 with dh 174 us, 5.4 TB/s; 262144 x
-// 64 4.4, 65536 x 520 3.9, 8192 x 8192 5.1, 2048 x 65536 3.2 (read again past the L2).
+// 64 4.4, 65536 x 520 3.9, 8192 x 8192 5.1, 2048 x 65536 3.2 (read again past the L2; past
+// 32768 columns the eight vectors of dw leave 48 to 57 registers spilled).
 template <typename TX, typename TR, int NV, bool WAVE, bool DROP>
 __global__ __launch_bounds__(1024) void add_norm_backward_kernel(
     const TX* __restrict__ dy, const TR* __restrict__ dh, const TR* __restrict__ h, const float* __restrict__ rstd,

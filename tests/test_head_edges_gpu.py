@@ -77,14 +77,18 @@ def test_blocks_past_the_last_kept_row(share):
 
 
 # A launch of 2^32 threads or more loses those past its low 32 bits without an error.
-def wide():
-    V, d = 65600, 65536  # V d is past 2^32
+V_WIDE, D_WIDE = 65600, 65536  # their product is past 2^32
+
+
+@pytest.fixture
+def room():
     torch.cuda.empty_cache()
-    return V, d
+    yield
+    torch.cuda.empty_cache()
 
 
-def test_a_zero_gradient_of_more_elements_than_a_launch_has_threads():
-    V, d = wide()
+def test_a_zero_gradient_of_more_elements_than_a_launch_has_threads(room):
+    V, d = V_WIDE, D_WIDE
     W = torch.ones(V, d, dtype=torch.bfloat16, device="cuda")
     H = torch.ones(0, d, dtype=torch.bfloat16, device="cuda")
     none = torch.zeros(0, device="cuda")
@@ -92,8 +96,8 @@ def test_a_zero_gradient_of_more_elements_than_a_launch_has_threads():
     assert float(dW.amax()) == float(dW.amin()) == 0
 
 
-def test_a_rounded_gradient_of_more_elements_than_a_launch_has_threads():
-    V, d = wide()
+def test_a_rounded_gradient_of_more_elements_than_a_launch_has_threads(room):
+    V, d = V_WIDE, D_WIDE
     g = torch.Generator("cuda")
     g.manual_seed(1)
     W = torch.empty(V, d, device="cuda").normal_(0.0, 2.0 ** -8, generator=g)
@@ -116,9 +120,8 @@ def test_a_rounded_gradient_of_more_elements_than_a_launch_has_threads():
     assert not dW[:, 4:-4].any()
 
 
-def test_packed_states_of_more_pieces_than_a_launch_has_threads():
+def test_packed_states_of_more_pieces_than_a_launch_has_threads(room):
     T, d, V = 524_400, 65536, 8  # T d / 8 is past 2^32
-    torch.cuda.empty_cache()
     if torch.cuda.mem_get_info()[0] < 160 << 30:
         pytest.skip("needs 160 GiB")
     H = torch.zeros(T, d, dtype=torch.bfloat16, device="cuda")

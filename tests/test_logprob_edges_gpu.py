@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import chunked_kl_loss_amd as ckl
-from tests.test_logprob_gpu import EPS, normal, rows_reference, some_tokens, within
+from tests.test_logprob_gpu import DT, EPS, HALF, normal, rows_reference, some_tokens, within
 
 pytestmark = pytest.mark.gpu
 
@@ -60,3 +60,25 @@ def test_a_row_of_one_far_value_is_uniform(fill, top):
     assert within(lp, want, 4 * EPS * want.abs())
     if top:
         assert within(val[:, :3], want[:, None].expand(2, 3), (4 * EPS * want.abs())[:, None].expand(2, 3))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gradients_of_forbidden_tokens(dtype):
+    # none, but where one is the given token: that of its own log probability, which the formula leaves it
+    T, V = 4, 1003
+    z = normal((T, V), DT[dtype], 1, 2.0)
+    z[:, ::3] = -torch.inf
+    tok = torch.tensor([0, 1, 3, 999])
+    Z = z.cuda().requires_grad_(True)
+    lp, ent, _, _ = ckl.token_logprobs(Z, tok.cuda())
+    (dz,) = torch.autograd.grad((lp, ent), (Z,), (torch.full_like(lp, 1.5), torch.full_like(ent, 0.5)))
+    dz, gone = dz.double().cpu(), torch.isinf(z)
+    own = torch.zeros_like(gone)
+    own[torch.arange(T), tok] = True
+    assert (dz[gone & own] == 1.5).all() and int((gone & own).sum()) == 3 and not dz[gone & ~own].any()
+    q = torch.softmax(z.double(), 1)
+    logq = torch.where(gone, 0.0, torch.log_softmax(z.double(), 1))
+    want = 1.5 * own - q * (1.5 + 0.5 * (logq - (q * logq).sum(1, keepdim=True)))
+    # sums and arguments: as in the log probabilities' tolerance; one rounding
+    tau = ((V / 256 + 40) * EPS + 2.0 ** -20) * 10
+    assert ((dz - want).abs() <= tau * (q + EPS) + HALF[DT[dtype]] * want.abs()).all()
