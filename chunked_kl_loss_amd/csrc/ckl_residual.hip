@@ -102,7 +102,8 @@ __global__ __launch_bounds__(256) void dropout_kernel(const T* __restrict__ x, i
 // (WAVE: the first kind.)  A row is held in registers between the sum of squares and
 // the output, so everything is read once.  Bound by memory: 32768 x 2880 bf16 125 us, 6.0
 // TB/s; 262144 x 64 6.3, 65536 x 520 5.9, 32768 x 2048 7.0, 8192 x 8192 7.0, 2048 x 65536
-// 5.3.  The output in 8 bits: 65536 x 2880 as int8 230 us, 5.8 TB/s, as e4m3 221, 6.0.
+// 5.3.  The output in 8 bits: 65536 x 2880 as int8 222 to 240 us, 5.5 to 5.9
+// TB/s, as e4m3 221, 6.0.
 struct RowShape {
   int threads, per;  // threads a row takes, vectors of eight a thread
 };
